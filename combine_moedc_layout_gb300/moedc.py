@@ -29,15 +29,24 @@ ERR_UNIMPLEMENTED = 6
 
 BF16 = 0
 FP8_E4M3 = 1
+F16 = 2                     # F16 and F32: router, sorted rows, 4-bit products
+F32 = 3
 SCALES_COL_MAJOR = 0x100    # OR into FP8_E4M3: scales stored [E, H/128, cap]
 SCALES_PER_TOKEN = 0x200    # OR into FP8_E4M3: one scale per row, scales [E, cap]
 TOKEN_SCALE_MAX_H = 32768   # MOEDC_TOKEN_SCALE_MAX_H
+
+GATE_SOFTMAX = 0
+GATE_SIGMOID = 1
+GATE_NORMALIZE = 0x10       # OR into either: weights renormalised over the chosen experts
+SWIGLU = 1                  # MOEDC_SWIGLU
 
 EXPORTED = ("moedc_api_version", "moedc_strerror", "moedc_layout_workspace_bytes",
             "moedc_layout", "moedc_dispatch", "moedc_combine", "moedc_layout_dispatch",
             "moedc_layout_static_scratch", "moedc_dequant_e4m3", "moedc_rank_layout",
             "moedc_rank_dispatch", "moedc_rank_combine", "moedc_combine_e4m3",
-            "moedc_layout_dispatch_workspace_bytes", "moedc_test_set_wait_extra")
+            "moedc_gate", "moedc_gate_grad", "moedc_sort_rows", "moedc_sort_workspace_bytes",
+           "moedc_sort", "moedc_unsort", "moedc_unsort_grad", "moedc_matvec_int4",
+           "moedc_layout_dispatch_workspace_bytes", "moedc_test_set_wait_extra")
 
 STATIC_SCRATCH_BYTES = 1 << 20   # MOEDC_STATIC_SCRATCH_BYTES
 
@@ -65,6 +74,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
                            "(python -c 'import __graft_entry__ as g; g.build()')")
     lib = ctypes.CDLL(p)
     P, I, Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    L, F = ctypes.c_int64, ctypes.c_float
     lib.moedc_api_version.argtypes = []
     lib.moedc_api_version.restype = I
     lib.moedc_strerror.argtypes = [I]
@@ -94,6 +104,23 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.moedc_rank_combine.restype = I
     lib.moedc_combine_e4m3.argtypes = [P, P, I, I, I, I, P, P, P, I, I, P, P, P]
     lib.moedc_combine_e4m3.restype = I
+    lib.moedc_gate.argtypes = [P, L, I, I, I, I, P, I, F, P, P, P]
+    lib.moedc_gate.restype = I
+    lib.moedc_gate_grad.argtypes = [P, L, I, I, I, I, P, I, F, P, P, P, P]
+    lib.moedc_gate_grad.restype = I
+    lib.moedc_sort_rows.argtypes = [I, I, I, I]
+    lib.moedc_sort_rows.restype = Z
+    lib.moedc_sort_workspace_bytes.argtypes = [I, I, I]
+    lib.moedc_sort_workspace_bytes.restype = Z
+    lib.moedc_sort.argtypes = [P, L, I, I, I, P, I, I, I, I, P, P, P, P, P, P, Z, P, P]
+    lib.moedc_sort.restype = I
+    lib.moedc_unsort.argtypes = [P, I, I, I, P, P, I, I, P, P]
+    lib.moedc_unsort.restype = I
+    lib.moedc_unsort_grad.argtypes = [P, L, P, I, I, I, I, P, P, P, I, P, P, P]
+    lib.moedc_unsort_grad.restype = I
+    lib.moedc_matvec_int4.argtypes = [P, L, I, I, I, P, P, I, P, I, I, I, I, P, P, P, I, I, P, P,
+                                      P]
+    lib.moedc_matvec_int4.restype = I
     lib.moedc_test_set_wait_extra.argtypes = [ctypes.c_uint]
     lib.moedc_test_set_wait_extra.restype = None
     if path is None:
@@ -203,6 +230,54 @@ def moedc_rank_dispatch(x, T, H, rank_slot, num_tokens_per_rank, R, cap_rank, ou
 def moedc_rank_combine(rank_out, R, cap_rank, H, rank_slot, T, y, stream=None) -> int:
     return load().moedc_rank_combine(_p(rank_out), R, cap_rank, H, _p(rank_slot), T, _p(y),
                                      _stream(stream))
+
+
+def moedc_gate(logits, ld_logits, dtype, T, E, K, bias, flags, scale, topk_idx, topk_weights,
+               stream=None) -> int:
+    return load().moedc_gate(_p(logits), ld_logits, dtype, T, E, K, _p(bias), flags, scale,
+                             _p(topk_idx), _p(topk_weights), _stream(stream))
+
+
+def moedc_gate_grad(logits, ld_logits, dtype, T, E, K, bias, flags, scale, topk_idx, dweights,
+                    dlogits, stream=None) -> int:
+    return load().moedc_gate_grad(_p(logits), ld_logits, dtype, T, E, K, _p(bias), flags, scale,
+                                  _p(topk_idx), _p(dweights), _p(dlogits), _stream(stream))
+
+
+def moedc_sort_rows(T: int, K: int, E: int, align: int) -> int:
+    return int(load().moedc_sort_rows(T, K, E, align))
+
+
+def moedc_sort_workspace_bytes(T: int, K: int, E: int) -> int:
+    return int(load().moedc_sort_workspace_bytes(T, K, E))
+
+
+def moedc_sort(x, ldx, dtype, T, H, topk_idx, K, E, align, rows, sorted, row, src, offsets,
+               counts, workspace, workspace_bytes, dev_status, stream=None) -> int:
+    return load().moedc_sort(_p(x), ldx, dtype, T, H, _p(topk_idx), K, E, align, rows,
+                             _p(sorted), _p(row), _p(src), _p(offsets), _p(counts),
+                             _p(workspace), workspace_bytes, _p(dev_status), _stream(stream))
+
+
+def moedc_unsort(sorted, dtype, rows, H, row, topk_weights, T, K, y, stream=None) -> int:
+    return load().moedc_unsort(_p(sorted), dtype, rows, H, _p(row), _p(topk_weights), T, K, _p(y),
+                               _stream(stream))
+
+
+def moedc_unsort_grad(dy, lddy, sorted, dtype, T, H, K, row, src, topk_weights, rows, dsorted,
+                      dweights, stream=None) -> int:
+    return load().moedc_unsort_grad(_p(dy), lddy, _p(sorted), dtype, T, H, K, _p(row), _p(src),
+                                    _p(topk_weights), rows, _p(dsorted), _p(dweights),
+                                    _stream(stream))
+
+
+def moedc_matvec_int4(x, ldx, dtype, x_rows, Kd, wq, scales, scale_dtype, zeros, group, E, N,
+                      flags, offsets, counts, src, top_k, rows, out, dev_status,
+                      stream=None) -> int:
+    return load().moedc_matvec_int4(_p(x), ldx, dtype, x_rows, Kd, _p(wq), _p(scales),
+                                    scale_dtype, _p(zeros), group, E, N, flags, _p(offsets),
+                                    _p(counts), _p(src), top_k, rows, _p(out), _p(dev_status),
+                                    _stream(stream))
 
 
 # ---------------------------------------------------------------- conveniences
@@ -376,3 +451,243 @@ def rank_combine(rank_out: torch.Tensor, rank_slot: torch.Tensor) -> torch.Tenso
     y = torch.empty((T, H), dtype=torch.bfloat16, device=rank_out.device)
     _check(moedc_rank_combine(rank_out, R, cap_rank, H, rank_slot, T, y), "moedc_rank_combine")
     return y
+
+
+# ------------------------------------------ router, sorted rows, 4-bit products
+
+_LM_DTYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+
+
+def _lm_dtype(t: torch.Tensor, name: str) -> int:
+    d = _LM_DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name} must be bfloat16, float16 or float32, not {t.dtype}")
+    return d
+
+
+def _need_rows(t: torch.Tensor, name: str) -> int:
+    """A 2-D CUDA tensor whose rows are contiguous; returns its row stride."""
+    if not t.is_cuda or t.dim() != 2 or (t.shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a CUDA matrix with contiguous rows")
+    ld = t.stride(0)
+    if ld < t.shape[1]:
+        if t.shape[0] > 1:
+            raise ValueError(f"{name} must not repeat or overlap its rows")
+        ld = t.shape[1]
+    return ld
+
+
+def _need_shape(t: torch.Tensor, shape, name: str) -> None:
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, not {tuple(t.shape)}")
+
+
+def gate(logits: torch.Tensor, K: int, bias: torch.Tensor | None = None,
+         flags: int = GATE_SOFTMAX | GATE_NORMALIZE, scale: float = 1.0, out=None):
+    """Top-k router: (topk_idx int32 [T, K], topk_weights fp32 [T, K]) from
+    logits [T, E].  `out` takes an earlier call's result to write into."""
+    ld = _need_rows(logits, "logits")
+    dtype = _lm_dtype(logits, "logits")
+    T, E = logits.shape
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        _need_shape(bias, (E,), "bias")
+    if out is None:
+        out = (_dev_i32((T, K), logits.device),
+               torch.empty((T, K), dtype=torch.float32, device=logits.device))
+    idx, w = out
+    _need(idx, torch.int32, "out[0]")
+    _need(w, torch.float32, "out[1]")
+    _need_shape(idx, (T, K), "out[0]")
+    _need_shape(w, (T, K), "out[1]")
+    _check(moedc_gate(logits, ld, dtype, T, E, K, bias, flags, scale, idx, w), "moedc_gate")
+    return out
+
+
+def gate_grad(logits: torch.Tensor, topk_idx: torch.Tensor, dweights: torch.Tensor,
+              bias: torch.Tensor | None = None, flags: int = GATE_SOFTMAX | GATE_NORMALIZE,
+              scale: float = 1.0, out: torch.Tensor | None = None) -> torch.Tensor:
+    """dlogits [T, E] of gate() with the same arguments, from dweights [T, K]."""
+    ld = _need_rows(logits, "logits")
+    dtype = _lm_dtype(logits, "logits")
+    _need(topk_idx, torch.int32, "topk_idx")
+    _need(dweights, torch.float32, "dweights")
+    T, E = logits.shape
+    K = topk_idx.shape[1]
+    _need_shape(topk_idx, (T, K), "topk_idx")
+    _need_shape(dweights, (T, K), "dweights")
+    if bias is not None:
+        _need(bias, torch.float32, "bias")
+        _need_shape(bias, (E,), "bias")
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    _need(out, logits.dtype, "out")
+    _need_shape(out, (T, E), "out")
+    _check(moedc_gate_grad(logits, ld, dtype, T, E, K, bias, flags, scale, topk_idx, dweights,
+                           out), "moedc_gate_grad")
+    return out
+
+
+@dataclass
+class Sorted:
+    rows: torch.Tensor | None     # [R, H], x's dtype (None: maps only)
+    row: torch.Tensor             # int32 [T, K]
+    src: torch.Tensor             # int32 [R]
+    offsets: torch.Tensor         # int32 [E + 1]
+    counts: torch.Tensor          # int32 [E]
+    status: torch.Tensor          # int32 [1] (device)
+    workspace: torch.Tensor
+
+
+def sort(x: torch.Tensor | None, topk_idx: torch.Tensor, E: int, align: int = 1,
+         status: torch.Tensor | None = None, out: Sorted | None = None,
+         rows: int | None = None) -> Sorted:
+    """Token rows sorted by expert (x None: the maps alone).  `rows` sets the
+    packed buffer's rows (default: as many as any routing of this shape
+    needs); `out` takes an earlier call's result of the same shapes to write
+    into, its workspace included."""
+    _need(topk_idx, torch.int32, "topk_idx")
+    T, K = topk_idx.shape
+    H, ld, dtype = 1, 1, BF16
+    if x is not None:
+        ld = _need_rows(x, "x")
+        dtype = _lm_dtype(x, "x")
+        H = x.shape[1]
+        _need_shape(x, (T, H), "x")
+    dev = topk_idx.device
+    if out is None:
+        if rows is None:
+            rows = moedc_sort_rows(T, K, E, align)
+            if rows == 0 and T > 0:
+                raise MoedcError(ERR_ARG, "moedc_sort_rows")
+        ws = moedc_sort_workspace_bytes(T, K, E)
+        out = Sorted(torch.empty((rows, H), dtype=x.dtype, device=dev) if x is not None else None,
+                     _dev_i32((T, K), dev), _dev_i32(rows, dev), _dev_i32(E + 1, dev),
+                     _dev_i32(E, dev),
+                     status if status is not None
+                     else torch.zeros(1, dtype=torch.int32, device=dev),
+                     torch.empty(ws, dtype=torch.uint8, device=dev))
+    else:
+        if status is not None:
+            out.status = status
+        n = out.src.shape[0]
+        if rows is not None and rows != n:
+            raise ValueError(f"out holds {n} rows, not {rows}")
+        rows = n
+        if (x is None) != (out.rows is None):
+            raise ValueError("out must hold rows exactly when x is given")
+        if x is not None:
+            _need(out.rows, x.dtype, "out.rows")
+            _need_shape(out.rows, (rows, H), "out.rows")
+        _need_shape(out.row, (T, K), "out.row")
+        _need_shape(out.counts, (E,), "out.counts")
+    _check(moedc_sort(x, ld, dtype, T, H, topk_idx, K, E, align, rows, out.rows, out.row, out.src,
+                      out.offsets, out.counts, out.workspace, out.workspace.numel(), out.status),
+           "moedc_sort")
+    return out
+
+
+def unsort(rows: torch.Tensor, row: torch.Tensor, topk_weights: torch.Tensor | None = None,
+           out: torch.Tensor | None = None) -> torch.Tensor:
+    """y [T, H]: each token's packed rows summed with their weights (None: 1)."""
+    dtype = _lm_dtype(rows, "rows")
+    _need(rows, rows.dtype, "rows")
+    _need(row, torch.int32, "row")
+    R, H = rows.shape
+    T, K = row.shape
+    if topk_weights is not None:
+        _need(topk_weights, torch.float32, "topk_weights")
+        _need_shape(topk_weights, (T, K), "topk_weights")
+    if out is None:
+        out = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
+    _need(out, rows.dtype, "out")
+    _need_shape(out, (T, H), "out")
+    _check(moedc_unsort(rows, dtype, R, H, row, topk_weights, T, K, out), "moedc_unsort")
+    return out
+
+
+def sort_grad(drows: torch.Tensor, row: torch.Tensor,
+              out: torch.Tensor | None = None) -> torch.Tensor:
+    """dx [T, H] of sort(): the gradients of a token's packed rows, summed."""
+    return unsort(drows, row, None, out)
+
+
+def unsort_grad(dy: torch.Tensor, rows: torch.Tensor | None, row: torch.Tensor,
+                src: torch.Tensor, topk_weights: torch.Tensor, out=None):
+    """(drows [R, H], dweights fp32 [T, K]) of unsort(); rows None: drows alone,
+    dweights None."""
+    ld = _need_rows(dy, "dy")
+    dtype = _lm_dtype(dy, "dy")
+    _need(row, torch.int32, "row")
+    _need(src, torch.int32, "src")
+    _need(topk_weights, torch.float32, "topk_weights")
+    T, H = dy.shape
+    K = row.shape[1]
+    R = src.shape[0]
+    _need_shape(row, (T, K), "row")
+    _need_shape(topk_weights, (T, K), "topk_weights")
+    if rows is not None:
+        _need(rows, dy.dtype, "rows")
+        _need_shape(rows, (R, H), "rows")
+    if out is None:
+        out = (torch.empty((R, H), dtype=dy.dtype, device=dy.device),
+               torch.empty((T, K), dtype=torch.float32, device=dy.device)
+               if rows is not None else None)
+    drows, dw = out
+    _need(drows, dy.dtype, "out[0]")
+    _need_shape(drows, (R, H), "out[0]")
+    if dw is not None:
+        _need(dw, torch.float32, "out[1]")
+        _need_shape(dw, (T, K), "out[1]")
+    _check(moedc_unsort_grad(dy, ld, rows, dtype, T, H, K, row, src, topk_weights, R, drows, dw),
+           "moedc_unsort_grad")
+    return out
+
+
+def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
+                zeros: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
+                counts: torch.Tensor | None = None, src: torch.Tensor | None = None,
+                top_k: int = 1, swiglu: bool = False, status: torch.Tensor | None = None,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """out [R, N]: packed expert rows times 4-bit weights wq uint8 [E, N, Kd/2]
+    ([N, Kd/2]: one linear layer) with scales [E, N, Kd/group]; swiglu: 2N
+    weight rows, silu(gate) * up.  offsets and counts from sort(); src and
+    top_k read x in token order."""
+    ld = _need_rows(x, "x")
+    dtype = _lm_dtype(x, "x")
+    if wq.dim() == 2:
+        wq, scales = wq[None], scales[None]
+        zeros = None if zeros is None else zeros[None]
+    _need(wq, torch.uint8, "wq")
+    _need(scales, scales.dtype, "scales")
+    E, wn, half = wq.shape
+    Kd = 2 * half
+    if x.shape[1] != Kd:
+        raise ValueError(f"x must have {Kd} channels, not {x.shape[1]}")
+    if scales.dim() != 3 or tuple(scales.shape[:2]) != (E, wn) or Kd % max(1, scales.shape[2]):
+        raise ValueError(f"scales must have shape [{E}, {wn}, {Kd} / group]")
+    if zeros is not None:
+        _need(zeros, torch.uint8, "zeros")
+        _need_shape(zeros, scales.shape, "zeros")
+    if swiglu and wn % 2:
+        raise ValueError("swiglu needs an even number of weight rows")
+    N = wn // 2 if swiglu else wn
+    if offsets is not None:
+        _need(offsets, torch.int32, "offsets")
+        _need_shape(offsets, (E + 1,), "offsets")
+    if counts is not None:
+        _need(counts, torch.int32, "counts")
+        _need_shape(counts, (E,), "counts")
+    if src is not None:
+        _need(src, torch.int32, "src")
+    R = src.shape[0] if src is not None else x.shape[0]
+    if out is None:
+        out = torch.empty((R, N), dtype=x.dtype, device=x.device)
+    _need(out, x.dtype, "out")
+    _need_shape(out, (R, N), "out")
+    if status is None:
+        status = torch.zeros(1, dtype=torch.int32, device=x.device)
+    _check(moedc_matvec_int4(x, ld, dtype, x.shape[0], Kd, wq, scales, _lm_dtype(scales, "scales"),
+                             zeros, Kd // max(1, scales.shape[2]), E, N, SWIGLU if swiglu else 0,
+                             offsets, counts, src, top_k, R, out, status), "moedc_matvec_int4")
+    return out

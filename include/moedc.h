@@ -96,7 +96,9 @@ typedef enum {
     MOEDC_ERR_UNIMPLEMENTED = 6
 } moedc_status;
 
-typedef enum { MOEDC_BF16 = 0, MOEDC_FP8_E4M3 = 1 } moedc_dtype;
+/* MOEDC_F16 and MOEDC_F32 are element types of the router, the sorted rows and
+ * the 4-bit products (below); dispatch and combine take the other two. */
+typedef enum { MOEDC_BF16 = 0, MOEDC_FP8_E4M3 = 1, MOEDC_F16 = 2, MOEDC_F32 = 3 } moedc_dtype;
 
 /* OR-ed into the out_dtype of moedc_dispatch / moedc_layout_dispatch with
  * MOEDC_FP8_E4M3: the fp32 scales are stored [E][G][cap] (per expert, one
@@ -344,6 +346,129 @@ MOEDC_EXPORT int moedc_layout_dispatch(const void* x, const int32_t* topk_idx,
                           void* recv, float* scales, int32_t* src_idx,
                           void* workspace, size_t workspace_bytes,
                           int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * Top-k router: topk_idx and topk_weights from the router's logits.
+ *   key[t][e] = logits[t][e] + bias[e]   (one binary32 sum; bias NULL = 0)
+ * An expert can be chosen when its logit and its key are neither NaN nor -inf
+ * (mask experts with -inf; a mask of the type's lowest finite value leaves the
+ * expert to be chosen last, with weight 0 next to ordinary logits).  +inf
+ * counts as the largest finite binary32.  topk_idx[t] holds the K experts
+ * with the largest keys, descending, ties to the lowest expert; where fewer
+ * can be chosen the rest is -1 with weight 0 (the masked entry of every other
+ * call).  The weights come from the logits WITHOUT the bias, which moves the
+ * choice alone (load balancing), with C the chosen experts of the token:
+ *   MOEDC_GATE_SOFTMAX                         scale * softmax(l)_e over the experts that can be chosen
+ *   MOEDC_GATE_SOFTMAX | MOEDC_GATE_NORMALIZE  scale * softmax(l)_e over C
+ *   MOEDC_GATE_SIGMOID                         scale * sigmoid(l_e)
+ *   MOEDC_GATE_SIGMOID | MOEDC_GATE_NORMALIZE  scale * sigmoid(l_e) / sum over C
+ *                                              (0 when that sum underflows to 0)
+ * in binary32.  logits: dtype MOEDC_BF16, MOEDC_F16 or MOEDC_F32, [T, E] with
+ * ld_logits >= E elements from row to row.  bias fp32 [E].
+ *
+ * moedc_gate_grad: dlogits [T, E] (contiguous, of the logits' dtype, rounded
+ * once) from dweights fp32 [T, K], with topk_idx as moedc_gate gave it and the
+ * same other arguments.  The choice is constant; the bias has no gradient.
+ * dweights of masked entries are not read into any result; experts that
+ * cannot be chosen get 0.
+ * Arguments: T >= 0, 1 <= K <= MOEDC_MAX_K, K <= E <= MOEDC_MAX_E.  No data errors.
+ */
+#define MOEDC_GATE_SOFTMAX 0
+#define MOEDC_GATE_SIGMOID 1
+#define MOEDC_GATE_NORMALIZE 0x10
+MOEDC_EXPORT int moedc_gate(const void* logits, int64_t ld_logits, int dtype, int T, int E, int K,
+                 const float* bias, int flags, float scale, int32_t* topk_idx,
+                 float* topk_weights, cudaStream_t stream);
+MOEDC_EXPORT int moedc_gate_grad(const void* logits, int64_t ld_logits, int dtype, int T, int E,
+                 int K, const float* bias, int flags, float scale, const int32_t* topk_idx,
+                 const float* dweights, void* dlogits, cudaStream_t stream);
+
+/*
+ * Token rows sorted by expert into one packed buffer (no capacity per expert,
+ * nothing dropped while the buffer holds moedc_sort_rows() rows), the weighted
+ * way back, and the gradients of both.
+ *
+ * moedc_sort: the entries (t, k) of each expert in ascending t, then k (the
+ * slots of moedc_layout), expert after expert, each expert's first row on a
+ * multiple of `align` rows:
+ *   counts[e]   = entries routed to expert e
+ *   offsets[0]  = 0, offsets[e + 1] = offsets[e] + counts[e] rounded up to align
+ *   row[t][k]   = offsets[e] + slot of the entry; -1 if masked or dropped
+ *   src[row]    = t * K + k of the entry there; -1 in rows no entry reaches
+ *   sorted[row] = x[t], 0 in rows no entry reaches (all `rows` rows are written,
+ *                 so a grouped GEMM may read the padding)
+ * rows: rows of sorted and src.  With fewer than the routing needs, the entries
+ * past the end are dropped, offsets stop at rows, and MOEDC_ERR_CAPACITY is
+ * raised.  x and sorted may both be NULL: the maps alone (a product that
+ * gathers its rows through src needs no copy).
+ * dtype: MOEDC_BF16, MOEDC_F16 or MOEDC_F32; any H >= 1; ldx >= H elements
+ * from row to row of x; sorted is contiguous.  Rows that are whole 16-byte
+ * units on 16-byte boundaries move 16 bytes at a time, others by element.
+ * workspace: moedc_sort_workspace_bytes, 16-byte aligned, no initialisation.
+ * Data errors: MOEDC_ERR_EXPERT_RANGE, MOEDC_ERR_CAPACITY, MOEDC_ERR_TIMEOUT as
+ * for moedc_layout.
+ *
+ * moedc_sort_rows: rows that hold any routing of this shape,
+ *   T * K + min(E, T * K) * (align - 1); 0 for rejected arguments.
+ *
+ * moedc_unsort:
+ *   y[t][h] = round( sum over k ascending of w[t][k] * sorted[row[t][k]][h] )
+ * binary32 accumulator, entries whose row is outside [0, rows) skipped.
+ * topk_weights NULL: every weight 1, which is the gradient of moedc_sort
+ * (dx from dsorted).
+ *
+ * moedc_unsort_grad, for every entry with row r in [0, rows):
+ *   dsorted[r][h]  = round( w[t][k] * dy[t][h] ); 0 in rows whose src is < 0
+ *   dweights[t][k] = sum over h of dy[t][h] * sorted[r][h]; 0 for other entries
+ * dweights may be NULL (then sorted is not read and may be NULL too).  row and
+ * src as moedc_sort gave them; dy has lddy >= H elements from row to row.  The
+ * order of every sum is fixed: equal inputs give equal bits.
+ */
+#define MOEDC_SORT_MAX_ALIGN 1024
+MOEDC_EXPORT size_t moedc_sort_rows(int T, int K, int E, int align);
+MOEDC_EXPORT size_t moedc_sort_workspace_bytes(int T, int K, int E);
+MOEDC_EXPORT int moedc_sort(const void* x, int64_t ldx, int dtype, int T, int H,
+                 const int32_t* topk_idx, int K, int E, int align, int rows, void* sorted,
+                 int32_t* row, int32_t* src, int32_t* offsets, int32_t* counts,
+                 void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                 cudaStream_t stream);
+MOEDC_EXPORT int moedc_unsort(const void* sorted, int dtype, int rows, int H, const int32_t* row,
+                 const float* topk_weights, int T, int K, void* y, cudaStream_t stream);
+MOEDC_EXPORT int moedc_unsort_grad(const void* dy, int64_t lddy, const void* sorted, int dtype,
+                 int T, int H, int K, const int32_t* row, const int32_t* src,
+                 const float* topk_weights, int rows, void* dsorted, float* dweights,
+                 cudaStream_t stream);
+
+/*
+ * Products of packed expert rows with 4-bit weights and group scales: the
+ * experts' linear layers of a decode step (E = 1: one ordinary linear layer).
+ * For every row r in [offsets[e], offsets[e] + counts[e]) and output n < N:
+ *   dot(w, r, n) = sum over k of x[r'][k] * (q[e][n][k] - z[e][n][k / group])
+ *                                         * scales[e][n][k / group]
+ *   out[r][n] = round( dot(n) )                                   flags 0
+ *   out[r][n] = round( silu(dot(n)) * dot(N + n) )                MOEDC_SWIGLU
+ * silu(a) = a / (1 + exp(-a)); binary32 sums.  r' = r, or src[r] / top_k when
+ * src is given (the token of a sorted row: x is then read in token order).
+ * With MOEDC_SWIGLU the weights have 2N rows, gate rows 0..N-1, up rows N..2N-1.
+ *   x       bf16 or f16 [x_rows, Kd], ldx elements from row to row
+ *   wq      uint8 [E, N or 2N, Kd / 2], element k in byte k / 2, even k in the
+ *           low four bits: q in 0..15
+ *   scales  [E, N or 2N, Kd / group], scale_dtype MOEDC_BF16, _F16 or _F32
+ *   zeros   uint8 [E, N or 2N, Kd / group], values 0..15; NULL: 8 everywhere
+ *   out     [rows, N], of x's dtype; rows that belong to no expert are not written
+ * offsets int32 [E + 1] and counts int32 [E] as from moedc_sort; both NULL with
+ * E = 1: all rows.  group is 32, 64 or 128, Kd a multiple of it; x and wq
+ * 16-byte aligned and ldx a multiple of 8.
+ * Data errors (dev_status): MOEDC_ERR_EXPERT_RANGE when a row's x row lies
+ * outside [0, x_rows) (it counts as zeros), MOEDC_ERR_CAPACITY when an
+ * expert's rows pass `rows` (those are skipped).
+ */
+#define MOEDC_SWIGLU 1
+MOEDC_EXPORT int moedc_matvec_int4(const void* x, int64_t ldx, int dtype, int x_rows, int Kd,
+                 const void* wq, const void* scales, int scale_dtype, const uint8_t* zeros,
+                 int group, int E, int N, int flags, const int32_t* offsets,
+                 const int32_t* counts, const int32_t* src, int top_k, int rows, void* out,
+                 int32_t* dev_status, cudaStream_t stream);
 
 /*
  * Test hook, not for production use.  With extra_arrivals = n > 0, every
