@@ -458,7 +458,7 @@ MOEDC_EXPORT int moedc_unsort_grad(const void* dy, int64_t lddy, const void* sor
  *   out     [rows, N], of x's dtype; rows that belong to no expert are not written
  * offsets int32 [E + 1] and counts int32 [E] as from moedc_sort; both NULL with
  * E = 1: all rows.  group is 32, 64 or 128, Kd a multiple of it; x and wq
- * 16-byte aligned and ldx a multiple of 8.
+ * 16-byte aligned, scales and zeros 4-byte aligned, ldx a multiple of 8.
  * Data errors (dev_status): MOEDC_ERR_EXPERT_RANGE when a row's x row lies
  * outside [0, x_rows) (it counts as zeros), MOEDC_ERR_CAPACITY when an
  * expert's rows pass `rows` (those are skipped).
