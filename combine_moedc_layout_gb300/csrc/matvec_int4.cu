@@ -7,114 +7,346 @@
 // SMs do per weight has to fit under that stream: 46 weights per SM and clock.
 //
 // Work is cut into units of (expert, tile of output channels, chunk of rows).
-// A block of eight warps takes units in turn; each warp owns 16 weight rows of
-// the tile and, when there are few tiles, one of `wk` interleaved parts of K
-// (the parts are added in shared memory at the unit's end).  Weights, scales
-// and the rows of x travel through a ring of cp.async stages that runs on
-// across units, so the stream never drains between them.
+// One persistent block per SM takes units in turn.  Its 16 consumer warps own
+// 16 weight rows each and, when there are few tiles, one of `wk` interleaved
+// parts of K (the parts are added in shared memory at the unit's end).  One
+// more warp fills a ring of stages by TMA that runs on across units, so the
+// stream never drains between them.  x is prepared once per call by a kernel of
+// its own (records of 256 channels in the order the products read them): doing
+// that in the ring, for every block again, took as long as the stream.
 //
 // The products run on the tensor cores with the weights as the 16-row operand
-// and eight rows of x as the other.  A weight never leaves registers between
-// its unpacking and its product: q | 0x4300 is the bf16 number 128 + q (f16:
-// 0x6400, 1024 + q), and subtracting 128 + z leaves q - z, exact in either
-// type.  The group's sum is formed in binary32 from these integers and only
-// then multiplied by the group's scale, so neither weights nor scales are ever
-// rounded.  tcgen05 reads its operands from shared or tensor memory, which
-// would cost every weight a 2-byte store and a 2-byte read on the way: at the
-// HBM rate 93 + 93 bytes per SM and clock, more than shared memory moves (128).
+// and eight rows of x as the other, both in f16 with binary32 sums.  The ALU,
+// which masks and shifts, issues every other clock and is the pipe that fills
+// first, so a weight costs it one mask and a quarter of a shift and nothing else:
+// a nibble in the low bits of an f16 is the subnormal q * 2^-24 (one nibble
+// higher q * 2^-20, with x scaled by 2^-4 to match), exact as it stands.  The
+// zero point is taken out of the group's sum, sum (q - z) x = sum q x - z sum x,
+// or, where groups are short and rows many, out of the weights.
+// x is brought into f16 per row and stage by a power of two that puts its
+// largest value into [2^14, 2^15): exact down to 2^-28 of that value, and
+// 2^-39 of it below.  The group's sum is then scaled in binary32, so neither
+// weights nor scales are ever rounded.  A row of x with an infinity or a NaN
+// gives NaN.
+// tcgen05 reads its operands from shared or tensor memory, which would cost
+// every weight a 2-byte store and a 2-byte read on the way: at the HBM rate
+// 93 + 93 bytes per SM and clock, more than shared memory moves (128).
 #include <climits>
+#include <mutex>
+#include <type_traits>
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
 
 #include "lm_common.cuh"
 
 namespace moedc {
 
-constexpr int kMvThreads = 256;
-constexpr int kMvWarps = kMvThreads / kWarp;
-constexpr int kMvChunk = 128;              // channels of one warp's part of a stage
-constexpr int kMvTokens = 32;              // rows x parts of K staged together: 32 / wk rows
-// one stage: weights (16 rows x 64 bytes per warp), x, scales and zero points
-// (a 4-byte word for each weight row and group); as many stages as let two
-// blocks share an SM
-constexpr int kMvW = kMvWarps * 16 * 64;
-constexpr int kMvX = kMvTokens * kMvChunk * 2;
-constexpr int kMvRed = kMvWarps * 8 * kWarp * (int)sizeof(float);
-template <int GROUP> struct MvRing {
-    static constexpr int per_warp = 16 * 4 * (kMvChunk / GROUP);   // scale words
-    static constexpr int words = kMvWarps * per_warp;
-    static constexpr int stage = kMvW + kMvX + 2 * words;
-    static constexpr int stages = GROUP == 128 ? 6 : 5;
-};
+constexpr int kMvConsumers = 16;                       // warps
+constexpr int kMvThreads = (kMvConsumers + 1) * kWarp;
+constexpr int kMvRows = kMvConsumers * 16;             // weight rows x parts of K in a stage
+constexpr int kMvChunk = 256;                          // channels of one part in a stage
+constexpr int kMvW = kMvRows * kMvChunk / 2;           // a stage's weights
+constexpr int kMvTokens = 32;                          // rows of x x parts of K, at most
+constexpr int kMvMaxStages = 6;
+constexpr int kMvRed = kMvConsumers * 8 * kWarp * (int)sizeof(float);
+constexpr unsigned long long kMvWaitNs = 200000000ull; // bound of every wait
+// A record of x: 256 channels in f16, then 2^-24 times the sum of each of up to
+// eight groups, then 2^12 / scale.  576 bytes apart, the rows that a quarter-warp
+// reads lie in different halves of the banks.
+constexpr int kMvRecord = kMvChunk * 2 + 64;
 
 struct MatvecArgs {
-    const void* x;
-    int64_t ldx;
+    const uint8_t* x;     // records [x_rows + 1][channels / 256], the last row zeros
     int x_rows, Kd;
-    const uint8_t* wq;
     const void* scales;
-    int scale_dtype;
     const uint8_t* zeros;
     int E, N;
     const int32_t *offsets, *counts, *src;
     int top_k, rows;
     int32_t* status;
-    int lk;          // log2 of the parts of K
-    bool swiglu;
+    bool swiglu, f16;   // f16: the type of the outputs (else bf16)
+    int lk;             // log2 of the parts of K
+    int chunk_rows;     // rows of a unit, at most: 8, 16 or 32
+    int stages, stage_bytes;
+    unsigned wait_extra;
 };
 
-// `bytes` of the 16 (or 4) are read, the rest is written as zeros
-__device__ __forceinline__ void cp_async16(void* dst, const void* src, int bytes)
+// ---------------------------------------------------------------- mbarriers
+
+__device__ __forceinline__ uint32_t smem_u32(const void* p)
 {
-    asm volatile("cp.async.cg.shared.global.L2::128B [%0], [%1], 16, %2;" ::"r"(
-                     (unsigned)__cvta_generic_to_shared(dst)), "l"(src), "r"(bytes) : "memory");
+    return (uint32_t)__cvta_generic_to_shared(p);
 }
-__device__ __forceinline__ void cp_async4(void* dst, const void* src, int bytes)
+__device__ __forceinline__ void mbar_init(uint64_t* b, int count)
 {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(
-                     (unsigned)__cvta_generic_to_shared(dst)), "l"(src), "r"(bytes) : "memory");
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
 }
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N> __device__ __forceinline__ void cp_async_wait()
+__device__ __forceinline__ void mbar_arrive(uint64_t* b)
 {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_expect(uint64_t* b, int bytes)
+{
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes)
+                 : "memory");
+}
+__device__ __forceinline__ bool mbar_try(uint64_t* b, int parity)
+{
+    uint32_t ok;
+    asm volatile("{\n .reg .pred p;\n"
+                 " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
+                 " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ unsigned long long globaltimer()
+{
+    unsigned long long t;
+    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
+    return t;
+}
+// Bounded: false when the wait ran out or another one of the block did
+// (*abort).  The callers then go on without waiting, so that every barrier of
+// the block is still met and the kernel ends; the status word tells.
+__device__ __noinline__ bool mbar_wait_slow(uint64_t* b, int parity, volatile int* abort)
+{
+    // the timer is read only once the wait is a long one: reading it takes longer than
+    // most waits
+    unsigned long long t0 = 0;
+    for (int i = 0; ; ++i) {
+        if (mbar_try(b, parity)) return true;
+        if (i % 1024 != 1023) continue;
+        if (*abort) return false;
+        const unsigned long long now = globaltimer();
+        if (t0 == 0) t0 = now;
+        else if (now - t0 > kMvWaitNs) break;
+    }
+    *abort = 1;
+    return false;
+}
+__device__ __forceinline__ bool mbar_wait(uint64_t* b, int parity, volatile int* abort)
+{
+    return mbar_try(b, parity) || mbar_wait_slow(b, parity, abort);
 }
 
-template <typename T> struct Int4Of;       // q | magic = base + q, exactly
-template <> struct Int4Of<__nv_bfloat16> {
-    static constexpr uint32_t magic = 0x43004300u;      // 128
-    static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b)
+// ---------------------------------------------------------- tensor products
+
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                        uint32_t a3, uint32_t b0, uint32_t b1, const float (&c)[4])
+{
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
+        "{%8,%9}, {%10,%11,%12,%13};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]),
+          "f"(c[3]));
+}
+
+template <typename V> __device__ __forceinline__ V lds(uint32_t at);
+template <> __device__ __forceinline__ uint32_t lds<uint32_t>(uint32_t at)
+{
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+template <> __device__ __forceinline__ uint4 lds<uint4>(uint32_t at)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+template <> __device__ __forceinline__ float lds<float>(uint32_t at)
+{
+    float v;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
+    return v;
+}
+
+// Scales and zero points of one warp's rows g and g + 8 for one stage, in
+// registers as they come from memory.
+template <int GROUP, typename S> struct MvScales {
+    static constexpr int n = kMvChunk / GROUP;                 // groups
+    static constexpr int words = n * (int)sizeof(S) / 4;
+    static constexpr int zwords = n == 8 ? 2 : 1;
+    uint32_t s[2][words];
+    uint32_t z[2][zwords];
+
+    static __device__ __forceinline__ void load_row(uint32_t (&s)[words], const S* p, bool whole, int have)
     {
-        uint32_t r;
-        asm("sub.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
+        if (whole) {
+            if constexpr (words == 1) {
+                s[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            } else if constexpr (words == 2) {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+                s[0] = v.x, s[1] = v.y;
+            } else {
+#pragma unroll
+                for (int i = 0; i < words / 4; ++i) {
+                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
+                    s[4 * i] = v.x, s[4 * i + 1] = v.y, s[4 * i + 2] = v.z, s[4 * i + 3] = v.w;
+                }
+            }
+        } else if constexpr (sizeof(S) == 4) {
+#pragma unroll
+            for (int i = 0; i < n; ++i) s[i] = __float_as_uint(__ldg(reinterpret_cast<const float*>(p) + min(i, have - 1)));
+        } else {
+#pragma unroll
+            for (int i = 0; i < n; i += 2) {
+                const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
+                s[i / 2] = (uint32_t)__ldg(h + min(i, have - 1)) | (uint32_t)__ldg(h + min(i + 1, have - 1)) << 16;
+            }
+        }
     }
-    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1)
+    static __device__ __forceinline__ void load_zeros(uint32_t (&z)[zwords], const uint8_t* p, bool whole, int have)
     {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        if (whole) {
+            if constexpr (n == 2) {
+                z[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
+            } else if constexpr (n == 4) {
+                z[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
+            } else {
+                const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
+                z[0] = v.x, z[1] = v.y;
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < zwords; ++i) z[i] = 0;
+#pragma unroll
+            for (int i = 0; i < n; ++i) z[i / 4] |= (uint32_t)__ldg(p + min(i, have - 1)) << (8 * (i % 4));
+        }
     }
-};
-template <> struct Int4Of<__half> {
-    static constexpr uint32_t magic = 0x64006400u;      // 1024
-    static __device__ __forceinline__ uint32_t minus(uint32_t a, uint32_t b)
+    // rows begin at element at0 and at1; groups past the last one read it again
+    __device__ __forceinline__ void load(const MatvecArgs& a, int64_t at0, int64_t at1, int group0,
+                                         int groups, bool whole)
     {
-        uint32_t r;
-        asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-        return r;
+        const S* sp = static_cast<const S*>(a.scales);
+        const int q = min(group0, whole ? groups - n : groups - 1), have = groups - q;
+        load_row(s[0], sp + at0 + q, whole, have);
+        load_row(s[1], sp + at1 + q, whole, have);
+        if (a.zeros) {
+            load_zeros(z[0], a.zeros + at0 + q, whole, have);
+            load_zeros(z[1], a.zeros + at1 + q, whole, have);
+        }
     }
-    static __device__ __forceinline__ void mma(float (&d)[4], const uint32_t (&a)[4], uint32_t b0,
-                                               uint32_t b1)
+    // times 2^12: x's factor carries the rest of the weights' 2^24
+    __device__ __forceinline__ float scale(int row, int q) const
     {
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, "
-            "{%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+        if constexpr (sizeof(S) == 4) {
+            return __uint_as_float(s[row][q]) * 4096.0f;
+        } else {
+            const uint32_t w = s[row][q / 2];
+            if constexpr (std::is_same<S, __nv_bfloat16>::value)
+                return __uint_as_float(q % 2 ? w & 0xffff0000u : w << 16) * 4096.0f;
+            else
+                return __half2float(__ushort_as_half((unsigned short)(q % 2 ? w >> 16 : w & 0xffffu))) * 4096.0f;
+        }
+    }
+    // minus the zero point: 2^23 + z is a binary32 number whose low bits are z
+    __device__ __forceinline__ float minus_zero(int row, int q) const
+    {
+        return 8388608.0f - __uint_as_float(__byte_perm(z[row][q / 4], 0x4b000000u, 0x7540 | (q % 4)));
+    }
+    // the zero point as the weights' f16 subnormals, of the low nibbles
+    __device__ __forceinline__ uint32_t zero_f16(int row, int q) const
+    {
+        return ((z[row][q / 4] >> (8 * (q % 4))) & 0xffu) * 0x00010001u;
     }
 };
 
-// A unit: rows [r0, r0 + m) of expert e and the tile's first output channel.
+__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// Whether the zero point is subtracted from the weights (8 instructions per 32
+// channels) instead of from the sums (6 per group and eight rows).
+constexpr bool mv_subtract(int group, int nt) { return 8 * (group / 32) < 6 * nt; }
+
+// One stage of one warp: its 16 weight rows x 256 channels with 8 NT rows of x.
+//   w    address of row g at word t (128 bytes a row, 16-byte pieces permuted by the
+//        row's low three bits); the warp's other eight rows lie kMvW / 2 further
+//   x    address of row g's record at its words t
+//   c    address of the sums of x row 2t
+template <int GROUP, int NT, bool FULL, typename S>
+__device__ __forceinline__ void mv_stage(uint32_t w, uint32_t x, uint32_t c,
+                                         const MvScales<GROUP, S>& sz, bool zeros, int steps,
+                                         float (&acc)[NT][4])
+{
+    constexpr int kPer = GROUP / 32;       // 32-channel steps of a group
+    constexpr bool kSub = mv_subtract(GROUP, NT);
+    const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float sum[NT][4];
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sum[i][j] = 0.0f;
+#pragma unroll
+    for (int q = 0; q < kMvChunk / GROUP; ++q) {
+        if (!FULL && q * kPer >= steps) break;
+        float tmp[NT][4];
+        uint32_t za = 0x00080008u, zb = 0x00080008u;
+        if (kSub && zeros) {
+            za = sz.zero_f16(0, q);
+            zb = sz.zero_f16(1, q);
+        }
+#pragma unroll
+        for (int p = 0; p < kPer; ++p) {
+            const int k = q * kPer + p;
+            const uint32_t at = w ^ (k << 4);
+            const uint32_t a = lds<uint32_t>(at), b = lds<uint32_t>(at + kMvW / 2);
+            constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
+            uint32_t m[8] = {a & lo, b & lo, a & hi, b & hi, (a >> 8) & lo, (b >> 8) & lo, (a >> 8) & hi, (b >> 8) & hi};
+            if (kSub) {
+                // exact: subnormals of one exponent
+#pragma unroll
+                for (int j = 0; j < 8; ++j) m[j] = sub_f16x2(m[j], (j % 2 ? zb : za) << (j & 2 ? 4 : 0));
+            }
+#pragma unroll
+            for (int i = 0; i < NT; ++i) {
+                const uint4 v = lds<uint4>(x + k * 64 + i * 8 * kMvRecord);
+                if (p == 0) mma_f16(tmp[i], m[0], m[1], m[2], m[3], v.x, v.y, none);
+                else mma_f16(tmp[i], m[0], m[1], m[2], m[3], v.x, v.y, tmp[i]);
+                mma_f16(tmp[i], m[4], m[5], m[6], m[7], v.z, v.w, tmp[i]);
+            }
+        }
+        const float s0 = sz.scale(0, q), s1 = sz.scale(1, q);
+        float z0 = -8.0f, z1 = -8.0f;
+        if (!kSub && zeros) {
+            z0 = sz.minus_zero(0, q);
+            z1 = sz.minus_zero(1, q);
+        }
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+            if (!kSub) {
+                const float u = lds<float>(c + q * 4 + i * 8 * kMvRecord);
+                const float v = lds<float>(c + q * 4 + i * 8 * kMvRecord + kMvRecord);
+                tmp[i][0] = fmaf(z0, u, tmp[i][0]);
+                tmp[i][1] = fmaf(z0, v, tmp[i][1]);
+                tmp[i][2] = fmaf(z1, u, tmp[i][2]);
+                tmp[i][3] = fmaf(z1, v, tmp[i][3]);
+            }
+            sum[i][0] = fmaf(s0, tmp[i][0], sum[i][0]);
+            sum[i][1] = fmaf(s0, tmp[i][1], sum[i][1]);
+            sum[i][2] = fmaf(s1, tmp[i][2], sum[i][2]);
+            sum[i][3] = fmaf(s1, tmp[i][3], sum[i][3]);
+        }
+    }
+    // the stage's factor of x
+#pragma unroll
+    for (int i = 0; i < NT; ++i) {
+        const float u = lds<float>(c + 32 + i * 8 * kMvRecord);
+        const float v = lds<float>(c + 32 + i * 8 * kMvRecord + kMvRecord);
+        acc[i][0] = fmaf(u, sum[i][0], acc[i][0]);
+        acc[i][1] = fmaf(v, sum[i][1], acc[i][1]);
+        acc[i][2] = fmaf(u, sum[i][2], acc[i][2]);
+        acc[i][3] = fmaf(v, sum[i][3], acc[i][3]);
+    }
+}
+
+// --------------------------------------------------------------------- units
+
+// Rows [r0, r0 + m) of expert e and the tile's first output channel.
 struct MvUnit {
     int e, n0, r0, m;
 };
@@ -134,9 +366,10 @@ __device__ __forceinline__ void expert_rows(const MatvecArgs& a, int e, int& beg
     end = (int)(b < n ? n : 0);
 }
 
-// s_pre[e]: chunks of the experts before e
-__device__ __forceinline__ MvUnit mv_unit(const MatvecArgs& a, const int32_t* s_pre, int tiles,
-                                          int tile_n, int chunk_rows, int unit)
+// s_pre[e]: chunks of the experts before e; s_beg[e], s_end[e]: its rows
+__device__ __forceinline__ MvUnit mv_unit(const MatvecArgs& a, const int32_t* s_pre,
+                                          const int32_t* s_beg, const int32_t* s_end, int tiles,
+                                          int tile_n, int unit)
 {
     int lo = 0, hi = a.E - 1;   // last expert whose units begin at or before `unit`
     while (lo < hi) {
@@ -146,120 +379,63 @@ __device__ __forceinline__ MvUnit mv_unit(const MatvecArgs& a, const int32_t* s_
     const int chunks = s_pre[lo + 1] - s_pre[lo];
     const int in = unit - s_pre[lo] * tiles;
     const int tile = in / chunks, chunk = in - tile * chunks;   // chunks of one tile are neighbours
-    int beg, end;
-    bool over = false;
-    expert_rows(a, lo, beg, end, over);
     MvUnit u;
     u.e = lo;
     u.n0 = tile * tile_n;
-    u.r0 = beg + chunk * chunk_rows;
-    u.m = min(chunk_rows, end - u.r0);
+    u.r0 = s_beg[lo] + chunk * a.chunk_rows;
+    u.m = min(a.chunk_rows, s_end[lo] - u.r0);
     return u;
 }
 
-// Weight row that row i (0..15) of a warp's tile holds, -1 past the end: with
-// SwiGLU rows 0..7 are gate rows and rows 8..15 the up rows of the same outputs,
-// so that a thread holds both.
-__device__ __forceinline__ int mv_weight_row(const MatvecArgs& a, int n0, int i)
+// The x row of packed row r; the row of zeros where there is none.
+__device__ __forceinline__ int x_row(const MatvecArgs& a, int r, bool& bad)
 {
-    const int n = a.swiglu ? n0 + (i & 7) : n0 + i;
-    if (n >= a.N) return -1;
-    return a.swiglu && i >= 8 ? a.N + n : n;
+    int t = r;
+    if (a.src) {
+        const int i = __ldg(a.src + r);
+        t = i < 0 ? -1 : i / a.top_k;
+    }
+    if (t >= 0 && t < a.x_rows) return t;
+    bad = true;
+    return a.x_rows;
 }
 
-// One stage of one warp: 16 weight rows x 128 channels with 8 NT rows of x.
-// at0, at1: index (modulo 4) of the first scale and zero point of rows g and
-// g + 8, which tells their place in the words.
-template <typename T, int GROUP, int NT>
-__device__ __forceinline__ void mv_stage(const uint8_t* sw, const uint8_t* sx, const uint8_t* ss,
-                                         int scale_dtype, bool zeros, int at0, int at1, int steps,
-                                         float (&acc)[NT][4])
-{
-    const int lane = threadIdx.x % kWarp, g = lane >> 2, t = lane & 3;
-    constexpr int kPer = GROUP / 32;       // 32-channel steps of a group
-    float tmp[NT][4];
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {
-        if (w >= steps) break;
-        if (w % kPer == 0) {
-#pragma unroll
-            for (int i = 0; i < NT; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) tmp[i][j] = 0.0f;
-        }
-        const int q = w / kPer;            // the stage's group
-        const uint8_t* sq = ss + q * 64;   // its words: [16 rows]
-        uint32_t za, zb;
-        if (zeros) {
-            const uint8_t* sz = sq + MvRing<GROUP>::words;
-            const uint32_t a = sz[g * 4 + ((at0 + q) & 3)];
-            const uint32_t b = sz[(g + 8) * 4 + ((at1 + q) & 3)];
-            za = Int4Of<T>::magic | a | a << 16;
-            zb = Int4Of<T>::magic | b | b << 16;
-        } else {
-            za = zb = Int4Of<T>::magic | 0x00080008u;
-        }
-        const uint8_t* row = sw + g * 64 + ((w ^ ((g >> 1) & 3)) << 4) + t * 4;
-        const uint32_t wa = *reinterpret_cast<const uint32_t*>(row);
-        const uint32_t wb = *reinterpret_cast<const uint32_t*>(row + 8 * 64);
-        // register p holds weights p and p + 4 of the word
-        uint32_t lo[4], hi[4];
-#pragma unroll
-        for (int p = 0; p < 4; ++p) {
-            lo[p] = Int4Of<T>::minus(((wa >> (4 * p)) & 0x000f000fu) | Int4Of<T>::magic, za);
-            hi[p] = Int4Of<T>::minus(((wb >> (4 * p)) & 0x000f000fu) | Int4Of<T>::magic, zb);
-        }
-        const uint32_t a01[4] = {lo[0], hi[0], lo[1], hi[1]};
-        const uint32_t a23[4] = {lo[2], hi[2], lo[3], hi[3]};
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            const uint4 v = *reinterpret_cast<const uint4*>(
-                sx + (i * 8 + g) * 256 + (((w * 4 + t) ^ ((g & 1) << 2)) << 4));
-            Int4Of<T>::mma(tmp[i], a01, __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
-            Int4Of<T>::mma(tmp[i], a23, __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
-        }
-        if (w % kPer == kPer - 1) {
-            float s0, s1;
-            if (scale_dtype == MOEDC_F32) {
-                s0 = *reinterpret_cast<const float*>(sq + g * 4);
-                s1 = *reinterpret_cast<const float*>(sq + (g + 8) * 4);
-            } else {
-                const uint32_t h0 = *reinterpret_cast<const uint16_t*>(sq + g * 4 + ((at0 + q) & 1) * 2);
-                const uint32_t h1 = *reinterpret_cast<const uint16_t*>(sq + (g + 8) * 4 + ((at1 + q) & 1) * 2);
-                if (scale_dtype == MOEDC_BF16) {
-                    s0 = __uint_as_float(h0 << 16);
-                    s1 = __uint_as_float(h1 << 16);
-                } else {
-                    s0 = __half2float(__ushort_as_half((unsigned short)h0));
-                    s1 = __half2float(__ushort_as_half((unsigned short)h1));
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < NT; ++i) {
-                acc[i][0] = fmaf(s0, tmp[i][0], acc[i][0]);
-                acc[i][1] = fmaf(s0, tmp[i][1], acc[i][1]);
-                acc[i][2] = fmaf(s1, tmp[i][2], acc[i][2]);
-                acc[i][3] = fmaf(s1, tmp[i][3], acc[i][3]);
-            }
+// Where a stage's slot and phase go round the ring.
+struct MvRing {
+    int slot = 0, phase = 0;
+    __device__ __forceinline__ void next(int stages)
+    {
+        if (++slot == stages) {
+            slot = 0;
+            phase ^= 1;
         }
     }
+};
+
+__device__ __forceinline__ void store16(uint16_t* p, float v, bool f16)
+{
+    *p = f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
 }
 
 // The unit's end: the parts of K added, the epilogue, the outputs.
-template <typename T, int NT>
+template <int NT>
 __device__ __forceinline__ void mv_store(const MatvecArgs& a, const MvUnit& u, float* s_red,
-                                         float (&acc)[NT][4], T* __restrict__ out)
+                                         float (&acc)[NT][4], uint16_t* __restrict__ out)
 {
     const int lane = threadIdx.x % kWarp, g = lane >> 2, t = lane & 3;
     const int warp = threadIdx.x / kWarp;
     const int wk = 1 << a.lk, part = warp & (wk - 1), tile = warp >> a.lk;
     if (wk > 1) {
-        // [warp][value][lane]: conflict-free
+        // consumers only: the first barrier ends the reads of the unit before
+        asm volatile("bar.sync 1, %0;" ::"n"(kMvConsumers * kWarp) : "memory");
+        if (part != 0) {
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
+            for (int i = 0; i < NT; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) s_red[(warp * NT * 4 + i * 4 + j) * kWarp + lane] = acc[i][j];
-        __syncthreads();
+                for (int j = 0; j < 4; ++j)
+                    s_red[(warp * NT * 4 + i * 4 + j) * kWarp + lane] = acc[i][j];
+        }
+        asm volatile("bar.sync 1, %0;" ::"n"(kMvConsumers * kWarp) : "memory");
         if (part != 0) return;
         for (int p = 1; p < wk; ++p)
 #pragma unroll
@@ -268,49 +444,165 @@ __device__ __forceinline__ void mv_store(const MatvecArgs& a, const MvUnit& u, f
                 for (int j = 0; j < 4; ++j)
                     acc[i][j] += s_red[((warp + p) * NT * 4 + i * 4 + j) * kWarp + lane];
     }
-    const int n0 = u.n0 + tile * (a.swiglu ? 8 : 16);
+    const int n = u.n0 + tile * 8 + g, n2 = n + (kMvRows >> a.lk) / 2;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
             const int r = i * 8 + t * 2 + c;
             if (r >= u.m) continue;
-            T* o = out + (int64_t)(u.r0 + r) * a.N;
+            uint16_t* o = out + (int64_t)(u.r0 + r) * a.N;
             if (a.swiglu) {
                 const float v = acc[i][c];
-                if (n0 + g < a.N) o[n0 + g] = from_f32<T>(v / (1.0f + expf(-v)) * acc[i][2 + c]);
+                if (n < a.N) store16(o + n, v / (1.0f + expf(-v)) * acc[i][2 + c], a.f16);
             } else {
-                if (n0 + g < a.N) o[n0 + g] = from_f32<T>(acc[i][c]);
-                if (n0 + g + 8 < a.N) o[n0 + g + 8] = from_f32<T>(acc[i][2 + c]);
+                if (n < a.N) store16(o + n, acc[i][c], a.f16);
+                if (n2 < a.N) store16(o + n2, acc[i][2 + c], a.f16);
             }
         }
 }
 
-template <typename T, int GROUP>
-__global__ void __launch_bounds__(kMvThreads, 2)
-matvec_int4_kernel(const __grid_constant__ MatvecArgs a, T* __restrict__ out)
+// Records of x, a warp each: eight channels a lane, brought into f16 range,
+// summed by group, and stored in the order of the weights' registers, channels
+// (0,4), (1,5) 2^-4, (2,6), (3,7) 2^-4.
+template <typename T>
+__global__ void __launch_bounds__(256)
+matvec_x_kernel(const T* __restrict__ x, int64_t ldx, int x_rows, int Kd, int group,
+                uint8_t* __restrict__ records)
 {
-    extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ int64_t s_scan[kMvWarps];
     pdl_enter();
-    using Ring = MvRing<GROUP>;
-    constexpr int kStage = Ring::stage, kStages = Ring::stages;
-    uint8_t* ring = smem;
-    float* s_red = reinterpret_cast<float*>(smem + kStages * kStage);
-    int32_t* s_pre = reinterpret_cast<int32_t*>(smem + kStages * kStage + kMvRed);
+    const int lane = threadIdx.x % kWarp;
+    const int chunks = (Kd + kMvChunk - 1) / kMvChunk;
+    const int64_t n = (int64_t)(x_rows + 1) * chunks;
+    for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / kWarp; i < n; i += (int64_t)gridDim.x * 8) {
+        const int64_t r = i / chunks;
+        const int k = (int)(i - r * chunks) * kMvChunk + lane * 8;
+        Pack<T, 8> h;
+        float f[8] = {};
+        if (r < x_rows && k < Kd) {
+            h = *reinterpret_cast<const Pack<T, 8>*>(x + r * ldx + k);
+#pragma unroll
+            for (int j = 0; j < 8; ++j) f[j] = to_f32(h.v[j]);
+        }
+        unsigned top = 0;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) top = max(top, __float_as_uint(f[j]) & 0x7fffffffu);
+        // scale = 2^sc: the record's largest exponent goes to 14
+        const int sc = min(127, 141 - (int)(__reduce_max_sync(0xffffffffu, top) >> 23));
+        const float scale = __uint_as_float((unsigned)(sc + 127) << 23);
+        float sum = 0.0f;
+        Pack<__half2, 4> o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            __half2 b = __floats2half2_rn(f[j] * scale, f[j + 4] * scale);
+            const float2 v = __half22float2(b);
+            sum += v.x + v.y;
+            if (j & 1) b = __floats2half2_rn(v.x * 0.0625f, v.y * 0.0625f);   // the odd nibble
+            o.v[j] = b;
+        }
+        for (int d = group / 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        uint8_t* to = records + i * kMvRecord;
+        reinterpret_cast<Pack<__half2, 4>*>(to)[lane] = o;
+        float* sums = reinterpret_cast<float*>(to + kMvChunk * 2);
+        const int per = group / 8;
+        if (lane % per == 0) sums[lane / per] = sum * 5.9604644775390625e-8f;
+        if (lane == 0) sums[8] = __uint_as_float((unsigned)(139 - sc) << 23);
+    }
+}
+
+// What a consumer warp carries through its units.
+struct MvWarp {
+    uint32_t base, ow, ox, oc;     // shared-memory offsets: weights, x, sums of x
+    int part, row, half;
+    int64_t at0, at1;              // first scale of the unit's two rows
+    bool whole;                    // a row's groups of a stage are one aligned load
+};
+
+// First scales of the warp's two rows of a unit; rows past the last read the last
+// one's, and nothing uses them.
+__device__ __forceinline__ void mv_rows(const MatvecArgs& a, MvWarp& w, const MvUnit& u, int groups)
+{
+    const int n0 = min(u.n0 + w.row, a.N - 1);
+    const int n1 = a.swiglu ? n0 + a.N : min(u.n0 + w.half + w.row, a.N - 1);
+    const int64_t first = (int64_t)u.e * (a.swiglu ? 2 * a.N : a.N);
+    w.at0 = (first + n0) * groups;
+    w.at1 = (first + n1) * groups;
+}
+
+// All stages of one unit with 8 NT rows of x.  `now` holds the first stage's
+// scales and is left with those of the next unit's (`un`, when there is one).
+template <int GROUP, int NT, typename S>
+__device__ __forceinline__ void mv_consume(const MatvecArgs& a, MvWarp& w, MvRing& ring, uint64_t* full,
+                                           uint64_t* empty, volatile int* abort, int ksteps, int groups,
+                                           bool more, const MvUnit& un, MvScales<GROUP, S>& now,
+                                           float (&acc)[NT][4])
+{
+    constexpr int kGroups = kMvChunk / GROUP;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
+    int left = a.Kd - w.part * kMvChunk, q = w.part * kGroups;
+    const bool zeros = a.zeros != nullptr;
+    for (int s = 1; s <= ksteps; ++s, left -= kMvChunk << a.lk) {
+        MvScales<GROUP, S> next = now;
+        q += kGroups << a.lk;
+        if (s == ksteps) {
+            q = w.part * kGroups;
+            if (more) mv_rows(a, w, un, groups);
+        }
+        next.load(a, w.at0, w.at1, q, groups, w.whole);
+        mbar_wait(full + ring.slot, ring.phase, abort);
+        const uint32_t at = w.base + ring.slot * a.stage_bytes;
+        if (left >= kMvChunk) mv_stage<GROUP, NT, true>(at + w.ow, at + w.ox, at + w.oc, now, zeros, 8, acc);
+        else mv_stage<GROUP, NT, false>(at + w.ow, at + w.ox, at + w.oc, now, zeros, left / 32, acc);
+        __syncwarp();
+        if (threadIdx.x % kWarp == 0) mbar_arrive(empty + ring.slot);
+        ring.next(a.stages);
+        now = next;
+    }
+}
+
+// NTMAX: eights of rows in a unit, at most
+template <int GROUP, typename S, int NTMAX>
+__global__ void __launch_bounds__(kMvThreads, 1)
+matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__ CUtensorMap wmap,
+                   uint16_t* __restrict__ out)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int64_t s_scan[kMvThreads / kWarp];
+    __shared__ uint64_t full[kMvMaxStages], empty[kMvMaxStages], never;
+    __shared__ volatile int s_abort;
+    constexpr int kGroups = kMvChunk / GROUP;      // of a row in a stage
 
     const int lane = threadIdx.x % kWarp, g = lane >> 2, t = lane & 3;
     const int warp = threadIdx.x / kWarp;
     const int wk = 1 << a.lk, part = warp & (wk - 1), tile = warp >> a.lk;
-    const int chunk_rows = kMvTokens >> a.lk;
-    const int tile_n = (kMvWarps >> a.lk) * (a.swiglu ? 8 : 16);
+    const int half = (kMvRows >> a.lk) / 2;                // weight rows of half a tile
+    const int tile_n = a.swiglu ? half : 2 * half;
     const int tiles = (a.N + tile_n - 1) / tile_n;
     const int groups = a.Kd / GROUP;
     const int wrows = a.swiglu ? 2 * a.N : a.N;
     const int ksteps = (a.Kd + (kMvChunk << a.lk) - 1) / (kMvChunk << a.lk);
+    // a stage: weights [half of the tile][part][row][128 bytes] (with SwiGLU the halves
+    // are gate and up rows), x [part][row] as records
+    float* s_red = reinterpret_cast<float*>(smem + a.stages * a.stage_bytes);
+    int32_t* s_pre = reinterpret_cast<int32_t*>(smem + a.stages * a.stage_bytes + kMvRed);
+    int32_t *s_beg = s_pre + a.E + 1, *s_end = s_beg + a.E;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < a.stages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, kMvConsumers);
+        }
+        mbar_init(&never, 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    pdl_enter();
 
     // chunks of the experts before each one
-    bool bad = false, over = false;
+    bool over = false;
     {
         const int per = (a.E + kMvThreads - 1) / kMvThreads;
         const int e0 = threadIdx.x * per;
@@ -318,7 +610,9 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, T* __restrict__ out)
         for (int e = e0; e < min(a.E, e0 + per); ++e) {
             int beg, end;
             expert_rows(a, e, beg, end, over);
-            const int c = (end - beg) / chunk_rows + ((end - beg) % chunk_rows != 0);
+            const int c = (end - beg) / a.chunk_rows + ((end - beg) % a.chunk_rows != 0);
+            s_beg[e] = beg;
+            s_end[e] = end;
             s_pre[e] = c;
             sum += c;
         }
@@ -346,128 +640,95 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, T* __restrict__ out)
         __syncthreads();
     }
     const int units = s_pre[a.E] * tiles;
-    if (over) raise_status(a.status, MOEDC_ERR_CAPACITY);
+    if (over && blockIdx.x == 0) raise_status(a.status, MOEDC_ERR_CAPACITY);
 
-    // ---- what this thread copies, for the unit the ring's head is in
-    int p_unit = blockIdx.x, p_step = 0;
-    const uint8_t* p_w[2];      // rows g and g + 8, 16 bytes t of 64
-    int64_t p_s[2];             // their first scale's index
-    const uint8_t* p_x[2];      // two pieces of x: token (and part) by thread, null: zeros
-    auto open = [&]() {
-        const MvUnit u = mv_unit(a, s_pre, tiles, tile_n, chunk_rows, p_unit);
-        const int n0 = u.n0 + tile * (a.swiglu ? 8 : 16);
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int n = mv_weight_row(a, n0, g + 8 * i);
-            const int64_t row = (int64_t)u.e * wrows + n;
-            p_w[i] = n < 0 ? nullptr : a.wq + row * (a.Kd / 2) + t * 16;
-            p_s[i] = n < 0 ? -1 : row * groups;
-            // pieces of x: thread i * 256 + tid of [32 / wk rows][wk parts][16 pieces]
-            const int id = i * kMvThreads + threadIdx.x;
-            const int r = id >> (4 + a.lk);
-            int64_t xr = -1;
-            if (r < u.m) {
-                xr = u.r0 + r;
-                if (a.src) {
-                    const int at = __ldg(a.src + u.r0 + r);
-                    xr = at < 0 ? -1 : at / a.top_k;
+    MvRing ring;
+    if (warp < kMvConsumers) {
+        if (a.wait_extra) mbar_wait(&never, 0, &s_abort);
+        MvWarp w;
+        w.part = part;
+        w.row = tile * 8 + g;                              // in each half of the tile
+        w.half = half;
+        w.base = smem_u32(smem);
+        w.ow = part * half * 128 + w.row * 128 + (g << 4) + t * 4;
+        w.ox = kMvW + (part * a.chunk_rows + g) * kMvRecord + t * 16;
+        w.oc = kMvW + (part * a.chunk_rows + 2 * t) * kMvRecord + kMvChunk * 2;
+        w.whole = groups % kGroups == 0 &&
+                  reinterpret_cast<uintptr_t>(a.scales) % (kGroups * sizeof(S) < 16 ? kGroups * sizeof(S) : 16) == 0 &&
+                  reinterpret_cast<uintptr_t>(a.zeros) % kGroups == 0;
+        int unit = blockIdx.x;
+        if (unit < units) {
+            MvUnit u = mv_unit(a, s_pre, s_beg, s_end, tiles, tile_n, unit);
+            MvScales<GROUP, S> now;
+            mv_rows(a, w, u, groups);
+            now.load(a, w.at0, w.at1, part * kGroups, groups, w.whole);
+            while (unit < units) {
+                unit += gridDim.x;
+                const bool more = unit < units;
+                MvUnit un = u;
+                if (more) un = mv_unit(a, s_pre, s_beg, s_end, tiles, tile_n, unit);
+                if (NTMAX == 1 || u.m <= 8) {
+                    float acc[1][4];
+                    mv_consume<GROUP, 1, S>(a, w, ring, full, empty, &s_abort, ksteps, groups, more, un, now, acc);
+                    mv_store<1>(a, u, s_red, acc, out);
+                } else if (NTMAX == 2 || u.m <= 16) {
+                    float acc[2][4];
+                    mv_consume<GROUP, 2, S>(a, w, ring, full, empty, &s_abort, ksteps, groups, more, un, now, acc);
+                    mv_store<2>(a, u, s_red, acc, out);
+                } else if constexpr (NTMAX == 4) {
+                    float acc[4][4];
+                    mv_consume<GROUP, 4, S>(a, w, ring, full, empty, &s_abort, ksteps, groups, more, un, now, acc);
+                    mv_store<4>(a, u, s_red, acc, out);
                 }
-                if (xr < 0 || xr >= a.x_rows) {
-                    xr = -1;
-                    bad = true;
-                }
-            }
-            p_x[i] = xr < 0 ? nullptr : static_cast<const uint8_t*>(a.x) + xr * a.ldx * 2;
-        }
-    };
-    auto issue = [&](int slot) {
-        if (p_unit < units) {
-            if (p_step == 0) open();
-            uint8_t* st = ring + slot * kStage;
-            const int k0 = (p_step << a.lk) * kMvChunk;            // of the stage
-            const int kw = k0 + part * kMvChunk;                   // of this warp
-            uint8_t* w = st + warp * 1024 + g * 64 + ((t ^ ((g >> 1) & 3)) << 4);
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const bool ok = p_w[i] && kw + t * 32 < a.Kd;
-                cp_async16(w + i * 512, ok ? p_w[i] + kw / 2 : a.wq, ok ? 16 : 0);
-                const int id = i * kMvThreads + threadIdx.x;
-                const int c = id & 15, xp = (id >> 4) & (wk - 1), r = id >> (4 + a.lk);
-                const int kx = k0 + xp * kMvChunk + c * 8;
-                const bool okx = p_x[i] && kx < a.Kd;
-                cp_async16(st + kMvW + (xp * chunk_rows + r) * 256 + ((c ^ ((r & 1) << 2)) << 4),
-                           okx ? p_x[i] + (int64_t)kx * 2 : a.x, okx ? 16 : 0);
-            }
-            // scales and zero points of (row, group): the aligned 4-byte word that holds each.
-            // Lane t of row g takes groups t of its two rows.
-            constexpr int kGroups = kMvChunk / GROUP;
-            const int gi = kw / GROUP + t;
-            if (t < kGroups && gi < groups) {
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    if (p_s[i] < 0) continue;
-                    const int64_t at = p_s[i] + gi;
-                    const int64_t total = (int64_t)a.E * wrows * groups;
-                    uint8_t* s = st + kMvW + kMvX + warp * Ring::per_warp + t * 64 + (g + 8 * i) * 4;
-                    if (a.scale_dtype == MOEDC_F32) {
-                        cp_async4(s, static_cast<const float*>(a.scales) + at, 4);
-                    } else {
-                        const int64_t w2 = at & ~(int64_t)1;
-                        cp_async4(s, static_cast<const uint16_t*>(a.scales) + w2, w2 + 1 < total ? 4 : 2);
-                    }
-                    if (a.zeros) {
-                        const int64_t w4 = at & ~(int64_t)3;
-                        cp_async4(s + Ring::words, a.zeros + w4, (int)min((int64_t)4, total - w4));
-                    }
-                }
-            }
-            if (++p_step == ksteps) {
-                p_step = 0;
-                p_unit += gridDim.x;
+                u = un;
             }
         }
-        cp_async_commit();   // an empty group past the end keeps the count
-    };
-
-#pragma unroll
-    for (int s = 0; s < kStages - 1; ++s) issue(s);
-
-    int slot = 0;
-    // one unit with 8 NT rows of x
-    auto run = [&](auto nt, const MvUnit& u) {
-        constexpr int NT = decltype(nt)::value;
-        float acc[NT][4];
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-        const int n0 = u.n0 + tile * (a.swiglu ? 8 : 16);
-        const int64_t base = (int64_t)u.e * wrows;
-        const int i0 = (int)(((base + mv_weight_row(a, n0, g)) * groups) & 3);
-        const int i1 = (int)(((base + mv_weight_row(a, n0, g + 8)) * groups) & 3);
-        for (int s = 0; s < ksteps; ++s) {
-            cp_async_wait<kStages - 2>();
-            __syncthreads();
-            issue(slot == 0 ? kStages - 1 : slot - 1);
-            const uint8_t* st = ring + slot * kStage;
-            const int kw = ((s << a.lk) + part) * kMvChunk;
-            const int g0 = kw / GROUP;
-            mv_stage<T, GROUP, NT>(st + warp * 1024, st + kMvW + part * chunk_rows * 256,
-                                   st + kMvW + kMvX + warp * Ring::per_warp, a.scale_dtype,
-                                   a.zeros != nullptr, i0 + g0, i1 + g0,
-                                   min(4, (a.Kd - kw) / 32), acc);
-            slot = slot + 1 == kStages ? 0 : slot + 1;
+    } else {
+        // the producer warp: two TMA boxes of weights per part, one for each half of the
+        // tile's rows, and a bulk copy for each record of x, by lane
+        int issued = 0;
+        bool bad = false;
+        const int chunks = (a.Kd + kMvChunk - 1) / kMvChunk;
+        for (int unit = blockIdx.x; unit < units && !s_abort; unit += gridDim.x) {
+            const MvUnit u = mv_unit(a, s_pre, s_beg, s_end, tiles, tile_n, unit);
+            const int wrow = u.e * wrows + u.n0;
+            const int r = lane >> a.lk, p = lane & (wk - 1);       // this lane's record
+            const bool mine = r < u.m;
+            const uint8_t* xr = mine ? a.x + (int64_t)x_row(a, u.r0 + r, bad) * chunks * kMvRecord : nullptr;
+            for (int s = 0; s < ksteps; ++s) {
+                const bool go = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
+                if (!__all_sync(0xffffffffu, go)) break;
+                uint8_t* st = smem + ring.slot * a.stage_bytes;
+                const uint32_t bar = smem_u32(full + ring.slot);
+                const int c0 = s << a.lk;
+                const int live = min(wk, chunks - c0);             // parts that have channels left
+                if (lane == 0) mbar_arrive_expect(full + ring.slot, live * (2 * half * 128 + u.m * kMvRecord));
+                __syncwarp();
+                if (lane < 2 * live)
+                    asm volatile(
+                        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+                        "[%0], [%1, {%2, %3}], [%4];" ::"r"(
+                            smem_u32(st + (lane & 1) * (kMvW / 2) + (lane >> 1) * half * 128)), "l"(&wmap),
+                        "r"((c0 + (lane >> 1)) * (kMvChunk / 2)),
+                        "r"(wrow + (lane & 1) * (a.swiglu ? a.N : half)), "r"(bar) : "memory");
+                if (mine && p < live)
+                    asm volatile(
+                        "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
+                            smem_u32(st + kMvW + (p * a.chunk_rows + r) * kMvRecord)),
+                        "l"(xr + (int64_t)(c0 + p) * kMvRecord), "n"(kMvRecord), "r"(bar) : "memory");
+                ring.next(a.stages);
+                ++issued;
+            }
         }
-        mv_store<T, NT>(a, u, s_red, acc, out);
-    };
-    for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
-        const MvUnit u = mv_unit(a, s_pre, tiles, tile_n, chunk_rows, unit);
-        if (u.m <= 8) run(std::integral_constant<int, 1>{}, u);
-        else if (u.m <= 16) run(std::integral_constant<int, 2>{}, u);
-        else run(std::integral_constant<int, 4>{}, u);
+        // no copy may land after the block has gone, whatever else gave up
+        for (int n = max(0, issued - a.stages); n < issued; ++n) {
+            volatile int alone = 0;
+            if (!mbar_wait(full + n % a.stages, (n / a.stages) & 1, &alone)) s_abort = 1;
+        }
+        if (bad) raise_status(a.status, MOEDC_ERR_EXPERT_RANGE);
     }
-    cp_async_wait<0>();
-    if (bad) raise_status(a.status, MOEDC_ERR_EXPERT_RANGE);
+    __syncthreads();
+    if (threadIdx.x == 0 && s_abort) raise_status(a.status, MOEDC_ERR_TIMEOUT);
 }
 
 }  // namespace moedc
@@ -475,77 +736,178 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, T* __restrict__ out)
 namespace moedc_host {
 namespace {
 
-template <int GROUP> size_t mv_smem(int E)
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 {
-    using Ring = moedc::MvRing<GROUP>;
-    return (size_t)Ring::stages * Ring::stage + moedc::kMvRed + (size_t)(E + 1) * sizeof(int32_t);
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+        void* p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
+                                             &found) != cudaSuccess || found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
+    }();
+    return fn;
 }
 
-template <typename T, int GROUP>
-int launch_matvec(moedc::MatvecArgs a, void* out, cudaStream_t stream)
+constexpr int kMvSmem = 227 * 1024;
+
+// Parts of K and rows of a unit.  A block's time for a unit grows with the
+// weights it holds and, once the products outweigh the unpacking, with the
+// rows; the whole takes as long as the rounds of units the blocks need.  The
+// number of experts with rows and their mean rows are the host's guess: at most
+// every row has its own.
+void mv_shape(moedc::MatvecArgs& a, int blocks)
 {
-    auto* k = moedc::matvec_int4_kernel<T, GROUP>;
-    const size_t smem = mv_smem<GROUP>(a.E);
-    if (cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             (int)mv_smem<GROUP>(MOEDC_MAX_E)) != cudaSuccess)
-        return MOEDC_ERR_CUDA;
-    const int resident = resident_blocks((const void*)k, moedc::kMvThreads, smem);
-    // parts of K: as few as give every block some eight units (the last round of
-    // units is then at most an eighth of the work), counting every expert that
-    // can have rows
     const int64_t active = a.E < a.rows ? a.E : a.rows;
-    const int64_t per = (a.rows + active - 1) / active;
-    int64_t units = 0;
-    for (a.lk = 0;; ++a.lk) {
-        const int tile_n = (moedc::kMvWarps >> a.lk) * (a.swiglu ? 8 : 16);
-        const int chunk = moedc::kMvTokens >> a.lk;
-        units = active * ((a.N + tile_n - 1) / tile_n) * ((per + chunk - 1) / chunk);
-        if (a.lk == 2 || units >= 8 * (int64_t)resident) break;
-    }
+    const double per = (double)a.rows / active;
+    double best = 0.0;
+    for (int lk = 0; lk <= 2; ++lk)
+        for (int chunk = 8; chunk <= moedc::kMvTokens >> lk; chunk *= 2) {
+            const int tile_n = (moedc::kMvRows >> lk) / (a.swiglu ? 2 : 1);
+            const double tiles = (a.N + tile_n - 1) / tile_n;
+            const double chunks = (double)(int64_t)((per + chunk - 1) / chunk);
+            const double rounds = (double)(int64_t)((active * tiles * chunks + blocks - 1) / blocks);
+            const double rows = per < chunk ? per : chunk;
+            const double cost = rounds / (1 << lk) * (rows <= 8 ? 44.0 : rows <= 16 ? 44.0 : 55.0);
+            if (best == 0.0 || cost < best * 0.97) {
+                best = cost;
+                a.lk = lk;
+                a.chunk_rows = chunk;
+            }
+        }
+}
+
+template <int GROUP, typename S, int NTMAX>
+int launch_matvec(moedc::MatvecArgs a, const void* wq, void* out, cudaStream_t stream)
+{
+    auto* k = moedc::matvec_int4_kernel<GROUP, S, NTMAX>;
+    static std::once_flag once;
+    static cudaError_t attr = cudaSuccess;
+    std::call_once(once, [&] {
+        attr = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kMvSmem - 1024);
+    });
+    if (attr != cudaSuccess) return MOEDC_ERR_CUDA;
+    const int blocks = sm_count();
+    a.stage_bytes = (moedc::kMvW + (a.chunk_rows << a.lk) * moedc::kMvRecord + 1023) / 1024 * 1024;
+    const size_t fixed = moedc::kMvRed + (3 * (size_t)a.E + 1) * sizeof(int32_t);
+    a.stages = (int)((kMvSmem - 1024 - fixed) / a.stage_bytes);
+    if (a.stages > moedc::kMvMaxStages) a.stages = moedc::kMvMaxStages;
+    const size_t smem = (size_t)a.stages * a.stage_bytes + fixed;
+
+    const auto encode = tensor_map_encoder();
+    if (!encode) return MOEDC_ERR_CUDA;
+    const int wrows = a.swiglu ? 2 * a.N : a.N;
+    const int part_rows = moedc::kMvRows >> a.lk;
+    CUtensorMap map;
+    const cuuint64_t dims[2] = {(cuuint64_t)a.Kd / 2, (cuuint64_t)a.E * wrows};
+    const cuuint64_t strides[1] = {(cuuint64_t)a.Kd / 2};
+    const cuuint32_t box[2] = {moedc::kMvChunk / 2, (cuuint32_t)part_rows / 2};
+    const cuuint32_t elem[2] = {1, 1};
+    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(wq), dims, strides, box, elem,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+        return MOEDC_ERR_CUDA;
+
+    const int tile_n = part_rows / (a.swiglu ? 2 : 1);
+    const int64_t most = ((int64_t)a.rows / a.chunk_rows + (a.E < a.rows ? a.E : a.rows)) *
+                         ((a.N + tile_n - 1) / tile_n);
     clear_stale_error();
-    launch(k, (int)(units < resident ? units : resident), moedc::kMvThreads, smem, stream, a,
-           static_cast<T*>(out));
+    launch(k, (int)(most < blocks ? most : blocks), moedc::kMvThreads, smem, stream, a, map,
+           static_cast<uint16_t*>(out));
     return launch_status();
 }
 
-template <typename T>
-int launch_matvec_group(const moedc::MatvecArgs& a, int group, void* out, cudaStream_t stream)
+template <int GROUP, typename S>
+int launch_matvec_rows(const moedc::MatvecArgs& a, const void* wq, void* out, cudaStream_t stream)
 {
-    return group == 32   ? launch_matvec<T, 32>(a, out, stream)
-           : group == 64 ? launch_matvec<T, 64>(a, out, stream)
-                         : launch_matvec<T, 128>(a, out, stream);
+    return a.chunk_rows == 8    ? launch_matvec<GROUP, S, 1>(a, wq, out, stream)
+           : a.chunk_rows == 16 ? launch_matvec<GROUP, S, 2>(a, wq, out, stream)
+                                : launch_matvec<GROUP, S, 4>(a, wq, out, stream);
+}
+
+template <typename S>
+int launch_matvec_group(const moedc::MatvecArgs& a, int group, const void* wq, void* out, cudaStream_t stream)
+{
+    return group == 32   ? launch_matvec_rows<32, S>(a, wq, out, stream)
+           : group == 64 ? launch_matvec_rows<64, S>(a, wq, out, stream)
+                         : launch_matvec_rows<128, S>(a, wq, out, stream);
+}
+
+template <typename T>
+int launch_matvec_x(const void* x, int64_t ldx, int x_rows, int Kd, int group, uint8_t* records, cudaStream_t stream)
+{
+    const int64_t n = ((int64_t)x_rows + 1) * ((Kd + moedc::kMvChunk - 1) / moedc::kMvChunk);
+    const int64_t want = (n + 7) / 8, most = 8 * (int64_t)sm_count();
+    clear_stale_error();
+    launch(moedc::matvec_x_kernel<T>, (int)(want < most ? want : most), 256, 0, stream,
+           static_cast<const T*>(x), ldx, x_rows, Kd, group, records);
+    return launch_status();
 }
 
 }  // namespace
 }  // namespace moedc_host
+
+extern "C" size_t moedc_matvec_int4_workspace_bytes(int x_rows, int Kd)
+{
+    if (x_rows < 0 || Kd < 1) return 0;
+    return ((size_t)x_rows + 1) * ((Kd + (size_t)moedc::kMvChunk - 1) / moedc::kMvChunk) * moedc::kMvRecord;
+}
 
 extern "C" int moedc_matvec_int4(const void* x, int64_t ldx, int dtype, int x_rows, int Kd,
                                  const void* wq, const void* scales, int scale_dtype,
                                  const uint8_t* zeros, int group, int E, int N, int flags,
                                  const int32_t* offsets, const int32_t* counts,
                                  const int32_t* src, int top_k, int rows, void* out,
-                                 int32_t* dev_status, cudaStream_t stream)
+                                 void* workspace, size_t workspace_bytes, int32_t* dev_status,
+                                 cudaStream_t stream)
 {
     using namespace moedc_host;
     if ((dtype != MOEDC_BF16 && dtype != MOEDC_F16) || !lm_dtype_ok(scale_dtype)) return MOEDC_ERR_ARG;
     if (group != 32 && group != 64 && group != 128) return MOEDC_ERR_ARG;
     if (Kd < group || Kd % group != 0 || E < 1 || E > MOEDC_MAX_E || N < 1 || x_rows < 0 ||
-        rows < 0 || (flags & ~MOEDC_SWIGLU) != 0 || (flags && N > INT32_MAX / 2))
+        x_rows == INT32_MAX || rows < 0 || (flags & ~MOEDC_SWIGLU) != 0)
         return MOEDC_ERR_ARG;
     if ((offsets == nullptr) != (counts == nullptr) || (!offsets && E != 1)) return MOEDC_ERR_ARG;
     if (src && top_k < 1) return MOEDC_ERR_ARG;
     if (!wq || !scales || !dev_status || ldx < Kd || ldx % 8 != 0) return MOEDC_ERR_ARG;
-    if (!aligned(x, 16) || !aligned(wq, 16) || !aligned(scales, 4) || !aligned(zeros, 4) ||
+    if (!aligned(x, 16) || !aligned(wq, 16) || !aligned(scales, lm_dtype_size(scale_dtype)) ||
         !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(src, 4) || !aligned(out, 2) ||
         !aligned(dev_status, 4))
         return MOEDC_ERR_ARG;
-    // units (expert, tile, chunk of at least 8 rows) are counted in 32 bits
-    if (((int64_t)rows / 8 + E) * ((int64_t)N / 16 + 1) > INT32_MAX) return MOEDC_ERR_ARG;
+    // weight rows and units (expert, tile, chunk of at least 8 rows) are counted in 32 bits
+    if ((int64_t)E * N * (flags ? 2 : 1) > INT32_MAX - moedc::kMvRows ||
+        ((int64_t)rows / 8 + E) * ((int64_t)N / 32 + 1) > INT32_MAX)
+        return MOEDC_ERR_ARG;
     if (rows == 0) return MOEDC_OK;
     if (!out || !x) return MOEDC_ERR_ARG;
-    const moedc::MatvecArgs a{x, ldx, x_rows, Kd, static_cast<const uint8_t*>(wq), scales,
-                              scale_dtype, zeros, E, N, offsets, counts, src, top_k, rows,
-                              dev_status, 0, (flags & MOEDC_SWIGLU) != 0};
-    return dtype == MOEDC_F16 ? launch_matvec_group<__half>(a, group, out, stream)
-                              : launch_matvec_group<__nv_bfloat16>(a, group, out, stream);
+    if (!workspace || !aligned(workspace, 16) ||
+        workspace_bytes < moedc_matvec_int4_workspace_bytes(x_rows, Kd))
+        return MOEDC_ERR_ARG;
+    moedc::MatvecArgs a{};
+    a.x_rows = x_rows;
+    a.Kd = Kd;
+    a.scales = scales;
+    a.zeros = zeros;
+    a.E = E;
+    a.N = N;
+    a.offsets = offsets;
+    a.counts = counts;
+    a.src = src;
+    a.top_k = top_k;
+    a.rows = rows;
+    a.status = dev_status;
+    a.swiglu = (flags & MOEDC_SWIGLU) != 0;
+    a.wait_extra = test_wait_extra();
+    a.f16 = dtype == MOEDC_F16;
+    uint8_t* records = static_cast<uint8_t*>(workspace);
+    a.x = records;
+    mv_shape(a, sm_count());
+    const int st = dtype == MOEDC_F16
+                       ? launch_matvec_x<__half>(x, ldx, x_rows, Kd, group, records, stream)
+                       : launch_matvec_x<__nv_bfloat16>(x, ldx, x_rows, Kd, group, records, stream);
+    if (st != MOEDC_OK) return st;
+    return scale_dtype == MOEDC_F32   ? launch_matvec_group<float>(a, group, wq, out, stream)
+           : scale_dtype == MOEDC_F16 ? launch_matvec_group<__half>(a, group, wq, out, stream)
+                                      : launch_matvec_group<__nv_bfloat16>(a, group, wq, out, stream);
 }

@@ -46,7 +46,7 @@ EXPORTED = ("moedc_api_version", "moedc_strerror", "moedc_layout_workspace_bytes
             "moedc_rank_dispatch", "moedc_rank_combine", "moedc_combine_e4m3",
             "moedc_gate", "moedc_gate_grad", "moedc_sort_rows", "moedc_sort_workspace_bytes",
            "moedc_sort", "moedc_unsort", "moedc_unsort_grad", "moedc_matvec_int4",
-           "moedc_layout_dispatch_workspace_bytes", "moedc_test_set_wait_extra")
+           "moedc_matvec_int4_workspace_bytes", "moedc_layout_dispatch_workspace_bytes", "moedc_test_set_wait_extra")
 
 STATIC_SCRATCH_BYTES = 1 << 20   # MOEDC_STATIC_SCRATCH_BYTES
 
@@ -119,8 +119,10 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.moedc_unsort_grad.argtypes = [P, L, P, I, I, I, I, P, P, P, I, P, P, P]
     lib.moedc_unsort_grad.restype = I
     lib.moedc_matvec_int4.argtypes = [P, L, I, I, I, P, P, I, P, I, I, I, I, P, P, P, I, I, P, P,
-                                      P]
+                                      Z, P, P]
     lib.moedc_matvec_int4.restype = I
+    lib.moedc_matvec_int4_workspace_bytes.argtypes = [I, I]
+    lib.moedc_matvec_int4_workspace_bytes.restype = Z
     lib.moedc_test_set_wait_extra.argtypes = [ctypes.c_uint]
     lib.moedc_test_set_wait_extra.restype = None
     if path is None:
@@ -271,13 +273,17 @@ def moedc_unsort_grad(dy, lddy, sorted, dtype, T, H, K, row, src, topk_weights, 
                                     _stream(stream))
 
 
+def moedc_matvec_int4_workspace_bytes(x_rows: int, Kd: int) -> int:
+    return int(load().moedc_matvec_int4_workspace_bytes(x_rows, Kd))
+
+
 def moedc_matvec_int4(x, ldx, dtype, x_rows, Kd, wq, scales, scale_dtype, zeros, group, E, N,
-                      flags, offsets, counts, src, top_k, rows, out, dev_status,
-                      stream=None) -> int:
+                      flags, offsets, counts, src, top_k, rows, out, workspace, workspace_bytes,
+                      dev_status, stream=None) -> int:
     return load().moedc_matvec_int4(_p(x), ldx, dtype, x_rows, Kd, _p(wq), _p(scales),
                                     scale_dtype, _p(zeros), group, E, N, flags, _p(offsets),
-                                    _p(counts), _p(src), top_k, rows, _p(out), _p(dev_status),
-                                    _stream(stream))
+                                    _p(counts), _p(src), top_k, rows, _p(out), _p(workspace),
+                                    workspace_bytes, _p(dev_status), _stream(stream))
 
 
 # ---------------------------------------------------------------- conveniences
@@ -648,11 +654,13 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
                 zeros: torch.Tensor | None = None, offsets: torch.Tensor | None = None,
                 counts: torch.Tensor | None = None, src: torch.Tensor | None = None,
                 top_k: int = 1, swiglu: bool = False, status: torch.Tensor | None = None,
-                out: torch.Tensor | None = None) -> torch.Tensor:
+                out: torch.Tensor | None = None,
+                workspace: torch.Tensor | None = None) -> torch.Tensor:
     """out [R, N]: packed expert rows times 4-bit weights wq uint8 [E, N, Kd/2]
     ([N, Kd/2]: one linear layer) with scales [E, N, Kd/group]; swiglu: 2N
     weight rows, silu(gate) * up.  offsets and counts from sort(); src and
-    top_k read x in token order."""
+    top_k read x in token order.  workspace: moedc_matvec_int4_workspace_bytes
+    bytes, allocated here when None."""
     ld = _need_rows(x, "x")
     dtype = _lm_dtype(x, "x")
     if wq.dim() == 2:
@@ -687,7 +695,11 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
     _need_shape(out, (R, N), "out")
     if status is None:
         status = torch.zeros(1, dtype=torch.int32, device=x.device)
+    if workspace is None:
+        workspace = torch.empty(moedc_matvec_int4_workspace_bytes(x.shape[0], Kd),
+                                dtype=torch.uint8, device=x.device)
     _check(moedc_matvec_int4(x, ld, dtype, x.shape[0], Kd, wq, scales, _lm_dtype(scales, "scales"),
                              zeros, Kd // max(1, scales.shape[2]), E, N, SWIGLU if swiglu else 0,
-                             offsets, counts, src, top_k, R, out, status), "moedc_matvec_int4")
+                             offsets, counts, src, top_k, R, out, workspace, workspace.numel(),
+                             status), "moedc_matvec_int4")
     return out

@@ -165,3 +165,20 @@ def test_refusals():
                 lambda: moedc.matvec_int4(x, wq, s, out=torch.zeros(2, 15, dtype=torch.bfloat16).cuda())):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_clean():
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(3, 512, generator=g).to(torch.bfloat16).cuda()
+    wq, s, _ = _weights(g, 1, 70, 512, 64, False, torch.bfloat16)
+    want = moedc.matvec_int4(x, wq, s)
+    torch.cuda.synchronize()
+    status = torch.zeros(1, dtype=torch.int32).cuda()
+    moedc.load().moedc_test_set_wait_extra(1)
+    try:
+        moedc.matvec_int4(x, wq, s, status=status)
+        assert int(status) == moedc.ERR_TIMEOUT
+    finally:
+        moedc.load().moedc_test_set_wait_extra(0)
+    status.zero_()
+    assert torch.equal(moedc.matvec_int4(x, wq, s, status=status), want) and int(status) == 0

@@ -86,15 +86,21 @@ def test_sort_arguments(lib):
 
 def test_matvec_arguments(lib):
     def mv(x=F, ldx=256, dt=moedc.BF16, xr=4, Kd=256, wq=F, s=F, sdt=moedc.BF16, z=None, g=64,
-           E=2, N=16, flags=0, off=F, cnt=F, src=None, k=1, rows=4, out=F, st=F):
+           E=2, N=16, flags=0, off=F, cnt=F, src=None, k=1, rows=4, out=F, ws=F, wsb=1 << 20,
+           st=F):
         return lib.moedc_matvec_int4(x, ldx, dt, xr, Kd, wq, s, sdt, z, g, E, N, flags, off, cnt,
-                                     src, k, rows, out, st, None)
+                                     src, k, rows, out, ws, wsb, st, None)
 
     for bad in (dict(x=None), dict(ldx=255), dict(ldx=260), dict(dt=moedc.F32), dict(dt=1),
                 dict(xr=-1), dict(Kd=0), dict(Kd=288), dict(wq=None), dict(wq=P(264)),
                 dict(s=None), dict(s=ODD), dict(sdt=1), dict(g=16), dict(g=256), dict(g=0),
                 dict(E=0), dict(E=1025), dict(N=0), dict(flags=2), dict(off=None),
                 dict(cnt=None), dict(off=None, cnt=None), dict(src=F, k=0), dict(rows=-1),
-                dict(out=None), dict(out=ODD), dict(st=None), dict(x=P(264))):
+                dict(out=None), dict(out=ODD), dict(st=None), dict(x=P(264)), dict(ws=None),
+                dict(ws=P(264)), dict(wsb=5 * 576 - 1), dict(N=1 << 30, E=4)):
         assert mv(**bad) == moedc.ERR_ARG, bad
     assert mv(rows=0) == moedc.OK
+    # one record of 576 bytes per row and 256 channels, and a row of zeros
+    assert moedc.moedc_matvec_int4_workspace_bytes(4, 256) == 5 * 576
+    assert moedc.moedc_matvec_int4_workspace_bytes(1, 288) == 2 * 2 * 576
+    assert moedc.moedc_matvec_int4_workspace_bytes(-1, 256) == 0
