@@ -30,14 +30,25 @@ struct GateArgs {
 // (a NaN stays one)
 __device__ __forceinline__ float gate_logit(float l) { return l > FLT_MAX ? FLT_MAX : l; }
 
-// Order-preserving map of the selection key to unsigned; 0 for an expert that
-// cannot be chosen (logit or key NaN or -inf).  The +0 makes -0 tie with +0.
-__device__ __forceinline__ unsigned gate_key(float l, float b)
+// Order-preserving map to unsigned; 0 for what cannot be chosen (NaN or -inf).
+// The +0 makes -0 tie with +0.
+__device__ __forceinline__ unsigned gate_order(float key)
 {
-    const float key = l + b + 0.0f;
-    if (!(l > -INFINITY) || !(key > -INFINITY)) return 0u;
-    const unsigned u = __float_as_uint(key);
-    return u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+    const unsigned u = __float_as_uint(key + 0.0f);
+    const unsigned m = u ^ ((unsigned)((int)u >> 31) | 0x80000000u);
+    return key > -INFINITY ? m : 0u;
+}
+__device__ __forceinline__ float gate_unorder(unsigned m)
+{
+    return __uint_as_float(m & 0x80000000u ? m ^ 0x80000000u : ~m);
+}
+
+// The selection key of a logit and its bias (0 without one)
+template <bool BIAS> __device__ __forceinline__ unsigned gate_key(float l, float b)
+{
+    if (!BIAS) return gate_order(l);
+    const unsigned m = gate_order(l + b);
+    return l > -INFINITY ? m : 0u;
 }
 
 // s (1 - s) of s = sigmoid(l), without the cancellation of 1 - s
@@ -49,8 +60,18 @@ __device__ __forceinline__ float sigmoid_slope(float l)
 
 __device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
 
-// Lane i < K holds chosen expert i (e < 0: none): its p = w / scale, and the
-// sum S of the sigmoids over the chosen.  `den` and `top` are the softmax's
+// exp for the dense sums, x <= 0: 2^(x log2 e), the power by ex2.approx (results
+// below 2^-126 become 0).  Its relative error of |x| 2^-24 and some ulp is that of
+// x itself as a difference of two logits; expf takes four times the instructions.
+__device__ __forceinline__ float exp_fast(float x)
+{
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x * 1.4426950408889634f));
+    return y;
+}
+
+// Lane i < K holds chosen expert i (live: there is one): its p = w / scale, and
+// the sum S of the sigmoids over the chosen.  `den` and `top` are the softmax's
 // denominator and maximum over all experts, used when not renormalised.
 struct GateWeights {
     float p, total;
@@ -72,57 +93,146 @@ __device__ __forceinline__ GateWeights gate_weights(const GateArgs& a, bool live
         const float sum = warp_sum(ex);
         g.p = live ? ex / sum : 0.0f;
     } else {
-        g.p = live ? expf(l - top) / den : 0.0f;
+        g.p = live ? exp_fast(l - top) / den : 0.0f;
     }
     return g;
 }
 
-// N experts per lane: expert e = lane + 32 j
-template <typename T, int N>
+// A lane's experts: N of them, V neighbours to an access.  Value j holds expert
+//   (lane + 32 (j / V)) V + j % V.
+template <int V> __device__ __forceinline__ int gate_expert(int lane, int j)
+{
+    return (lane + kWarp * (j / V)) * V + j % V;
+}
+
+// The row's logits (-inf past E) and bias sums' keys.
+template <typename T, int N, int V, bool BIAS>
+__device__ __forceinline__ void gate_load(const GateArgs& a, const T* row, int lane, float (&l)[N],
+                                          unsigned (&key)[N])
+{
+#pragma unroll
+    for (int j = 0; j < N; j += V) {
+        const int e = gate_expert<V>(lane, j);
+        Pack<T, V> v;
+        Pack<float, V> b;
+        const bool in = e < a.E;
+        if (in) v = *reinterpret_cast<const Pack<T, V>*>(row + e);
+        if (BIAS && in) {
+#pragma unroll
+            for (int c = 0; c < V; ++c) b.v[c] = __ldg(a.bias + e + c);
+        }
+#pragma unroll
+        for (int c = 0; c < V; ++c) {
+            const float raw = in ? to_f32(v.v[c]) : -INFINITY;
+            key[j + c] = gate_key<BIAS>(raw, BIAS && in ? b.v[c] : 0.0f);
+            l[j + c] = fminf(raw, FLT_MAX);       // a NaN has key 0
+        }
+    }
+}
+
+// Softmax over the experts that can be chosen: the maximum, each one's
+// exponential in l's place, and their sum.
+template <int N, bool BIAS>
+__device__ __forceinline__ void gate_softmax(float (&l)[N], const unsigned (&key)[N], float& top,
+                                             float& den)
+{
+    unsigned m = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) m = max(m, BIAS ? (key[j] ? gate_order(l[j]) : 0u) : key[j]);
+    m = __reduce_max_sync(0xffffffffu, m);
+    top = m ? fminf(gate_unorder(m), FLT_MAX) : 0.0f;
+    den = 0.0f;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const float e = exp_fast(l[j] - top);
+        l[j] = key[j] ? e : 0.0f;
+        den += l[j];
+    }
+    den = warp_sum(den);
+}
+
+// The K largest keys of the warp in (key descending, expert ascending) order,
+// lane i getting the i-th's expert, -1 where there is none.
+//
+// The K-th largest of the 32 lanes' own maxima bounds the K-th largest key from
+// below, so only the keys at or above it (some ten of 256) are candidates; they
+// are packed into a slot each and ranked against one another.  Where more than
+// 32 keys tie at the bound, the K maxima are taken one after another instead.
+template <int N, int V>
+__device__ __forceinline__ int gate_choose(unsigned (&key)[N], int K, int lane, unsigned long long* s_cand)
+{
+    unsigned mine = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) mine = max(mine, key[j]);
+    unsigned bound = 0;
+    for (int i = 0; i < K; ++i) {
+        bound = __reduce_max_sync(0xffffffffu, mine);
+        if (mine == bound) mine = 0;
+    }
+    bound = max(bound, 1u);            // 0 cannot be chosen
+    int count = 0;
+#pragma unroll
+    for (int j = 0; j < N; ++j) {
+        const bool in = key[j] >= bound;
+        const unsigned who = __ballot_sync(0xffffffffu, in);
+        const int at = count + __popc(who & lanemask_lt());
+        if (in && at < kWarp)
+            s_cand[at] = (unsigned long long)key[j] << 32 | (unsigned)~gate_expert<V>(lane, j);
+        count += __popc(who);
+    }
+    int chosen = -1;
+    if (count <= kWarp) {
+        if (lane == 0 && count < kWarp) s_cand[count] = 0;     // an odd count's other half
+        __syncwarp();
+        const unsigned long long c = lane < count ? s_cand[lane] : 0;
+        int rank = 0;
+        for (int i = 0; i < count; i += 2) {
+            const ulonglong2 o = *reinterpret_cast<const ulonglong2*>(s_cand + i);
+            rank += (o.x > c) + (o.y > c);
+        }
+        __syncwarp();
+        // the candidate of rank i to lane i
+        if (lane < count) s_cand[rank] = c;
+        __syncwarp();
+        if (lane < min(count, K)) chosen = (int)~(unsigned)s_cand[lane];
+        __syncwarp();
+        return chosen;
+    }
+    for (int i = 0; i < K; ++i) {
+        unsigned best = 0;
+#pragma unroll
+        for (int j = 0; j < N; ++j) best = max(best, key[j]);
+        const unsigned m = __reduce_max_sync(0xffffffffu, best);
+        if (m == 0) break;
+        int e = INT_MAX;
+#pragma unroll
+        for (int j = N - 1; j >= 0; --j)
+            if (key[j] == m) e = gate_expert<V>(lane, j);
+        const int win = __reduce_min_sync(0xffffffffu, e);
+#pragma unroll
+        for (int j = 0; j < N; ++j)
+            if (gate_expert<V>(lane, j) == win) key[j] = 0;
+        if (lane == i) chosen = win;
+    }
+    return chosen;
+}
+
+template <typename T, int N, int V, bool BIAS>
 __global__ void __launch_bounds__(kGateWarps * kWarp)
 gate_kernel(GateArgs a, int32_t* __restrict__ topk_idx, float* __restrict__ topk_weights)
 {
+    __shared__ __align__(16) unsigned long long s_cand[kGateWarps][kWarp];
     pdl_enter();
-    const int lane = threadIdx.x % kWarp;
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     const int64_t nwarps = (int64_t)gridDim.x * kGateWarps;
-    for (int64_t t = (int64_t)blockIdx.x * kGateWarps + threadIdx.x / kWarp; t < a.T; t += nwarps) {
+    for (int64_t t = (int64_t)blockIdx.x * kGateWarps + warp; t < a.T; t += nwarps) {
         const T* row = static_cast<const T*>(a.logits) + t * a.ld;
         float l[N];
         unsigned key[N];
-        float top = -FLT_MAX, den = 0.0f;
-#pragma unroll
-        for (int j = 0; j < N; ++j) {
-            const int e = lane + kWarp * j;
-            l[j] = e < a.E ? gate_logit(to_f32(row[e])) : -INFINITY;
-            key[j] = gate_key(l[j], a.bias && e < a.E ? __ldg(a.bias + e) : 0.0f);
-        }
-        if (!a.sigmoid && !a.normalize) {
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (key[j]) top = fmaxf(top, l[j]);
-            top = warp_max(top);
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (key[j]) den += expf(l[j] - top);
-            den = warp_sum(den);
-        }
-        int mine = -1;   // lane i: the i-th chosen expert
-        for (int i = 0; i < a.K; ++i) {
-            unsigned best = 0;
-#pragma unroll
-            for (int j = 0; j < N; ++j) best = max(best, key[j]);
-            const unsigned m = __reduce_max_sync(0xffffffffu, best);
-            if (m == 0) break;
-            int e = INT_MAX;
-#pragma unroll
-            for (int j = N - 1; j >= 0; --j)
-                if (key[j] == m) e = lane + kWarp * j;
-            const int win = __reduce_min_sync(0xffffffffu, e);
-#pragma unroll
-            for (int j = 0; j < N; ++j)
-                if (lane + kWarp * j == win) key[j] = 0;
-            if (lane == i) mine = win;
-        }
+        gate_load<T, N, V, BIAS>(a, row, lane, l, key);
+        float top = 0.0f, den = 1.0f;
+        if (!a.sigmoid && !a.normalize) gate_softmax<N, BIAS>(l, key, top, den);
+        const int mine = gate_choose<N, V>(key, a.K, lane, s_cand[warp]);
         const float lc = mine >= 0 ? gate_logit(to_f32(row[mine])) : 0.0f;
         const GateWeights g = gate_weights(a, mine >= 0, lc, top, den);
         if (lane < a.K) {
@@ -132,43 +242,37 @@ gate_kernel(GateArgs a, int32_t* __restrict__ topk_idx, float* __restrict__ topk
     }
 }
 
-template <typename T>
+// DENSE: the softmax over all experts, whose gradient reaches every one.
+template <typename T, int N, int V, bool BIAS, bool DENSE>
 __global__ void __launch_bounds__(kGateWarps * kWarp)
 gate_grad_kernel(GateArgs a, const int32_t* __restrict__ topk_idx,
                  const float* __restrict__ dweights, T* __restrict__ dlogits)
 {
-    extern __shared__ float s_rows[];   // [kGateWarps][E]
-    pdl_enter();
+    // what the chosen experts get; zero for all others, from row to row
+    __shared__ __align__(16) float s_own[kGateWarps][N * kWarp];
     const int lane = threadIdx.x % kWarp;
-    float* acc = s_rows + (threadIdx.x / kWarp) * a.E;
+    float* add = s_own[threadIdx.x / kWarp];
+    for (int c = lane; c < N * kWarp; c += kWarp) add[c] = 0.0f;
+    __syncwarp();
+    pdl_enter();
     const int64_t nwarps = (int64_t)gridDim.x * kGateWarps;
     for (int64_t t = (int64_t)blockIdx.x * kGateWarps + threadIdx.x / kWarp; t < a.T; t += nwarps) {
         const T* row = static_cast<const T*>(a.logits) + t * a.ld;
-        int e = -1;
-        float d = 0.0f, l = 0.0f;
-        if (lane < a.K) {
-            e = topk_idx[t * a.K + lane];
-            if (e >= a.E || e < 0) e = -1;
-            if (e >= 0) {
-                l = gate_logit(to_f32(row[e]));
-                if (!gate_key(l, a.bias ? a.bias[e] : 0.0f)) e = -1;
-            }
-            if (e >= 0) d = dweights[t * a.K + lane];
+        float v[N];
+        unsigned key[N];
+        float top = 0.0f, den = 1.0f;
+        int e = lane < a.K ? topk_idx[t * a.K + lane] : -1;
+        float d = lane < a.K ? dweights[t * a.K + lane] : 0.0f;
+        if (DENSE) gate_load<T, N, V, BIAS>(a, row, lane, v, key);
+        float l = 0.0f;
+        if (e >= 0 && e < a.E) {
+            l = gate_logit(to_f32(row[e]));
+            if (!gate_key<BIAS>(l, BIAS ? __ldg(a.bias + e) : 0.0f)) e = -1;
+        } else {
+            e = -1;
         }
-        float top = -FLT_MAX, den = 0.0f;
-        const bool dense = !a.sigmoid && !a.normalize;
-        if (dense) {
-            for (int c = lane; c < a.E; c += kWarp) {
-                const float v = gate_logit(to_f32(row[c]));
-                if (gate_key(v, a.bias ? a.bias[c] : 0.0f)) top = fmaxf(top, v);
-            }
-            top = warp_max(top);
-            for (int c = lane; c < a.E; c += kWarp) {
-                const float v = gate_logit(to_f32(row[c]));
-                if (gate_key(v, a.bias ? a.bias[c] : 0.0f)) den += expf(v - top);
-            }
-            den = warp_sum(den);
-        }
+        if (e < 0) d = 0.0f;
+        if (DENSE) gate_softmax<N, BIAS>(v, key, top, den);   // v: the exponentials
         const GateWeights g = gate_weights(a, e >= 0, l, top, den);
         const float dot = (a.sigmoid && !a.normalize) ? 0.0f : warp_sum(g.p * d);
         float own;
@@ -176,21 +280,25 @@ gate_grad_kernel(GateArgs a, const int32_t* __restrict__ topk_idx,
             own = a.normalize ? (g.total > 0.0f ? sigmoid_slope(l) / g.total * (d - dot) : 0.0f)
                               : sigmoid_slope(l) * d;
         else
-            own = dense ? g.p * d : g.p * (d - dot);
+            own = DENSE ? g.p * d : g.p * (d - dot);
+        if (e >= 0) atomicAdd(add + e, own * a.scale);   // distinct experts: one addition each
         __syncwarp();
-        for (int c = lane; c < a.E; c += kWarp) {
-            float v = 0.0f;
-            if (dense) {
-                const float lg = gate_logit(to_f32(row[c]));
-                if (gate_key(lg, a.bias ? a.bias[c] : 0.0f)) v = -expf(lg - top) / den * dot;
-            }
-            acc[c] = v;
+        // a token that chose nothing has den = 0 and no gradient
+        const float all = DENSE && den > 0.0f ? -dot * a.scale / den : 0.0f;
+#pragma unroll
+        for (int j = 0; j < N; j += V) {
+            const int c0 = gate_expert<V>(lane, j);
+            if (c0 >= a.E) break;
+            const Pack<float, V> own_v = *reinterpret_cast<const Pack<float, V>*>(add + c0);
+            Pack<T, V> o;
+#pragma unroll
+            for (int c = 0; c < V; ++c)
+                o.v[c] = from_f32<T>(DENSE ? fmaf(v[j + c], all, own_v.v[c]) : own_v.v[c]);
+            *reinterpret_cast<Pack<T, V>*>(dlogits + t * a.E + c0) = o;
         }
         __syncwarp();
-        if (e >= 0) atomicAdd(acc + e, own);   // distinct experts: one addition each
+        if (e >= 0) add[e] = 0.0f;
         __syncwarp();
-        for (int c = lane; c < a.E; c += kWarp)
-            dlogits[t * a.E + c] = from_f32<T>(acc[c] * a.scale);
     }
 }
 
@@ -209,44 +317,70 @@ bool gate_args_ok(const void* logits, int64_t ld, int dtype, int T, int E, int K
            aligned(logits, lm_dtype_size(dtype)) && aligned(bias, 4) && (T == 0 || logits);
 }
 
-int gate_blocks(const void* kernel, size_t smem, int T)
+template <typename... KArgs, typename... Args>
+int launch_gate(void (*kernel)(KArgs...), int T, cudaStream_t stream, Args... args)
 {
     const int64_t want = ((int64_t)T + moedc::kGateWarps - 1) / moedc::kGateWarps;
-    const int64_t most = resident_blocks(kernel, moedc::kGateWarps * moedc::kWarp, smem);
-    return (int)(want < most ? want : most);
+    const int64_t most = resident_blocks((const void*)kernel, moedc::kGateWarps * moedc::kWarp, 0);
+    clear_stale_error();
+    launch(kernel, (int)(want < most ? want : most), moedc::kGateWarps * moedc::kWarp, 0, stream, args...);
+    return launch_status();
+}
+
+// Four neighbouring experts to an access where rows keep them aligned, one elsewhere.
+template <typename T> bool gate_wide(const moedc::GateArgs& a, const void* dlogits)
+{
+    return a.E % 4 == 0 && a.ld % 4 == 0 && aligned(a.logits, 4 * sizeof(T)) &&
+           aligned(dlogits, 4 * sizeof(T));
 }
 
 template <typename T, int N>
-int launch_gate(const moedc::GateArgs& a, int32_t* idx, float* w, cudaStream_t stream)
+int run_gate(const moedc::GateArgs& a, int32_t* idx, float* w, cudaStream_t stream)
 {
-    auto* k = moedc::gate_kernel<T, N>;
-    const int blocks = gate_blocks((const void*)k, 0, a.T);
-    clear_stale_error();
-    launch(k, blocks, moedc::kGateWarps * moedc::kWarp, 0, stream, a, idx, w);
-    return launch_status();
+    const bool wide = gate_wide<T>(a, nullptr);
+    if (a.bias)
+        return wide ? launch_gate(moedc::gate_kernel<T, N, 4, true>, a.T, stream, a, idx, w)
+                    : launch_gate(moedc::gate_kernel<T, N, 1, true>, a.T, stream, a, idx, w);
+    return wide ? launch_gate(moedc::gate_kernel<T, N, 4, false>, a.T, stream, a, idx, w)
+                : launch_gate(moedc::gate_kernel<T, N, 1, false>, a.T, stream, a, idx, w);
+}
+
+template <typename T, int N, int V>
+int run_gate_grad(const moedc::GateArgs& a, const int32_t* idx, const float* dw, void* dl, cudaStream_t stream)
+{
+    T* out = static_cast<T*>(dl);
+    const bool dense = !a.sigmoid && !a.normalize;
+    if (a.bias)
+        return dense ? launch_gate(moedc::gate_grad_kernel<T, N, V, true, true>, a.T, stream, a, idx, dw, out)
+                     : launch_gate(moedc::gate_grad_kernel<T, N, V, true, false>, a.T, stream, a, idx, dw, out);
+    return dense ? launch_gate(moedc::gate_grad_kernel<T, N, V, false, true>, a.T, stream, a, idx, dw, out)
+                 : launch_gate(moedc::gate_grad_kernel<T, N, V, false, false>, a.T, stream, a, idx, dw, out);
+}
+
+// Experts of a lane: as many as E needs, in steps that keep the registers few.
+#define MOEDC_GATE_N(E, CALL)        \
+    (E <= 128   ? CALL(4)            \
+     : E <= 256 ? CALL(8)            \
+     : E <= 384 ? CALL(12)           \
+     : E <= 512 ? CALL(16)           \
+                : CALL(32))
+
+template <typename T>
+int gate_by_size(const moedc::GateArgs& a, int32_t* idx, float* w, cudaStream_t stream)
+{
+#define MOEDC_CALL(N) run_gate<T, N>(a, idx, w, stream)
+    return MOEDC_GATE_N(a.E, MOEDC_CALL);
+#undef MOEDC_CALL
 }
 
 template <typename T>
-int launch_gate_n(const moedc::GateArgs& a, int32_t* idx, float* w, cudaStream_t stream)
+int gate_grad_by_size(const moedc::GateArgs& a, const int32_t* idx, const float* dw, void* dl, cudaStream_t stream)
 {
-    if (a.E <= 64) return launch_gate<T, 2>(a, idx, w, stream);
-    if (a.E <= 128) return launch_gate<T, 4>(a, idx, w, stream);
-    if (a.E <= 256) return launch_gate<T, 8>(a, idx, w, stream);
-    if (a.E <= 512) return launch_gate<T, 16>(a, idx, w, stream);
-    return launch_gate<T, 32>(a, idx, w, stream);
-}
-
-template <typename T>
-int launch_gate_grad(const moedc::GateArgs& a, const int32_t* idx, const float* dw, void* dl,
-                     cudaStream_t stream)
-{
-    auto* k = moedc::gate_grad_kernel<T>;
-    const size_t smem = (size_t)moedc::kGateWarps * a.E * sizeof(float);
-    const int blocks = gate_blocks((const void*)k, smem, a.T);
-    clear_stale_error();
-    launch(k, blocks, moedc::kGateWarps * moedc::kWarp, smem, stream, a, idx, dw,
-           static_cast<T*>(dl));
-    return launch_status();
+    const bool wide = gate_wide<T>(a, dl);
+#define MOEDC_CALL(N) \
+    (wide ? run_gate_grad<T, N, 4>(a, idx, dw, dl, stream) : run_gate_grad<T, N, 1>(a, idx, dw, dl, stream))
+    return MOEDC_GATE_N(a.E, MOEDC_CALL);
+#undef MOEDC_CALL
 }
 
 }  // namespace
@@ -263,9 +397,9 @@ extern "C" int moedc_gate(const void* logits, int64_t ld_logits, int dtype, int 
     if (!topk_idx || !topk_weights) return MOEDC_ERR_ARG;
     const moedc::GateArgs a{logits, ld_logits, T, E, K, bias, (flags & MOEDC_GATE_SIGMOID) != 0,
                             (flags & MOEDC_GATE_NORMALIZE) != 0, scale};
-    return dtype == MOEDC_F32   ? launch_gate_n<float>(a, topk_idx, topk_weights, stream)
-           : dtype == MOEDC_F16 ? launch_gate_n<__half>(a, topk_idx, topk_weights, stream)
-                                : launch_gate_n<__nv_bfloat16>(a, topk_idx, topk_weights, stream);
+    return dtype == MOEDC_F32   ? gate_by_size<float>(a, topk_idx, topk_weights, stream)
+           : dtype == MOEDC_F16 ? gate_by_size<__half>(a, topk_idx, topk_weights, stream)
+                                : gate_by_size<__nv_bfloat16>(a, topk_idx, topk_weights, stream);
 }
 
 extern "C" int moedc_gate_grad(const void* logits, int64_t ld_logits, int dtype, int T, int E,
@@ -281,8 +415,8 @@ extern "C" int moedc_gate_grad(const void* logits, int64_t ld_logits, int dtype,
     if (!topk_idx || !dweights || !dlogits) return MOEDC_ERR_ARG;
     const moedc::GateArgs a{logits, ld_logits, T, E, K, bias, (flags & MOEDC_GATE_SIGMOID) != 0,
                             (flags & MOEDC_GATE_NORMALIZE) != 0, scale};
-    return dtype == MOEDC_F32   ? launch_gate_grad<float>(a, topk_idx, dweights, dlogits, stream)
-           : dtype == MOEDC_F16 ? launch_gate_grad<__half>(a, topk_idx, dweights, dlogits, stream)
-                                : launch_gate_grad<__nv_bfloat16>(a, topk_idx, dweights, dlogits,
+    return dtype == MOEDC_F32   ? gate_grad_by_size<float>(a, topk_idx, dweights, dlogits, stream)
+           : dtype == MOEDC_F16 ? gate_grad_by_size<__half>(a, topk_idx, dweights, dlogits, stream)
+                                : gate_grad_by_size<__nv_bfloat16>(a, topk_idx, dweights, dlogits,
                                                                   stream);
 }
