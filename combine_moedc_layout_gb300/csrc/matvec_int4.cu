@@ -113,6 +113,7 @@ __device__ __noinline__ bool mbar_wait_slow(uint64_t* b, int parity, volatile in
     // the timer is read only once the wait is a long one: reading it takes longer than
     // most waits
     unsigned long long t0 = 0;
+    if (*abort) return false;
     for (int i = 0; ; ++i) {
         if (mbar_try(b, parity)) return true;
         if (i % 1024 != 1023) continue;
@@ -554,8 +555,9 @@ __device__ __forceinline__ void mv_consume(const MatvecArgs& a, MvWarp& w, MvRin
         next.load(a, w.at0, w.at1, q, groups, w.whole);
         mbar_wait(full + ring.slot, ring.phase, abort);
         const uint32_t at = w.base + ring.slot * a.stage_bytes;
+        // a part without channels left in the last stage has no records of x there either
         if (left >= kMvChunk) mv_stage<GROUP, NT, true>(at + w.ow, at + w.ox, at + w.oc, now, zeros, 8, acc);
-        else mv_stage<GROUP, NT, false>(at + w.ow, at + w.ox, at + w.oc, now, zeros, left / 32, acc);
+        else if (left > 0) mv_stage<GROUP, NT, false>(at + w.ow, at + w.ox, at + w.oc, now, zeros, left / 32, acc);
         __syncwarp();
         if (threadIdx.x % kWarp == 0) mbar_arrive(empty + ring.slot);
         ring.next(a.stages);

@@ -60,6 +60,45 @@ def test_swiglu_and_zero_points(group, zeros, dtype):
     _check(50, 3, 2, 24, group * 9, group, DTYPES[dtype], swiglu=False, zeros=zeros, seed=1)
 
 
+# enough 128-row tiles of weights to give every SM one: experts of few and of many rows,
+# odd output counts, channels that end inside a stage of 256
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("T,E,K,N,mult,swiglu,zeros", [
+    (40, 160, 2, 40, 2, False, False), (64, 160, 4, 33, 3, True, True),
+    (30, 20, 8, 1100, 5, False, True), (70, 12, 8, 900, 1, True, False),
+    (100, 20, 12, 1030, 4, False, False), (260, 16, 4, 1300, 2, False, True)])
+def test_many_tiles(T, E, K, N, mult, swiglu, zeros, group, dtype):
+    _check(T, E, K, N, group * mult, group, DTYPES[dtype], swiglu=swiglu, zeros=zeros, align=4,
+           mask=0.05)
+
+
+@pytest.mark.parametrize("sdtype", list(DTYPES))
+@pytest.mark.parametrize("group,mult", [(32, 11), (64, 7), (128, 5)])
+def test_many_tiles_scale_types(group, mult, sdtype):
+    _check(50, 160, 4, 60, group * mult, group, torch.bfloat16, zeros=True, sdtype=DTYPES[sdtype])
+
+
+def test_many_tiles_at_one_expert():
+    idx = torch.full((75, 1), 3, dtype=torch.int32)
+    _check(75, 160, 1, 70, 512, 64, torch.float16, idx=idx)
+    _check(21, 1, 1, 20000, 512, 128, torch.bfloat16, seed=2)
+
+
+@pytest.mark.parametrize("Kd", [128, 512, 640, 1280])
+def test_nothing_of_an_earlier_call_comes_through(Kd):
+    """Channels that end inside the last stage, after a call that left NaN
+    everywhere in the SMs' shared memory."""
+    g = torch.Generator().manual_seed(6)
+    wq, s, _ = _weights(g, 8, 4096, 2048, 64, False, torch.bfloat16)
+    bad = torch.full((64, 2048), float("nan"), dtype=torch.bfloat16).cuda()
+    idx = torch.arange(64, dtype=torch.int32).reshape(64, 1) % 8
+    m = moedc.sort(None, idx.cuda(), 8)
+    out = moedc.matvec_int4(bad, wq, s, offsets=m.offsets, counts=m.counts, src=m.src)
+    assert torch.isnan(out).all()
+    _check(5, 4, 2, 40, Kd, 64, torch.bfloat16, zeros=True)
+
+
 @pytest.mark.parametrize("sdtype", list(DTYPES))
 def test_scale_types(sdtype):
     _check(5, 4, 2, 40, 512, 64, torch.bfloat16, zeros=True, sdtype=DTYPES[sdtype])
