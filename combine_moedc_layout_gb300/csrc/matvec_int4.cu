@@ -32,6 +32,7 @@
 // every weight a 2-byte store and a 2-byte read on the way: at the HBM rate
 // 93 + 93 bytes per SM and clock, more than shared memory moves (128).
 #include <climits>
+#include <cmath>
 #include <mutex>
 #include <type_traits>
 
@@ -142,24 +143,22 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
           "f"(c[3]));
 }
 
-template <typename V> __device__ __forceinline__ V lds(uint32_t at);
-template <> __device__ __forceinline__ uint32_t lds<uint32_t>(uint32_t at)
+// plain loads, so that the compiler may order them between the waits as it likes
+template <typename V> __device__ __forceinline__ V lds(const uint8_t* at) { return *reinterpret_cast<const V*>(at); }
+
+// N neighbouring floats, 16 bytes at most at a time
+template <int N> __device__ __forceinline__ void lds_run(const uint8_t* at, float (&v)[N])
 {
-    uint32_t v;
-    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
-    return v;
-}
-template <> __device__ __forceinline__ uint4 lds<uint4>(uint32_t at)
-{
-    uint4 v;
-    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
-    return v;
-}
-template <> __device__ __forceinline__ float lds<float>(uint32_t at)
-{
-    float v;
-    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(at));
-    return v;
+    if constexpr (N == 2) {
+        const float2 r = lds<float2>(at);
+        v[0] = r.x, v[1] = r.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < N; i += 4) {
+            const float4 r = lds<float4>(at + i * 4);
+            v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
+        }
+    }
 }
 
 // Scales and zero points of one warp's rows g and g + 8 for one stage, in
@@ -215,30 +214,39 @@ template <int GROUP, typename S> struct MvScales {
             for (int i = 0; i < n; ++i) z[i / 4] |= (uint32_t)__ldg(p + min(i, have - 1)) << (8 * (i % 4));
         }
     }
-    // rows begin at element at0 and at1; groups past the last one read it again
-    __device__ __forceinline__ void load(const MatvecArgs& a, int64_t at0, int64_t at1, int group0,
-                                         int groups, bool whole)
+    // Of a unit's two rows: where their scales and zero points begin.  Without zero
+    // points z stays 8.
+    struct Rows {
+        const S* s[2];
+        const uint8_t* z[2];
+    };
+    __device__ __forceinline__ void clear()
     {
-        const S* sp = static_cast<const S*>(a.scales);
-        const int q = min(group0, whole ? groups - n : groups - 1), have = groups - q;
-        load_row(s[0], sp + at0 + q, whole, have);
-        load_row(s[1], sp + at1 + q, whole, have);
-        if (a.zeros) {
-            load_zeros(z[0], a.zeros + at0 + q, whole, have);
-            load_zeros(z[1], a.zeros + at1 + q, whole, have);
+#pragma unroll
+        for (int r = 0; r < 2; ++r)
+#pragma unroll
+            for (int i = 0; i < zwords; ++i) z[r][i] = 0x08080808u;
+    }
+    // the groups from q on; `have` of them exist (all, where they come as one load)
+    __device__ __forceinline__ void load(const Rows& rows, int q, int have, bool whole, bool zeros)
+    {
+        load_row(s[0], rows.s[0] + q, whole, have);
+        load_row(s[1], rows.s[1] + q, whole, have);
+        if (zeros) {
+            load_zeros(z[0], rows.z[0] + q, whole, have);
+            load_zeros(z[1], rows.z[1] + q, whole, have);
         }
     }
-    // times 2^12: x's factor carries the rest of the weights' 2^24
     __device__ __forceinline__ float scale(int row, int q) const
     {
         if constexpr (sizeof(S) == 4) {
-            return __uint_as_float(s[row][q]) * 4096.0f;
+            return __uint_as_float(s[row][q]);
         } else {
             const uint32_t w = s[row][q / 2];
             if constexpr (std::is_same<S, __nv_bfloat16>::value)
-                return __uint_as_float(q % 2 ? w & 0xffff0000u : w << 16) * 4096.0f;
+                return __uint_as_float(q % 2 ? w & 0xffff0000u : w << 16);
             else
-                return __half2float(__ushort_as_half((unsigned short)(q % 2 ? w >> 16 : w & 0xffffu))) * 4096.0f;
+                return __half2float(__ushort_as_half((unsigned short)(q % 2 ? w >> 16 : w & 0xffffu)));
         }
     }
     // minus the zero point: 2^23 + z is a binary32 number whose low bits are z
@@ -265,29 +273,34 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b)
 constexpr bool mv_subtract(int group, int nt) { return 8 * (group / 32) < 6 * nt; }
 
 // One stage of one warp: its 16 weight rows x 256 channels with 8 NT rows of x.
-//   w    address of row g at word t (128 bytes a row, 16-byte pieces permuted by the
+//   w    place of row g at word t (128 bytes a row, 16-byte pieces permuted by the
 //        row's low three bits); the warp's other eight rows lie kMvW / 2 further
-//   x    address of row g's record at its words t
-//   c    address of the sums of x row 2t
+//   x    place of row g's record at its words t
+//   c    place of the sums of x row 2t
 template <int GROUP, int NT, bool FULL, typename S>
-__device__ __forceinline__ void mv_stage(uint32_t w, uint32_t x, uint32_t c,
-                                         const MvScales<GROUP, S>& sz, bool zeros, int steps,
-                                         float (&acc)[NT][4])
+__device__ __forceinline__ void mv_stage(const uint8_t* st, uint32_t w, uint32_t x, uint32_t c,
+                                         const MvScales<GROUP, S>& sz, int steps, float (&acc)[NT][4])
 {
     constexpr int kPer = GROUP / 32;       // 32-channel steps of a group
+    constexpr int kGroups = kMvChunk / GROUP;
     constexpr bool kSub = mv_subtract(GROUP, NT);
     const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     float sum[NT][4];
+    // the sums of x rows 2t and 2t + 1, all groups at once
+    float u[NT][kGroups], v[NT][kGroups];
+    if (!kSub) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+        for (int i = 0; i < NT; ++i) {
+            lds_run<kGroups>(st + c + i * 8 * kMvRecord, u[i]);
+            lds_run<kGroups>(st + c + i * 8 * kMvRecord + kMvRecord, v[i]);
+        }
+    }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) sum[i][j] = 0.0f;
-#pragma unroll
-    for (int q = 0; q < kMvChunk / GROUP; ++q) {
+    for (int q = 0; q < kGroups; ++q) {
         if (!FULL && q * kPer >= steps) break;
         float tmp[NT][4];
-        uint32_t za = 0x00080008u, zb = 0x00080008u;
-        if (kSub && zeros) {
+        uint32_t za = 0, zb = 0;
+        if (kSub) {
             za = sz.zero_f16(0, q);
             zb = sz.zero_f16(1, q);
         }
@@ -295,7 +308,7 @@ __device__ __forceinline__ void mv_stage(uint32_t w, uint32_t x, uint32_t c,
         for (int p = 0; p < kPer; ++p) {
             const int k = q * kPer + p;
             const uint32_t at = w ^ (k << 4);
-            const uint32_t a = lds<uint32_t>(at), b = lds<uint32_t>(at + kMvW / 2);
+            const uint32_t a = lds<uint32_t>(st + at), b = lds<uint32_t>(st + at + kMvW / 2);
             constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
             uint32_t m[8] = {a & lo, b & lo, a & hi, b & hi, (a >> 8) & lo, (b >> 8) & lo, (a >> 8) & hi, (b >> 8) & hi};
             if (kSub) {
@@ -305,43 +318,38 @@ __device__ __forceinline__ void mv_stage(uint32_t w, uint32_t x, uint32_t c,
             }
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
-                const uint4 v = lds<uint4>(x + k * 64 + i * 8 * kMvRecord);
-                if (p == 0) mma_f16(tmp[i], m[0], m[1], m[2], m[3], v.x, v.y, none);
-                else mma_f16(tmp[i], m[0], m[1], m[2], m[3], v.x, v.y, tmp[i]);
-                mma_f16(tmp[i], m[4], m[5], m[6], m[7], v.z, v.w, tmp[i]);
+                const uint4 r = lds<uint4>(st + x + k * 64 + i * 8 * kMvRecord);
+                if (p == 0) mma_f16(tmp[i], m[0], m[1], m[2], m[3], r.x, r.y, none);
+                else mma_f16(tmp[i], m[0], m[1], m[2], m[3], r.x, r.y, tmp[i]);
+                mma_f16(tmp[i], m[4], m[5], m[6], m[7], r.z, r.w, tmp[i]);
             }
         }
         const float s0 = sz.scale(0, q), s1 = sz.scale(1, q);
-        float z0 = -8.0f, z1 = -8.0f;
-        if (!kSub && zeros) {
-            z0 = sz.minus_zero(0, q);
-            z1 = sz.minus_zero(1, q);
-        }
+        const float z0 = kSub ? 0.0f : sz.minus_zero(0, q), z1 = kSub ? 0.0f : sz.minus_zero(1, q);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
+            float (&d)[4] = tmp[i];
             if (!kSub) {
-                const float u = lds<float>(c + q * 4 + i * 8 * kMvRecord);
-                const float v = lds<float>(c + q * 4 + i * 8 * kMvRecord + kMvRecord);
-                tmp[i][0] = fmaf(z0, u, tmp[i][0]);
-                tmp[i][1] = fmaf(z0, v, tmp[i][1]);
-                tmp[i][2] = fmaf(z1, u, tmp[i][2]);
-                tmp[i][3] = fmaf(z1, v, tmp[i][3]);
+                d[0] = fmaf(z0, u[i][q], d[0]);
+                d[1] = fmaf(z0, v[i][q], d[1]);
+                d[2] = fmaf(z1, u[i][q], d[2]);
+                d[3] = fmaf(z1, v[i][q], d[3]);
             }
-            sum[i][0] = fmaf(s0, tmp[i][0], sum[i][0]);
-            sum[i][1] = fmaf(s0, tmp[i][1], sum[i][1]);
-            sum[i][2] = fmaf(s1, tmp[i][2], sum[i][2]);
-            sum[i][3] = fmaf(s1, tmp[i][3], sum[i][3]);
+            sum[i][0] = q ? fmaf(s0, d[0], sum[i][0]) : s0 * d[0];
+            sum[i][1] = q ? fmaf(s0, d[1], sum[i][1]) : s0 * d[1];
+            sum[i][2] = q ? fmaf(s1, d[2], sum[i][2]) : s1 * d[2];
+            sum[i][3] = q ? fmaf(s1, d[3], sum[i][3]) : s1 * d[3];
         }
     }
-    // the stage's factor of x
+    // the stage's factor of x, and the rest of the weights' 2^24
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const float u = lds<float>(c + 32 + i * 8 * kMvRecord);
-        const float v = lds<float>(c + 32 + i * 8 * kMvRecord + kMvRecord);
-        acc[i][0] = fmaf(u, sum[i][0], acc[i][0]);
-        acc[i][1] = fmaf(v, sum[i][1], acc[i][1]);
-        acc[i][2] = fmaf(u, sum[i][2], acc[i][2]);
-        acc[i][3] = fmaf(v, sum[i][3], acc[i][3]);
+        const float fu = lds<float>(st + c + 32 + i * 8 * kMvRecord);
+        const float fv = lds<float>(st + c + 32 + i * 8 * kMvRecord + kMvRecord);
+        acc[i][0] = fmaf(fu, 4096.0f * sum[i][0], acc[i][0]);
+        acc[i][1] = fmaf(fv, 4096.0f * sum[i][1], acc[i][1]);
+        acc[i][2] = fmaf(fu, 4096.0f * sum[i][2], acc[i][2]);
+        acc[i][3] = fmaf(fv, 4096.0f * sum[i][3], acc[i][3]);
     }
 }
 
@@ -513,51 +521,55 @@ matvec_x_kernel(const T* __restrict__ x, int64_t ldx, int x_rows, int Kd, int gr
 
 // What a consumer warp carries through its units.
 struct MvWarp {
-    uint32_t base, ow, ox, oc;     // shared-memory offsets: weights, x, sums of x
+    uint32_t ow, ox, oc;           // offsets in a stage: weights, x, sums of x
     int part, row, half;
-    int64_t at0, at1;              // first scale of the unit's two rows
     bool whole;                    // a row's groups of a stage are one aligned load
 };
 
-// First scales of the warp's two rows of a unit; rows past the last read the last
-// one's, and nothing uses them.
-__device__ __forceinline__ void mv_rows(const MatvecArgs& a, MvWarp& w, const MvUnit& u, int groups)
+// Where the scales of the warp's two rows of a unit begin; rows past the last read the
+// last one's, and nothing uses them.
+template <int GROUP, typename S>
+__device__ __forceinline__ void mv_rows(const MatvecArgs& a, const MvWarp& w, const MvUnit& u, int groups,
+                                        typename MvScales<GROUP, S>::Rows& rows)
 {
     const int n0 = min(u.n0 + w.row, a.N - 1);
     const int n1 = a.swiglu ? n0 + a.N : min(u.n0 + w.half + w.row, a.N - 1);
     const int64_t first = (int64_t)u.e * (a.swiglu ? 2 * a.N : a.N);
-    w.at0 = (first + n0) * groups;
-    w.at1 = (first + n1) * groups;
+    rows.s[0] = static_cast<const S*>(a.scales) + (first + n0) * groups;
+    rows.s[1] = static_cast<const S*>(a.scales) + (first + n1) * groups;
+    rows.z[0] = a.zeros + (first + n0) * groups;
+    rows.z[1] = a.zeros + (first + n1) * groups;
 }
 
 // All stages of one unit with 8 NT rows of x.  `now` holds the first stage's
 // scales and is left with those of the next unit's (`un`, when there is one).
 template <int GROUP, int NT, typename S>
-__device__ __forceinline__ void mv_consume(const MatvecArgs& a, MvWarp& w, MvRing& ring, uint64_t* full,
+__device__ __forceinline__ void mv_consume(const MatvecArgs& a, const MvWarp& w, const uint8_t* smem, MvRing& ring, uint64_t* full,
                                            uint64_t* empty, volatile int* abort, int ksteps, int groups,
                                            bool more, const MvUnit& un, MvScales<GROUP, S>& now,
-                                           float (&acc)[NT][4])
+                                           typename MvScales<GROUP, S>::Rows& rows, float (&acc)[NT][4])
 {
     constexpr int kGroups = kMvChunk / GROUP;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
 #pragma unroll
         for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-    int left = a.Kd - w.part * kMvChunk, q = w.part * kGroups;
     const bool zeros = a.zeros != nullptr;
-    for (int s = 1; s <= ksteps; ++s, left -= kMvChunk << a.lk) {
+    const int last = w.whole ? groups - kGroups : groups - 1;    // the last group to begin a load at
+    int left = a.Kd - w.part * kMvChunk, q = w.part * kGroups;
+    for (int s = ksteps; s > 0; --s, left -= kMvChunk << a.lk) {
         MvScales<GROUP, S> next = now;
-        q += kGroups << a.lk;
-        if (s == ksteps) {
-            q = w.part * kGroups;
-            if (more) mv_rows(a, w, un, groups);
+        q = min(q + (kGroups << a.lk), last);
+        if (s == 1) {
+            q = min(w.part * kGroups, last);
+            if (more) mv_rows<GROUP, S>(a, w, un, groups, rows);
         }
-        next.load(a, w.at0, w.at1, q, groups, w.whole);
+        next.load(rows, q, groups - q, w.whole, zeros);
         mbar_wait(full + ring.slot, ring.phase, abort);
-        const uint32_t at = w.base + ring.slot * a.stage_bytes;
+        const uint8_t* st = smem + ring.slot * a.stage_bytes;
         // a part without channels left in the last stage has no records of x there either
-        if (left >= kMvChunk) mv_stage<GROUP, NT, true>(at + w.ow, at + w.ox, at + w.oc, now, zeros, 8, acc);
-        else if (left > 0) mv_stage<GROUP, NT, false>(at + w.ow, at + w.ox, at + w.oc, now, zeros, left / 32, acc);
+        if (left >= kMvChunk) mv_stage<GROUP, NT, true>(st, w.ow, w.ox, w.oc, now, 8, acc);
+        else if (left > 0) mv_stage<GROUP, NT, false>(st, w.ow, w.ox, w.oc, now, left / 32, acc);
         __syncwarp();
         if (threadIdx.x % kWarp == 0) mbar_arrive(empty + ring.slot);
         ring.next(a.stages);
@@ -651,7 +663,6 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__
         w.part = part;
         w.row = tile * 8 + g;                              // in each half of the tile
         w.half = half;
-        w.base = smem_u32(smem);
         w.ow = part * half * 128 + w.row * 128 + (g << 4) + t * 4;
         w.ox = kMvW + (part * a.chunk_rows + g) * kMvRecord + t * 16;
         w.oc = kMvW + (part * a.chunk_rows + 2 * t) * kMvRecord + kMvChunk * 2;
@@ -662,8 +673,11 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__
         if (unit < units) {
             MvUnit u = mv_unit(a, s_pre, s_beg, s_end, tiles, tile_n, unit);
             MvScales<GROUP, S> now;
-            mv_rows(a, w, u, groups);
-            now.load(a, w.at0, w.at1, part * kGroups, groups, w.whole);
+            typename MvScales<GROUP, S>::Rows rows;
+            now.clear();
+            mv_rows<GROUP, S>(a, w, u, groups, rows);
+            const int q0 = min(part * kGroups, w.whole ? groups - kGroups : groups - 1);
+            now.load(rows, q0, groups - q0, w.whole, a.zeros != nullptr);
             while (unit < units) {
                 unit += gridDim.x;
                 const bool more = unit < units;
@@ -671,15 +685,15 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__
                 if (more) un = mv_unit(a, s_pre, s_beg, s_end, tiles, tile_n, unit);
                 if (NTMAX == 1 || u.m <= 8) {
                     float acc[1][4];
-                    mv_consume<GROUP, 1, S>(a, w, ring, full, empty, &s_abort, ksteps, groups, more, un, now, acc);
+                    mv_consume<GROUP, 1, S>(a, w, smem, ring, full, empty, &s_abort, ksteps, groups, more, un, now, rows, acc);
                     mv_store<1>(a, u, s_red, acc, out);
                 } else if (NTMAX == 2 || u.m <= 16) {
                     float acc[2][4];
-                    mv_consume<GROUP, 2, S>(a, w, ring, full, empty, &s_abort, ksteps, groups, more, un, now, acc);
+                    mv_consume<GROUP, 2, S>(a, w, smem, ring, full, empty, &s_abort, ksteps, groups, more, un, now, rows, acc);
                     mv_store<2>(a, u, s_red, acc, out);
                 } else if constexpr (NTMAX == 4) {
                     float acc[4][4];
-                    mv_consume<GROUP, 4, S>(a, w, ring, full, empty, &s_abort, ksteps, groups, more, un, now, acc);
+                    mv_consume<GROUP, 4, S>(a, w, smem, ring, full, empty, &s_abort, ksteps, groups, more, un, now, rows, acc);
                     mv_store<4>(a, u, s_red, acc, out);
                 }
                 u = un;
@@ -753,25 +767,31 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
 
 constexpr int kMvSmem = 227 * 1024;
 
-// Parts of K and rows of a unit.  A block's time for a unit grows with the
-// weights it holds and, once the products outweigh the unpacking, with the
-// rows; the whole takes as long as the rounds of units the blocks need.  The
-// number of experts with rows and their mean rows are the host's guess: at most
-// every row has its own.
+// Parts of K and rows of a unit: the pair with the least of
+//   rounds of units * (stages of a unit * cost of a stage + cost of a unit)
+// where the costs are the fit of a sweep over every pair at four shapes (16
+// tokens 2 x 1024 x 6144 with SwiGLU 110 / 108 / 125 us at 1 / 2 / 4 parts and
+// 8 rows; 128 tokens 2048 x 7168 with zero points 599 / 489 / 609 us; 255 tokens
+// 2050 x 2048 at 1 part 106 / 81 / 84 us with 8 / 16 / 32 rows, at 4 parts 153 us;
+// one token 7168 x 7168 30 / 21 / 22 us).  A stage takes longer with more rows; one
+// part with zero points holds more lines of scales open than L1 keeps.  How many
+// experts have rows, and how many each, is the guess of a uniform choice.
 void mv_shape(moedc::MatvecArgs& a, int blocks)
 {
-    const int64_t active = a.E < a.rows ? a.E : a.rows;
-    const double per = (double)a.rows / active;
+    const double active = a.E * (1.0 - exp(-(double)a.rows / a.E));
+    const double per = a.rows / active;
     double best = 0.0;
     for (int lk = 0; lk <= 2; ++lk)
         for (int chunk = 8; chunk <= moedc::kMvTokens >> lk; chunk *= 2) {
             const int tile_n = (moedc::kMvRows >> lk) / (a.swiglu ? 2 : 1);
             const double tiles = (a.N + tile_n - 1) / tile_n;
-            const double chunks = (double)(int64_t)((per + chunk - 1) / chunk);
-            const double rounds = (double)(int64_t)((active * tiles * chunks + blocks - 1) / blocks);
-            const double rows = per < chunk ? per : chunk;
-            const double cost = rounds / (1 << lk) * (rows <= 8 ? 44.0 : rows <= 16 ? 44.0 : 55.0);
-            if (best == 0.0 || cost < best * 0.97) {
+            const double chunks = per / chunk > 0.5 ? per / chunk + 0.5 : 1.0;
+            const double rounds = ceil(active * tiles * chunks / blocks);
+            const double stages = (a.Kd + (moedc::kMvChunk << lk) - 1) / (moedc::kMvChunk << lk);
+            double stage = chunk == 8 || per <= 8 ? 44.0 : chunk == 16 || per <= 16 ? 56.0 : 80.0;
+            if (lk == 0 && a.zeros) stage *= 1.25;
+            const double cost = rounds * (stages * stage + 90.0);
+            if (best == 0.0 || cost < best) {
                 best = cost;
                 a.lk = lk;
                 a.chunk_rows = chunk;
