@@ -39,7 +39,7 @@
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
-#include "lm_common.cuh"
+#include "matvec_int4.cuh"
 
 namespace moedc {
 
@@ -56,22 +56,6 @@ constexpr unsigned long long kMvWaitNs = 200000000ull; // bound of every wait
 // eight groups, then 2^12 / scale.  576 bytes apart, the rows that a quarter-warp
 // reads lie in different halves of the banks.
 constexpr int kMvRecord = kMvChunk * 2 + 64;
-
-struct MatvecArgs {
-    const uint8_t* x;     // records [x_rows + 1][channels / 256], the last row zeros
-    int x_rows, Kd;
-    const void* scales;
-    const uint8_t* zeros;
-    int E, N;
-    const int32_t *offsets, *counts, *src;
-    int top_k, rows;
-    int32_t* status;
-    bool swiglu, f16;   // f16: the type of the outputs (else bf16)
-    int lk;             // log2 of the parts of K
-    int chunk_rows;     // rows of a unit, at most: 8, 16 or 32
-    int stages, stage_bytes;
-    unsigned wait_extra;
-};
 
 // ---------------------------------------------------------------- mbarriers
 
@@ -353,62 +337,6 @@ __device__ __forceinline__ void mv_stage(const uint8_t* st, uint32_t w, uint32_t
     }
 }
 
-// --------------------------------------------------------------------- units
-
-// Rows [r0, r0 + m) of expert e and the tile's first output channel.
-struct MvUnit {
-    int e, n0, r0, m;
-};
-
-// First and last row of an expert, inside [0, rows].
-__device__ __forceinline__ void expert_rows(const MatvecArgs& a, int e, int& beg, int& end,
-                                            bool& over)
-{
-    int64_t b = a.offsets ? __ldg(a.offsets + e) : 0;
-    int64_t n = b + (a.counts ? __ldg(a.counts + e) : a.rows);
-    if (b < 0) b = 0;
-    if (n > a.rows) {
-        n = a.rows;
-        over = true;
-    }
-    beg = (int)(b < n ? b : 0);
-    end = (int)(b < n ? n : 0);
-}
-
-// s_pre[e]: chunks of the experts before e; s_beg[e], s_end[e]: its rows
-__device__ __forceinline__ MvUnit mv_unit(const MatvecArgs& a, const int32_t* s_pre,
-                                          const int32_t* s_beg, const int32_t* s_end, int tiles,
-                                          int tile_n, int unit)
-{
-    int lo = 0, hi = a.E - 1;   // last expert whose units begin at or before `unit`
-    while (lo < hi) {
-        const int mid = (lo + hi + 1) / 2;
-        if (s_pre[mid] * tiles <= unit) lo = mid; else hi = mid - 1;
-    }
-    const int chunks = s_pre[lo + 1] - s_pre[lo];
-    const int in = unit - s_pre[lo] * tiles;
-    const int tile = in / chunks, chunk = in - tile * chunks;   // chunks of one tile are neighbours
-    MvUnit u;
-    u.e = lo;
-    u.n0 = tile * tile_n;
-    u.r0 = s_beg[lo] + chunk * a.chunk_rows;
-    u.m = min(a.chunk_rows, s_end[lo] - u.r0);
-    return u;
-}
-
-// The x row of packed row r; the row of zeros where there is none.
-__device__ __forceinline__ int x_row(const MatvecArgs& a, int r, bool& bad)
-{
-    int t = r;
-    if (a.src) {
-        const int i = __ldg(a.src + r);
-        t = i < 0 ? -1 : i / a.top_k;
-    }
-    if (t >= 0 && t < a.x_rows) return t;
-    bad = true;
-    return a.x_rows;
-}
-
 // Where a stage's slot and phase go round the ring.
 struct MvRing {
     int slot = 0, phase = 0;
@@ -420,11 +348,6 @@ struct MvRing {
         }
     }
 };
-
-__device__ __forceinline__ void store16(uint16_t* p, float v, bool f16)
-{
-    *p = f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-}
 
 // The unit's end: the parts of K added, the epilogue, the outputs.
 template <int NT>
@@ -615,44 +538,7 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__
     }
     pdl_enter();
 
-    // chunks of the experts before each one
-    bool over = false;
-    {
-        const int per = (a.E + kMvThreads - 1) / kMvThreads;
-        const int e0 = threadIdx.x * per;
-        int64_t sum = 0;
-        for (int e = e0; e < min(a.E, e0 + per); ++e) {
-            int beg, end;
-            expert_rows(a, e, beg, end, over);
-            const int c = (end - beg) / a.chunk_rows + ((end - beg) % a.chunk_rows != 0);
-            s_beg[e] = beg;
-            s_end[e] = end;
-            s_pre[e] = c;
-            sum += c;
-        }
-        int64_t incl = sum;
-#pragma unroll
-        for (int d = 1; d < kWarp; d <<= 1) {
-            const int64_t y = __shfl_up_sync(0xffffffffu, incl, d);
-            if (lane >= d) incl += y;
-        }
-        if (lane == kWarp - 1) s_scan[warp] = incl;
-        __syncthreads();
-        int64_t base = incl - sum;
-        for (int w = 0; w < warp; ++w) base += s_scan[w];
-        for (int e = e0; e < min(a.E, e0 + per); ++e) {
-            const int c = s_pre[e];
-            s_pre[e] = (int)base;
-            base += c;
-        }
-        // experts that overlap could claim more units than there are numbers: none then
-        if (e0 < a.E && e0 + per >= a.E) {
-            const bool fits = base * tiles <= INT_MAX;
-            s_pre[a.E] = fits ? (int)base : 0;
-            over |= !fits;
-        }
-        __syncthreads();
-    }
+    const bool over = mv_chunks<kMvThreads>(a, tiles, s_scan, s_pre, s_beg, s_end);
     const int units = s_pre[a.E] * tiles;
     if (over && blockIdx.x == 0) raise_status(a.status, MOEDC_ERR_CAPACITY);
 
@@ -710,7 +596,7 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__
             const int wrow = u.e * wrows + u.n0;
             const int r = lane >> a.lk, p = lane & (wk - 1);       // this lane's record
             const bool mine = r < u.m;
-            const uint8_t* xr = mine ? a.x + (int64_t)x_row(a, u.r0 + r, bad) * chunks * kMvRecord : nullptr;
+            const uint8_t* xr = mine ? a.records + (int64_t)x_row(a, u.r0 + r, bad) * chunks * kMvRecord : nullptr;
             for (int s = 0; s < ksteps; ++s) {
                 const bool go = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
                 if (!__all_sync(0xffffffffu, go)) break;
@@ -870,9 +756,10 @@ int launch_matvec_x(const void* x, int64_t ldx, int x_rows, int Kd, int group, u
 }  // namespace
 }  // namespace moedc_host
 
-extern "C" size_t moedc_matvec_int4_workspace_bytes(int x_rows, int Kd)
+extern "C" size_t moedc_matvec_int4_workspace_bytes(int x_rows, int Kd, int E, int N, int flags, int rows)
 {
-    if (x_rows < 0 || Kd < 1) return 0;
+    if (x_rows < 0 || Kd < 1 || E < 1 || N < 1 || rows < 1 || (flags & ~MOEDC_SWIGLU) != 0) return 0;
+    if (moedc_host::matvec_small_takes(Kd, E, N, flags != 0, rows)) return 0;
     return ((size_t)x_rows + 1) * ((Kd + (size_t)moedc::kMvChunk - 1) / moedc::kMvChunk) * moedc::kMvRecord;
 }
 
@@ -903,10 +790,15 @@ extern "C" int moedc_matvec_int4(const void* x, int64_t ldx, int dtype, int x_ro
         return MOEDC_ERR_ARG;
     if (rows == 0) return MOEDC_OK;
     if (!out || !x) return MOEDC_ERR_ARG;
-    if (!workspace || !aligned(workspace, 16) ||
-        workspace_bytes < moedc_matvec_int4_workspace_bytes(x_rows, Kd))
+    const bool small = matvec_small_takes(Kd, E, N, flags != 0, rows);
+    if (!small && (!workspace || !aligned(workspace, 16) ||
+                   workspace_bytes < moedc_matvec_int4_workspace_bytes(x_rows, Kd, E, N, flags, rows)))
         return MOEDC_ERR_ARG;
     moedc::MatvecArgs a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.wq = static_cast<const uint8_t*>(wq);
+    a.scale_dtype = scale_dtype;
     a.x_rows = x_rows;
     a.Kd = Kd;
     a.scales = scales;
@@ -922,8 +814,9 @@ extern "C" int moedc_matvec_int4(const void* x, int64_t ldx, int dtype, int x_ro
     a.swiglu = (flags & MOEDC_SWIGLU) != 0;
     a.wait_extra = test_wait_extra();
     a.f16 = dtype == MOEDC_F16;
+    if (small) return launch_matvec_small(a, group, out, stream);
     uint8_t* records = static_cast<uint8_t*>(workspace);
-    a.x = records;
+    a.records = records;
     mv_shape(a, sm_count());
     const int st = dtype == MOEDC_F16
                        ? launch_matvec_x<__half>(x, ldx, x_rows, Kd, group, records, stream)

@@ -121,7 +121,7 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.moedc_matvec_int4.argtypes = [P, L, I, I, I, P, P, I, P, I, I, I, I, P, P, P, I, I, P, P,
                                       Z, P, P]
     lib.moedc_matvec_int4.restype = I
-    lib.moedc_matvec_int4_workspace_bytes.argtypes = [I, I]
+    lib.moedc_matvec_int4_workspace_bytes.argtypes = [I, I, I, I, I, I]
     lib.moedc_matvec_int4_workspace_bytes.restype = Z
     lib.moedc_test_set_wait_extra.argtypes = [ctypes.c_uint]
     lib.moedc_test_set_wait_extra.restype = None
@@ -281,8 +281,9 @@ def moedc_unsort_grad(dy, lddy, sorted, dtype, T, H, K, row, src, topk_weights, 
                                     _stream(stream))
 
 
-def moedc_matvec_int4_workspace_bytes(x_rows: int, Kd: int) -> int:
-    return int(load().moedc_matvec_int4_workspace_bytes(x_rows, Kd))
+def moedc_matvec_int4_workspace_bytes(x_rows: int, Kd: int, E: int, N: int, flags: int,
+                                      rows: int) -> int:
+    return int(load().moedc_matvec_int4_workspace_bytes(x_rows, Kd, E, N, flags, rows))
 
 
 def moedc_matvec_int4(x, ldx, dtype, x_rows, Kd, wq, scales, scale_dtype, zeros, group, E, N,
@@ -518,7 +519,9 @@ def gate(logits: torch.Tensor, K: int, bias: torch.Tensor | None = None,
     _need(w, torch.float32, "out[1]")
     _need_shape(idx, (T, K), "out[0]")
     _need_shape(w, (T, K), "out[1]")
-    _check(moedc_gate(logits, ld, dtype, T, E, K, bias, flags, scale, idx, w), "moedc_gate")
+    _check((_lib or load()).moedc_gate(logits.data_ptr(), ld, dtype, T, E, K, _p(bias), flags,
+                                       scale, idx.data_ptr(), w.data_ptr(), _stream(None)),
+           "moedc_gate")
     return out
 
 
@@ -541,8 +544,9 @@ def gate_grad(logits: torch.Tensor, topk_idx: torch.Tensor, dweights: torch.Tens
         out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
     _need(out, logits.dtype, "out")
     _need_shape(out, (T, E), "out")
-    _check(moedc_gate_grad(logits, ld, dtype, T, E, K, bias, flags, scale, topk_idx, dweights,
-                           out), "moedc_gate_grad")
+    _check((_lib or load()).moedc_gate_grad(logits.data_ptr(), ld, dtype, T, E, K, _p(bias), flags,
+                                            scale, topk_idx.data_ptr(), dweights.data_ptr(),
+                                            out.data_ptr(), _stream(None)), "moedc_gate_grad")
     return out
 
 
@@ -599,9 +603,12 @@ def sort(x: torch.Tensor | None, topk_idx: torch.Tensor, E: int, align: int = 1,
             _need_shape(out.rows, (rows, H), "out.rows")
         _need_shape(out.row, (T, K), "out.row")
         _need_shape(out.counts, (E,), "out.counts")
-    _check(moedc_sort(x, ld, dtype, T, H, topk_idx, K, E, align, rows, out.rows, out.row, out.src,
-                      out.offsets, out.counts, out.workspace, out.workspace.numel(), out.status),
-           "moedc_sort")
+    _check((_lib or load()).moedc_sort(_p(x), ld, dtype, T, H, topk_idx.data_ptr(), K, E, align,
+                                       rows, _p(out.rows), out.row.data_ptr(),
+                                       out.src.data_ptr(), out.offsets.data_ptr(),
+                                       out.counts.data_ptr(), out.workspace.data_ptr(),
+                                       out.workspace.numel(), out.status.data_ptr(),
+                                       _stream(None)), "moedc_sort")
     return out
 
 
@@ -620,7 +627,9 @@ def unsort(rows: torch.Tensor, row: torch.Tensor, topk_weights: torch.Tensor | N
         out = torch.empty((T, H), dtype=rows.dtype, device=rows.device)
     _need(out, rows.dtype, "out")
     _need_shape(out, (T, H), "out")
-    _check(moedc_unsort(rows, dtype, R, H, row, topk_weights, T, K, out), "moedc_unsort")
+    _check((_lib or load()).moedc_unsort(rows.data_ptr(), dtype, R, H, row.data_ptr(),
+                                         _p(topk_weights), T, K, out.data_ptr(), _stream(None)),
+           "moedc_unsort")
     return out
 
 
@@ -657,8 +666,10 @@ def unsort_grad(dy: torch.Tensor, rows: torch.Tensor | None, row: torch.Tensor,
     if dw is not None:
         _need(dw, torch.float32, "out[1]")
         _need_shape(dw, (T, K), "out[1]")
-    _check(moedc_unsort_grad(dy, ld, rows, dtype, T, H, K, row, src, topk_weights, R, drows, dw),
-           "moedc_unsort_grad")
+    _check((_lib or load()).moedc_unsort_grad(dy.data_ptr(), ld, _p(rows), dtype, T, H, K,
+                                              row.data_ptr(), src.data_ptr(),
+                                              topk_weights.data_ptr(), R, drows.data_ptr(),
+                                              _p(dw), _stream(None)), "moedc_unsort_grad")
     return out
 
 
@@ -672,7 +683,7 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
     ([N, Kd/2]: one linear layer) with scales [E, N, Kd/group]; swiglu: 2N
     weight rows, silu(gate) * up.  offsets and counts from sort(); src and
     top_k read x in token order.  workspace: moedc_matvec_int4_workspace_bytes
-    bytes, allocated here when None."""
+    bytes, allocated here when None and needed."""
     ld = _need_rows(x, "x")
     dtype = _lm_dtype(x, "x")
     if wq.dim() == 2:
@@ -684,7 +695,8 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
     Kd = 2 * half
     if x.shape[1] != Kd:
         raise ValueError(f"x must have {Kd} channels, not {x.shape[1]}")
-    if scales.dim() != 3 or scales.shape[:2] != (E, wn) or Kd % max(1, scales.shape[2]):
+    groups = scales.shape[-1]
+    if scales.shape != (E, wn, groups) or Kd % max(1, groups):
         raise ValueError(f"scales must have shape [{E}, {wn}, {Kd} / group]")
     if zeros is not None:
         _need(zeros, torch.uint8, "zeros")
@@ -707,11 +719,17 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
     _need_shape(out, (R, N), "out")
     if status is None:
         status = torch.zeros(1, dtype=torch.int32, device=x.device)
+    lib = _lib or load()
+    flags = SWIGLU if swiglu else 0
+    xr = x.shape[0]
     if workspace is None:
-        workspace = torch.empty(moedc_matvec_int4_workspace_bytes(x.shape[0], Kd),
-                                dtype=torch.uint8, device=x.device)
-    _check(moedc_matvec_int4(x, ld, dtype, x.shape[0], Kd, wq, scales, _lm_dtype(scales, "scales"),
-                             zeros, Kd // max(1, scales.shape[2]), E, N, SWIGLU if swiglu else 0,
-                             offsets, counts, src, top_k, R, out, workspace, workspace.numel(),
-                             status), "moedc_matvec_int4")
+        n = lib.moedc_matvec_int4_workspace_bytes(xr, Kd, E, N, flags, R)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+    _check(lib.moedc_matvec_int4(x.data_ptr(), ld, dtype, xr, Kd, wq.data_ptr(),
+                                 scales.data_ptr(), _lm_dtype(scales, "scales"), _p(zeros),
+                                 Kd // max(1, groups), E, N, flags, _p(offsets), _p(counts),
+                                 _p(src), top_k, R, out.data_ptr(), _p(workspace),
+                                 0 if workspace is None else workspace.numel(),
+                                 status.data_ptr(), _stream(None)), "moedc_matvec_int4")
     return out

@@ -460,16 +460,19 @@ MOEDC_EXPORT int moedc_unsort_grad(const void* dy, int64_t lddy, const void* sor
  * E = 1: all rows.  group is 32, 64 or 128, Kd a multiple of it; x and wq
  * 16-byte aligned and ldx a multiple of 8.  A row of x that holds an infinity
  * or a NaN gives NaN.
- * workspace: moedc_matvec_int4_workspace_bytes, 16-byte aligned, no
- * initialisation (x in the order the products read it); 0 is returned for
- * rejected arguments.  Calls that can run at the same time need their own.
+ * workspace: moedc_matvec_int4_workspace_bytes of the same arguments, 16-byte
+ * aligned, no initialisation (x in the order the products read it).  The query
+ * returns 0, and workspace may be NULL, where the weights to read are so few
+ * that one launch without preparation is the faster form (and for arguments
+ * that the call rejects).  Calls that can run at the same time need their own.
  * Data errors (dev_status): MOEDC_ERR_EXPERT_RANGE when a row's x row lies
  * outside [0, x_rows) (it counts as zeros), MOEDC_ERR_CAPACITY when an
  * expert's rows pass `rows` (those are skipped), MOEDC_ERR_TIMEOUT if a bounded
  * wait for the kernel's own copies gave up (its outputs are then unspecified).
  */
 #define MOEDC_SWIGLU 1
-MOEDC_EXPORT size_t moedc_matvec_int4_workspace_bytes(int x_rows, int Kd);
+MOEDC_EXPORT size_t moedc_matvec_int4_workspace_bytes(int x_rows, int Kd, int E, int N,
+                 int flags, int rows);
 MOEDC_EXPORT int moedc_matvec_int4(const void* x, int64_t ldx, int dtype, int x_rows, int Kd,
                  const void* wq, const void* scales, int scale_dtype, const uint8_t* zeros,
                  int group, int E, int N, int flags, const int32_t* offsets,

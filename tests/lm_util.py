@@ -17,7 +17,7 @@ def rounding(ref: torch.Tensor, dtype: torch.dtype) -> torch.Tensor:
 
 
 def assert_within(got: torch.Tensor, ref: torch.Tensor, bound) -> None:
-    got = got.detach().cpu().double()
+    got = got.detach().to(ref.device).double()
     assert got.shape == ref.shape
     assert not torch.isnan(got).any()
     over = (got - ref).abs() - bound
@@ -122,20 +122,21 @@ def unsort_ref(sorted_, row, w):
 
 
 def int4_weights(wq, scales, zeros, group):
-    """f64 [.., N, Kd] of the packed form."""
-    q = wq.cpu().long()
-    w = torch.empty(*q.shape[:-1], 2 * q.shape[-1], dtype=torch.float64)
+    """f64 [.., N, Kd] of the packed form, where wq is."""
+    q = wq
+    w = torch.empty(*q.shape[:-1], 2 * q.shape[-1], dtype=torch.float64, device=q.device)
     w[..., 0::2] = (q % 16).double()
     w[..., 1::2] = (q // 16).double()
-    z = 8.0 if zeros is None else zeros.cpu().double().repeat_interleave(group, -1)
-    return (w - z) * scales.cpu().double().repeat_interleave(group, -1)
+    w -= 8.0 if zeros is None else zeros.double().repeat_interleave(group, -1)
+    w *= scales.double().repeat_interleave(group, -1)
+    return w
 
 
 def matvec_ref(x_rows, w, swiglu):
     """(out, bound on the binary32 sums' error) of x_rows [r, Kd] with w [n, Kd].
     A sum of Kd products in some 8 parallel chains, their join and the group
     scales: (Kd / 8 + 64) roundings of at most half an ulp of the magnitudes."""
-    x = x_rows.cpu().double()
+    x = x_rows.to(w.device).double()
     v, mag = x @ w.T, x.abs() @ w.abs().T
     err = (x.shape[1] / 8 + 64) * U32 * mag
     if not swiglu:

@@ -16,8 +16,13 @@ def _weights(g, E, n, Kd, group, zeros, sdtype):
 
 
 def _check(T, E, K, N, Kd, group, dtype, swiglu=False, zeros=False, align=1, mask=0.0,
-           gather=True, sdtype=None, seed=0, idx=None):
+           gather=True, sdtype=None, seed=0, idx=None, big=False):
     g = torch.Generator().manual_seed(seed + T + N)
+    if big:       # enough outputs for the form with prepared x
+        per = (min(E, T * K) + T * K // 8) * (2 if swiglu else 1) * Kd // 2
+        N += (11 << 20) // per
+        rows = moedc.moedc_sort_rows(T, K, E, align)
+        assert moedc.moedc_matvec_int4_workspace_bytes(T, Kd, E, N, int(swiglu), rows) > 0
     if idx is None:
         idx = torch.rand(T, E, generator=g).argsort(1)[:, :K].to(torch.int32)
         idx[torch.rand(T, K, generator=g) < mask] = -1
@@ -33,31 +38,38 @@ def _check(T, E, K, N, Kd, group, dtype, swiglu=False, zeros=False, align=1, mas
                             top_k=K, swiglu=swiglu, status=status, out=out)
     assert got is out and int(status) == 0
     _, src_ref, offsets, counts = sort_ref(idx, E, align, R)
-    w = int4_weights(wq, s, z, group)
     for e in range(E):
         rows = slice(int(offsets[e]), int(offsets[e]) + int(counts[e]))
         if counts[e] == 0:
             continue
-        ref, err = matvec_ref(x.cpu()[(src_ref[rows] // K).long()], w[e], swiglu)
+        w = int4_weights(wq[e], s[e], None if z is None else z[e], group)
+        ref, err = matvec_ref(x[(src_ref[rows] // K).long().cuda()], w, swiglu)
         assert_within(out[rows], ref, err + rounding(ref, dtype))
     assert (out[m.src < 0] == 7.0).all()           # rows of no expert stay as they were
 
 
+# both forms of the product: one launch for few weights, prepared x for many
+FORMS = pytest.mark.parametrize("big", [False, True], ids=["few", "many"])
+
+
+@FORMS
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("T,E,K,N,mult", [
     (1, 1, 1, 1, 1), (1, 4, 2, 16, 3), (3, 8, 2, 17, 5), (16, 12, 4, 130, 4), (40, 6, 2, 33, 7),
     (9, 2, 1, 64, 16), (70, 3, 2, 48, 2), (150, 2, 2, 20, 3)])
-def test_products(T, E, K, N, mult, group, dtype):
-    _check(T, E, K, N, group * mult, group, DTYPES[dtype])
+def test_products(T, E, K, N, mult, group, dtype, big):
+    _check(T, E, K, N, group * mult, group, DTYPES[dtype], big=big)
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16"])
 @pytest.mark.parametrize("group", [32, 64, 128])
 @pytest.mark.parametrize("zeros", [False, True])
-def test_swiglu_and_zero_points(group, zeros, dtype):
-    _check(13, 6, 3, 37, group * 5, group, DTYPES[dtype], swiglu=True, zeros=zeros)
-    _check(50, 3, 2, 24, group * 9, group, DTYPES[dtype], swiglu=False, zeros=zeros, seed=1)
+@FORMS
+def test_swiglu_and_zero_points(group, zeros, dtype, big):
+    _check(13, 6, 3, 37, group * 5, group, DTYPES[dtype], swiglu=True, zeros=zeros, big=big)
+    _check(50, 3, 2, 24, group * 9, group, DTYPES[dtype], swiglu=False, zeros=zeros, seed=1,
+           big=big)
 
 
 # enough 128-row tiles of weights to give every SM one: experts of few and of many rows,
@@ -96,29 +108,34 @@ def test_nothing_of_an_earlier_call_comes_through(Kd):
     m = moedc.sort(None, idx.cuda(), 8)
     out = moedc.matvec_int4(bad, wq, s, offsets=m.offsets, counts=m.counts, src=m.src)
     assert torch.isnan(out).all()
+    _check(5, 4, 2, 40, Kd, 64, torch.bfloat16, zeros=True, big=True)
     _check(5, 4, 2, 40, Kd, 64, torch.bfloat16, zeros=True)
 
 
 @pytest.mark.parametrize("sdtype", list(DTYPES))
-def test_scale_types(sdtype):
-    _check(5, 4, 2, 40, 512, 64, torch.bfloat16, zeros=True, sdtype=DTYPES[sdtype])
+@FORMS
+def test_scale_types(sdtype, big):
+    _check(5, 4, 2, 40, 512, 64, torch.bfloat16, zeros=True, sdtype=DTYPES[sdtype], big=big)
 
 
 @pytest.mark.parametrize("gather", [False, True])
-def test_aligned_groups_masked_entries_and_gather(gather):
-    _check(30, 9, 4, 50, 384, 128, torch.bfloat16, align=16, mask=0.4, gather=gather)
-    _check(8, 9, 4, 50, 384, 128, torch.bfloat16, align=4, mask=1.1, gather=gather)
+@FORMS
+def test_aligned_groups_masked_entries_and_gather(gather, big):
+    _check(30, 9, 4, 50, 384, 128, torch.bfloat16, align=16, mask=0.4, gather=gather, big=big)
+    _check(8, 9, 4, 50, 384, 128, torch.bfloat16, align=4, mask=1.1, gather=gather, big=big)
 
 
-def test_long_rows_of_real_sizes():
-    _check(4, 2, 2, 96, 7168, 128, torch.bfloat16)
-    _check(33, 2, 1, 64, 14336, 128, torch.bfloat16, seed=3)
-    _check(12, 3, 2, 64, 6144, 64, torch.bfloat16, swiglu=True, zeros=True, seed=4)
+@FORMS
+def test_long_rows_of_real_sizes(big):
+    _check(4, 2, 2, 96, 7168, 128, torch.bfloat16, big=big)
+    _check(33, 2, 1, 64, 14336, 128, torch.bfloat16, seed=3, big=big)
+    _check(12, 3, 2, 64, 6144, 64, torch.bfloat16, swiglu=True, zeros=True, seed=4, big=big)
 
 
-def test_every_row_at_one_expert():
+@FORMS
+def test_every_row_at_one_expert(big):
     idx = torch.full((97, 1), 2, dtype=torch.int32)
-    _check(97, 4, 1, 40, 256, 64, torch.float16, idx=idx)
+    _check(97, 4, 1, 40, 256, 64, torch.float16, idx=idx, big=big)
 
 
 def test_one_linear_layer_without_maps():
@@ -145,10 +162,11 @@ def test_strided_rows_other_stream_and_equal_bits():
     assert torch.equal(got, want)
 
 
-def test_infinite_inputs_stay_in_their_row():
+@FORMS
+def test_infinite_inputs_stay_in_their_row(big):
     g = torch.Generator().manual_seed(3)
     x = torch.randn(5, 256, generator=g).to(torch.bfloat16).cuda()
-    wq, s, _ = _weights(g, 1, 40, 256, 64, False, torch.bfloat16)
+    wq, s, _ = _weights(g, 1, 90000 if big else 40, 256, 64, False, torch.bfloat16)
     want = moedc.matvec_int4(x, wq[0], s[0])
     x[2, 100] = float("nan")
     x[3, 7] = float("inf")
@@ -159,14 +177,16 @@ def test_infinite_inputs_stay_in_their_row():
     assert not torch.isfinite(got[3].float()).any()
 
 
-def test_rows_past_the_end_and_bad_sources_are_reported():
+@FORMS
+def test_rows_past_the_end_and_bad_sources_are_reported(big):
     g = torch.Generator().manual_seed(4)
     x = torch.randn(4, 128, generator=g).to(torch.bfloat16).cuda()
-    wq, s, _ = _weights(g, 2, 20, 128, 64, False, torch.bfloat16)
+    n = 90000 if big else 20
+    wq, s, _ = _weights(g, 2, n, 128, 64, False, torch.bfloat16)
     offsets = torch.tensor([0, 3, 6], dtype=torch.int32).cuda()
     counts = torch.tensor([3, 3], dtype=torch.int32).cuda()
     status = torch.zeros(1, dtype=torch.int32).cuda()
-    out = torch.zeros(4, 20, dtype=torch.bfloat16).cuda()
+    out = torch.zeros(4, n, dtype=torch.bfloat16).cuda()
     moedc.matvec_int4(x, wq, s, offsets=offsets, counts=counts, status=status, out=out)
     assert int(status) == moedc.ERR_CAPACITY
     ref, err = matvec_ref(x[3:], int4_weights(wq[1], s[1], None, 64), False)
@@ -209,7 +229,7 @@ def test_refusals():
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_clean():
     g = torch.Generator().manual_seed(5)
     x = torch.randn(3, 512, generator=g).to(torch.bfloat16).cuda()
-    wq, s, _ = _weights(g, 1, 70, 512, 64, False, torch.bfloat16)
+    wq, s, _ = _weights(g, 1, 50000, 512, 64, False, torch.bfloat16)
     want = moedc.matvec_int4(x, wq, s)
     torch.cuda.synchronize()
     status = torch.zeros(1, dtype=torch.int32).cuda()

@@ -96,11 +96,17 @@ def test_matvec_arguments(lib):
                 dict(s=None), dict(s=ODD), dict(sdt=1), dict(g=16), dict(g=256), dict(g=0),
                 dict(E=0), dict(E=1025), dict(N=0), dict(flags=2), dict(off=None),
                 dict(cnt=None), dict(off=None, cnt=None), dict(src=F, k=0), dict(rows=-1),
-                dict(out=None), dict(out=ODD), dict(st=None), dict(x=P(264)), dict(ws=None),
-                dict(ws=P(264)), dict(wsb=5 * 576 - 1), dict(N=1 << 30, E=4)):
+                dict(out=None), dict(out=ODD), dict(st=None), dict(x=P(264)),
+                dict(N=1 << 30, E=4)):
         assert mv(**bad) == moedc.ERR_ARG, bad
+    # 8 experts of 65536 x 256 weights: beyond the form that needs no workspace
+    big = dict(E=8, N=1 << 16, rows=8)
+    for bad in (dict(ws=None), dict(ws=P(264)), dict(wsb=5 * 576 - 1)):
+        assert mv(**big, **bad) == moedc.ERR_ARG, bad
     assert mv(rows=0) == moedc.OK
     # one record of 576 bytes per row and 256 channels, and a row of zeros
-    assert moedc.moedc_matvec_int4_workspace_bytes(4, 256) == 5 * 576
-    assert moedc.moedc_matvec_int4_workspace_bytes(1, 288) == 2 * 2 * 576
-    assert moedc.moedc_matvec_int4_workspace_bytes(-1, 256) == 0
+    size = moedc.moedc_matvec_int4_workspace_bytes
+    assert size(4, 256, 8, 1 << 16, 0, 8) == 5 * 576
+    assert size(1, 288, 8, 1 << 16, 1, 8) == 2 * 2 * 576
+    assert size(4, 256, 2, 16, 0, 4) == 0                     # few weights: none
+    assert size(-1, 256, 8, 1 << 16, 0, 8) == 0 and size(4, 256, 8, 1 << 16, 2, 8) == 0
