@@ -2,8 +2,9 @@
 // and latency count: one launch, x read as it is, no workspace, no tensor map.
 //
 // A block takes a tile of 16 weight rows (with SwiGLU 8 gate and 8 up rows) and up
-// to eight rows of x; its eight warps take 128-channel chunks of K in turn, each
-// with all loads of two chunks in flight straight to registers, and add their sums
+// to eight rows of x; its four warps take 128-channel chunks of K in turn, each
+// with the weights of several chunks in flight straight to registers (16 bytes a
+// thread and row, turned round within four threads), and add their sums
 // in shared memory.  q | 0x4300 is the bf16 number 128 + q (f16: 0x6400, 1024 + q);
 // less 128 + z it is q - z, exact in either type, so the products need no
 // preparation of x beyond its order.  The group's sum is scaled in binary32.
@@ -11,7 +12,9 @@
 
 namespace moedc {
 
-constexpr int kSmThreads = 256;
+// Four warps and four blocks an SM: 25 MB 16.5 us; eight warps and two blocks 20.5,
+// two warps and eight blocks 20.5 us.
+constexpr int kSmThreads = 128;
 constexpr int kSmWarps = kSmThreads / kWarp;
 
 template <typename T> struct Int4Of;       // q | magic = base + q, exactly
@@ -48,25 +51,48 @@ template <> struct Int4Of<__half> {
     }
 };
 
-__device__ __forceinline__ float scale_at(const MatvecArgs& a, int64_t i)
+// A scale as it comes from memory: widened only where it is used, since widening
+// waits for the load.
+template <typename S> using SmRaw = typename std::conditional<sizeof(S) == 4, float, uint16_t>::type;
+template <typename S> __device__ __forceinline__ float sm_scale(SmRaw<S> v)
 {
-    return a.scale_dtype == MOEDC_F32   ? __ldg(static_cast<const float*>(a.scales) + i)
-           : a.scale_dtype == MOEDC_F16 ? __half2float(static_cast<const __half*>(a.scales)[i])
-                                        : __bfloat162float(static_cast<const __nv_bfloat16*>(a.scales)[i]);
+    if constexpr (sizeof(S) == 4) return v;
+    else if constexpr (std::is_same<S, __half>::value) return __half2float(__ushort_as_half(v));
+    else return __uint_as_float((uint32_t)v << 16);
 }
 
-// One chunk of 128 channels on its way: words of the two weight rows, x of the
-// thread's token, scales and zero points by group.
-template <int GROUP> struct SmChunk {
+// Chunks whose weights are in flight together: as many as registers hold beside
+// their scales.
+template <int GROUP> constexpr int kSmBatch = GROUP == 128 ? 4 : 2;
+
+// The weights of one chunk of 128 channels: two rows, scales and zero points by
+// group.
+template <int GROUP, typename S> struct SmChunk {
     static constexpr int groups = 128 / GROUP;
-    uint32_t w[2][4];
-    uint4 x[4];
-    float s[2][groups];
+    uint4 w[2];
+    SmRaw<S> s[2][groups];
     uint32_t z[2][groups];
 };
 
-template <typename T, int GROUP>
-__global__ void __launch_bounds__(kSmThreads)
+// Four threads hold four words each, thread t the words of 32 neighbouring channels
+// 32 t on; afterwards word j of thread t is word t of thread j, so that the same
+// word of the four threads is 32 neighbouring channels.
+__device__ __forceinline__ void quad_transpose(uint32_t (&w)[4], int t)
+{
+    uint32_t a = t & 1 ? w[0] : w[1], b = t & 1 ? w[2] : w[3];
+    a = __shfl_xor_sync(0xffffffffu, a, 1);
+    b = __shfl_xor_sync(0xffffffffu, b, 1);
+    if (t & 1) w[0] = a, w[2] = b;
+    else w[1] = a, w[3] = b;
+    a = t & 2 ? w[0] : w[2], b = t & 2 ? w[1] : w[3];
+    a = __shfl_xor_sync(0xffffffffu, a, 2);
+    b = __shfl_xor_sync(0xffffffffu, b, 2);
+    if (t & 2) w[0] = a, w[1] = b;
+    else w[2] = a, w[3] = b;
+}
+
+template <typename T, int GROUP, typename S>
+__global__ void __launch_bounds__(kSmThreads, 4)
 matvec_int4_small_kernel(const __grid_constant__ MatvecArgs a, uint16_t* __restrict__ out)
 {
     extern __shared__ int32_t s_mem[];       // pre [E + 1], beg [E], end [E]
@@ -92,28 +118,35 @@ matvec_int4_small_kernel(const __grid_constant__ MatvecArgs a, uint16_t* __restr
         const int64_t row[2] = {(int64_t)u.e * wrows + n0, (int64_t)u.e * wrows + n1};
         const int xr = g < u.m ? x_row(a, u.r0 + g, bad) : a.x_rows;
         const T* x = xr < a.x_rows ? static_cast<const T*>(a.x) + (int64_t)xr * a.ldx + t * 8 : nullptr;
-        auto load = [&](int c, SmChunk<GROUP>& k) __attribute__((always_inline)) {
+        auto load = [&](int c, SmChunk<GROUP, S>& k) __attribute__((always_inline)) {
+            const bool in = c * 128 + t * 32 < a.Kd;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                const bool in = c * 128 + j * 32 < a.Kd;
+            for (int r = 0; r < 2; ++r)
+                k.w[r] = in ? ld_global_nc(reinterpret_cast<const uint4*>(a.wq + row[r] * (a.Kd / 2) + c * 64 + t * 16))
+                            : make_uint4(0, 0, 0, 0);
 #pragma unroll
-                for (int r = 0; r < 2; ++r)
-                    k.w[r][j] = in ? __ldg(reinterpret_cast<const uint32_t*>(a.wq + row[r] * (a.Kd / 2) + c * 64 + j * 16 + t * 4)) : 0;
-                k.x[j] = in && x ? __ldg(reinterpret_cast<const uint4*>(x + c * 128 + j * 32)) : make_uint4(0, 0, 0, 0);
-            }
-#pragma unroll
-            for (int q = 0; q < SmChunk<GROUP>::groups; ++q)
+            for (int q = 0; q < SmChunk<GROUP, S>::groups; ++q)
 #pragma unroll
                 for (int r = 0; r < 2; ++r) {
-                    const int64_t at = row[r] * groups + min(c * SmChunk<GROUP>::groups + q, groups - 1);
-                    k.s[r][q] = scale_at(a, at);
+                    const int64_t at = row[r] * groups + min(c * SmChunk<GROUP, S>::groups + q, groups - 1);
+                    k.s[r][q] = __ldg(static_cast<const SmRaw<S>*>(a.scales) + at);
                     k.z[r][q] = a.zeros ? __ldg(a.zeros + at) : 8u;
                 }
         };
-        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-        auto add = [&](int c, const SmChunk<GROUP>& k) __attribute__((always_inline)) {
+        auto load_x = [&](int c, uint4 (&v)[4]) __attribute__((always_inline)) {
 #pragma unroll
-            for (int q = 0; q < SmChunk<GROUP>::groups; ++q) {
+            for (int j = 0; j < 4; ++j)
+                v[j] = x && c * 128 + j * 32 < a.Kd ? __ldg(reinterpret_cast<const uint4*>(x + c * 128 + j * 32))
+                                                    : make_uint4(0, 0, 0, 0);
+        };
+        float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+        auto add = [&](int c, const SmChunk<GROUP, S>& k, const uint4 (&xv)[4]) __attribute__((always_inline)) {
+            uint32_t wa[4] = {k.w[0].x, k.w[0].y, k.w[0].z, k.w[0].w};
+            uint32_t wb[4] = {k.w[1].x, k.w[1].y, k.w[1].z, k.w[1].w};
+            quad_transpose(wa, t);
+            quad_transpose(wb, t);
+#pragma unroll
+            for (int q = 0; q < SmChunk<GROUP, S>::groups; ++q) {
                 if (c * 128 + q * GROUP >= a.Kd) break;
                 float d[4] = {0.0f, 0.0f, 0.0f, 0.0f};
                 const uint32_t za = Int4Of<T>::magic | k.z[0][q] * 0x00010001u;
@@ -123,27 +156,36 @@ matvec_int4_small_kernel(const __grid_constant__ MatvecArgs a, uint16_t* __restr
                     uint32_t m[8];
 #pragma unroll
                     for (int p = 0; p < 4; ++p) {
-                        m[2 * p] = Int4Of<T>::minus(((k.w[0][j] >> (4 * p)) & 0x000f000fu) | Int4Of<T>::magic, za);
-                        m[2 * p + 1] = Int4Of<T>::minus(((k.w[1][j] >> (4 * p)) & 0x000f000fu) | Int4Of<T>::magic, zb);
+                        m[2 * p] = Int4Of<T>::minus(((wa[j] >> (4 * p)) & 0x000f000fu) | Int4Of<T>::magic, za);
+                        m[2 * p + 1] = Int4Of<T>::minus(((wb[j] >> (4 * p)) & 0x000f000fu) | Int4Of<T>::magic, zb);
                     }
                     // registers of weights p and p + 4 of a word, x in the same pairs
-                    const uint4 v = k.x[j];
+                    const uint4 v = xv[j];
                     Int4Of<T>::mma(d, m, __byte_perm(v.x, v.z, 0x5410), __byte_perm(v.x, v.z, 0x7632));
                     Int4Of<T>::mma(d, m + 4, __byte_perm(v.y, v.w, 0x5410), __byte_perm(v.y, v.w, 0x7632));
                 }
-                acc[0] = fmaf(k.s[0][q], d[0], acc[0]);
-                acc[1] = fmaf(k.s[0][q], d[1], acc[1]);
-                acc[2] = fmaf(k.s[1][q], d[2], acc[2]);
-                acc[3] = fmaf(k.s[1][q], d[3], acc[3]);
+                const float s0 = sm_scale<S>(k.s[0][q]), s1 = sm_scale<S>(k.s[1][q]);
+                acc[0] = fmaf(s0, d[0], acc[0]);
+                acc[1] = fmaf(s0, d[1], acc[1]);
+                acc[2] = fmaf(s1, d[2], acc[2]);
+                acc[3] = fmaf(s1, d[3], acc[3]);
             }
         };
-        for (int c = warp; c < chunks; c += 2 * kSmWarps) {
-            SmChunk<GROUP> k0, k1;
-            const bool two = c + kSmWarps < chunks;
-            load(c, k0);
-            if (two) load(c + kSmWarps, k1);
-            add(c, k0);
-            if (two) add(c + kSmWarps, k1);
+        // a part past the last chunk loads zeros and the last scale, and adds nothing
+        constexpr int kB = kSmBatch<GROUP>;
+        for (int c = warp; c < chunks; c += kB * kSmWarps) {
+            SmChunk<GROUP, S> k[kB];
+#pragma unroll
+            for (int b = 0; b < kB; ++b) load(c + b * kSmWarps, k[b]);
+            uint4 now[4], next[4];
+            load_x(c, now);
+#pragma unroll
+            for (int b = 0; b < kB; ++b) {
+                if (b + 1 < kB) load_x(c + (b + 1) * kSmWarps, next);
+                add(c + b * kSmWarps, k[b], now);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) now[j] = next[j];
+            }
         }
         __syncthreads();                       // the unit before has been read
 #pragma unroll
@@ -179,10 +221,10 @@ matvec_int4_small_kernel(const __grid_constant__ MatvecArgs a, uint16_t* __restr
 namespace moedc_host {
 namespace {
 
-template <typename T, int GROUP>
+template <typename T, int GROUP, typename S>
 int launch_small(const moedc::MatvecArgs& a, void* out, cudaStream_t stream)
 {
-    auto* k = moedc::matvec_int4_small_kernel<T, GROUP>;
+    auto* k = moedc::matvec_int4_small_kernel<T, GROUP, S>;
     const size_t smem = (3 * (size_t)a.E + 1) * sizeof(int32_t);
     const int tile_n = a.swiglu ? 8 : 16;
     const int64_t want = ((int64_t)a.rows / 8 + (a.E < a.rows ? a.E : a.rows)) * ((a.N + tile_n - 1) / tile_n);
@@ -192,16 +234,25 @@ int launch_small(const moedc::MatvecArgs& a, void* out, cudaStream_t stream)
     return launch_status();
 }
 
+template <typename T, int GROUP>
+int launch_small_scale(const moedc::MatvecArgs& a, void* out, cudaStream_t stream)
+{
+    return a.scale_dtype == MOEDC_F32   ? launch_small<T, GROUP, float>(a, out, stream)
+           : a.scale_dtype == MOEDC_F16 ? launch_small<T, GROUP, __half>(a, out, stream)
+                                        : launch_small<T, GROUP, __nv_bfloat16>(a, out, stream);
+}
+
 }  // namespace
 
 #ifndef MOEDC_SMALL_BYTES
-#define MOEDC_SMALL_BYTES (10ll << 20)
+#define MOEDC_SMALL_BYTES (25ll << 20)
 #endif
 
 // Few weights to read, each expert's rows (eight at a time read them again, from
-// L2) counted.  Time on the GPU, this form / the one with prepared x: 2 MB 8.2 /
-// 10.3 us, 10 MB 12.3 / 12.3 us, 18 MB 15.0 / 12.3 us, 36 MB 28.7 / 16.4 us; on the
-// host this form saves a launch, a tensor map and the workspace, some 6 us.
+// L2) counted.  Time on the GPU, this form / the one with prepared x: 2 MB 8.1 /
+// 10.3 us, 10 MB 10.3 / 12.3 us, 20 MB 12.3 / 13.0 us, 25 MB 16.5 / 16.1 us, 36 MB
+// 20.5 / 16.4 us; on the host this form saves a launch, a tensor map and the
+// workspace, some 6 us of 20.
 bool matvec_small_takes(int Kd, int E, int N, bool swiglu, int rows)
 {
     const int64_t active = E < rows ? E : rows;
@@ -214,12 +265,12 @@ int launch_matvec_small(const moedc::MatvecArgs& b, int group, void* out, cudaSt
     moedc::MatvecArgs a = b;
     a.chunk_rows = 8;
     if (a.f16)
-        return group == 32   ? launch_small<__half, 32>(a, out, stream)
-               : group == 64 ? launch_small<__half, 64>(a, out, stream)
-                             : launch_small<__half, 128>(a, out, stream);
-    return group == 32   ? launch_small<__nv_bfloat16, 32>(a, out, stream)
-           : group == 64 ? launch_small<__nv_bfloat16, 64>(a, out, stream)
-                         : launch_small<__nv_bfloat16, 128>(a, out, stream);
+        return group == 32   ? launch_small_scale<__half, 32>(a, out, stream)
+               : group == 64 ? launch_small_scale<__half, 64>(a, out, stream)
+                             : launch_small_scale<__half, 128>(a, out, stream);
+    return group == 32   ? launch_small_scale<__nv_bfloat16, 32>(a, out, stream)
+           : group == 64 ? launch_small_scale<__nv_bfloat16, 64>(a, out, stream)
+                         : launch_small_scale<__nv_bfloat16, 128>(a, out, stream);
 }
 
 }  // namespace moedc_host

@@ -144,13 +144,14 @@ def _p(t: torch.Tensor | None):
 # The current stream's handle without building a Stream object, which takes
 # longer (2.9 us) than the rest of a small call's marshalling.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
 
 
 def _stream(stream: torch.cuda.Stream | None):
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream is not None:
-        return _raw_stream(torch.cuda.current_device())
+        return _raw_stream(_device())
     return torch.cuda.current_stream().cuda_stream
 
 

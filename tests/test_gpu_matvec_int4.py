@@ -20,7 +20,7 @@ def _check(T, E, K, N, Kd, group, dtype, swiglu=False, zeros=False, align=1, mas
     g = torch.Generator().manual_seed(seed + T + N)
     if big:       # enough outputs for the form with prepared x
         per = (min(E, T * K) + T * K // 8) * (2 if swiglu else 1) * Kd // 2
-        N += (11 << 20) // per
+        N += (26 << 20) // per + 1
         rows = moedc.moedc_sort_rows(T, K, E, align)
         assert moedc.moedc_matvec_int4_workspace_bytes(T, Kd, E, N, int(swiglu), rows) > 0
     if idx is None:
@@ -166,7 +166,7 @@ def test_strided_rows_other_stream_and_equal_bits():
 def test_infinite_inputs_stay_in_their_row(big):
     g = torch.Generator().manual_seed(3)
     x = torch.randn(5, 256, generator=g).to(torch.bfloat16).cuda()
-    wq, s, _ = _weights(g, 1, 90000 if big else 40, 256, 64, False, torch.bfloat16)
+    wq, s, _ = _weights(g, 1, 220000 if big else 40, 256, 64, False, torch.bfloat16)
     want = moedc.matvec_int4(x, wq[0], s[0])
     x[2, 100] = float("nan")
     x[3, 7] = float("inf")
@@ -181,7 +181,7 @@ def test_infinite_inputs_stay_in_their_row(big):
 def test_rows_past_the_end_and_bad_sources_are_reported(big):
     g = torch.Generator().manual_seed(4)
     x = torch.randn(4, 128, generator=g).to(torch.bfloat16).cuda()
-    n = 90000 if big else 20
+    n = 220000 if big else 20
     wq, s, _ = _weights(g, 2, n, 128, 64, False, torch.bfloat16)
     offsets = torch.tensor([0, 3, 6], dtype=torch.int32).cuda()
     counts = torch.tensor([3, 3], dtype=torch.int32).cuda()
@@ -229,7 +229,7 @@ def test_refusals():
 def test_a_wait_that_runs_out_is_reported_and_the_next_call_is_clean():
     g = torch.Generator().manual_seed(5)
     x = torch.randn(3, 512, generator=g).to(torch.bfloat16).cuda()
-    wq, s, _ = _weights(g, 1, 50000, 512, 64, False, torch.bfloat16)
+    wq, s, _ = _weights(g, 1, 110000, 512, 64, False, torch.bfloat16)
     want = moedc.matvec_int4(x, wq, s)
     torch.cuda.synchronize()
     status = torch.zeros(1, dtype=torch.int32).cuda()
