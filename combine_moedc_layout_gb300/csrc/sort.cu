@@ -145,6 +145,8 @@ __device__ __forceinline__ void sort_rows(const SortArgs& a, const U* __restrict
     if (dropped) raise_status(a.status, MOEDC_ERR_CAPACITY);
 }
 
+constexpr int kSortAhead = 64 << 20;       // bytes of x brought to L2 ahead, at most
+
 // After the layout: slots and counts from memory.
 template <typename U>
 __global__ void __launch_bounds__(kSortThreads)
@@ -152,6 +154,17 @@ sort_kernel(SortArgs a, const U* __restrict__ x, const int32_t* __restrict__ top
             const int32_t* __restrict__ slot, const int32_t* __restrict__ counts, U* __restrict__ sorted)
 {
     extern __shared__ int32_t s_mem[];   // off [E + 1], pad [E + 1], cnt [E]
+    // While the layout runs, the token rows come to L2 (as many as may stay there).  No
+    // value is used before the wait.
+    if (a.units) {
+        const int64_t lines = ((int64_t)a.units * (int)sizeof(U) + 127) / 128;
+        const int64_t most = min(a.T * lines, (int64_t)kSortAhead / 128);
+        for (int64_t i = (int64_t)blockIdx.x * kSortThreads + threadIdx.x; i < most; i += (int64_t)gridDim.x * kSortThreads) {
+            const int64_t t = i / lines;
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                reinterpret_cast<const char*>(x + t * a.ldx) + (i - t * lines) * 128));
+        }
+    }
     pdl_enter();
     int32_t *s_off = s_mem, *s_pad = s_off + a.E + 1, *s_cnt = s_pad + a.E + 1;
     for (int e = threadIdx.x; e < a.E; e += kSortThreads) s_cnt[e] = min(max(__ldg(counts + e), 0), a.rows);
