@@ -489,6 +489,7 @@ __device__ __forceinline__ void mv_consume(const MatvecArgs& a, const MvWarp& w,
         }
         next.load(rows, q, groups - q, w.whole, zeros);
         mbar_wait(full + ring.slot, ring.phase, abort);
+        __syncwarp();   // the products want the warp's lanes together, a wait may part them
         const uint8_t* st = smem + ring.slot * a.stage_bytes;
         // a part without channels left in the last stage has no records of x there either
         if (left >= kMvChunk) mv_stage<GROUP, NT, true>(st, w.ow, w.ox, w.oc, now, 8, acc);
