@@ -28,93 +28,25 @@
 // 2^-39 of it below.  The group's sum is then scaled in binary32, so neither
 // weights nor scales are ever rounded.  A row of x with an infinity or a NaN
 // gives NaN.
-// tcgen05 reads its operands from shared or tensor memory, which would cost
-// every weight a 2-byte store and a 2-byte read on the way: at the HBM rate
-// 93 + 93 bytes per SM and clock, more than shared memory moves (128).
+// For few rows tcgen05 is the slower form: a product with 16 columns of x takes it
+// 120 clocks for 16 channels of 128 weight rows, and every stage four hand-overs (16
+// tokens 241 us, 128 tokens 930 us in the shapes below); where experts have many rows
+// it is taken (matvec_int4_tc.cu).
 #include <climits>
 #include <cmath>
 #include <mutex>
-#include <type_traits>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
-#include "matvec_int4.cuh"
+#include "matvec_int4_ring.cuh"
 
 namespace moedc {
 
 constexpr int kMvConsumers = 16;                       // warps
 constexpr int kMvThreads = (kMvConsumers + 1) * kWarp;
 constexpr int kMvRows = kMvConsumers * 16;             // weight rows x parts of K in a stage
-constexpr int kMvChunk = 256;                          // channels of one part in a stage
 constexpr int kMvW = kMvRows * kMvChunk / 2;           // a stage's weights
 constexpr int kMvTokens = 32;                          // rows of x x parts of K, at most
 constexpr int kMvMaxStages = 6;
 constexpr int kMvRed = kMvConsumers * 8 * kWarp * (int)sizeof(float);
-constexpr unsigned long long kMvWaitNs = 200000000ull; // bound of every wait
-// A record of x: 256 channels in f16, then 2^-24 times the sum of each of up to
-// eight groups, then 2^12 / scale.  576 bytes apart, the rows that a quarter-warp
-// reads lie in different halves of the banks.
-constexpr int kMvRecord = kMvChunk * 2 + 64;
-
-// ---------------------------------------------------------------- mbarriers
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p)
-{
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ void mbar_init(uint64_t* b, int count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* b)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect(uint64_t* b, int bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint64_t* b, int parity)
-{
-    uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n"
-                 " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-                 " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ unsigned long long globaltimer()
-{
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-// Bounded: false when the wait ran out or another one of the block did
-// (*abort).  The callers then go on without waiting, so that every barrier of
-// the block is still met and the kernel ends; the status word tells.
-__device__ __noinline__ bool mbar_wait_slow(uint64_t* b, int parity, volatile int* abort)
-{
-    // the timer is read only once the wait is a long one: reading it takes longer than
-    // most waits
-    unsigned long long t0 = 0;
-    if (*abort) return false;
-    for (int i = 0; ; ++i) {
-        if (mbar_try(b, parity)) return true;
-        if (i % 1024 != 1023) continue;
-        if (*abort) return false;
-        const unsigned long long now = globaltimer();
-        if (t0 == 0) t0 = now;
-        else if (now - t0 > kMvWaitNs) break;
-    }
-    *abort = 1;
-    return false;
-}
-__device__ __forceinline__ bool mbar_wait(uint64_t* b, int parity, volatile int* abort)
-{
-    return mbar_try(b, parity) || mbar_wait_slow(b, parity, abort);
-}
-
 // ---------------------------------------------------------- tensor products
 
 __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2,
@@ -145,113 +77,6 @@ template <int N> __device__ __forceinline__ void lds_run(const uint8_t* at, floa
     }
 }
 
-// Scales and zero points of one warp's rows g and g + 8 for one stage, in
-// registers as they come from memory.
-template <int GROUP, typename S> struct MvScales {
-    static constexpr int n = kMvChunk / GROUP;                 // groups
-    static constexpr int words = n * (int)sizeof(S) / 4;
-    static constexpr int zwords = n == 8 ? 2 : 1;
-    uint32_t s[2][words];
-    uint32_t z[2][zwords];
-
-    static __device__ __forceinline__ void load_row(uint32_t (&s)[words], const S* p, bool whole, int have)
-    {
-        if (whole) {
-            if constexpr (words == 1) {
-                s[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-            } else if constexpr (words == 2) {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-                s[0] = v.x, s[1] = v.y;
-            } else {
-#pragma unroll
-                for (int i = 0; i < words / 4; ++i) {
-                    const uint4 v = __ldg(reinterpret_cast<const uint4*>(p) + i);
-                    s[4 * i] = v.x, s[4 * i + 1] = v.y, s[4 * i + 2] = v.z, s[4 * i + 3] = v.w;
-                }
-            }
-        } else if constexpr (sizeof(S) == 4) {
-#pragma unroll
-            for (int i = 0; i < n; ++i) s[i] = __float_as_uint(__ldg(reinterpret_cast<const float*>(p) + min(i, have - 1)));
-        } else {
-#pragma unroll
-            for (int i = 0; i < n; i += 2) {
-                const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
-                s[i / 2] = (uint32_t)__ldg(h + min(i, have - 1)) | (uint32_t)__ldg(h + min(i + 1, have - 1)) << 16;
-            }
-        }
-    }
-    static __device__ __forceinline__ void load_zeros(uint32_t (&z)[zwords], const uint8_t* p, bool whole, int have)
-    {
-        if (whole) {
-            if constexpr (n == 2) {
-                z[0] = __ldg(reinterpret_cast<const uint16_t*>(p));
-            } else if constexpr (n == 4) {
-                z[0] = __ldg(reinterpret_cast<const uint32_t*>(p));
-            } else {
-                const uint2 v = __ldg(reinterpret_cast<const uint2*>(p));
-                z[0] = v.x, z[1] = v.y;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < zwords; ++i) z[i] = 0;
-#pragma unroll
-            for (int i = 0; i < n; ++i) z[i / 4] |= (uint32_t)__ldg(p + min(i, have - 1)) << (8 * (i % 4));
-        }
-    }
-    // Of a unit's two rows: where their scales and zero points begin.  Without zero
-    // points z stays 8.
-    struct Rows {
-        const S* s[2];
-        const uint8_t* z[2];
-    };
-    __device__ __forceinline__ void clear()
-    {
-#pragma unroll
-        for (int r = 0; r < 2; ++r)
-#pragma unroll
-            for (int i = 0; i < zwords; ++i) z[r][i] = 0x08080808u;
-    }
-    // the groups from q on; `have` of them exist (all, where they come as one load)
-    __device__ __forceinline__ void load(const Rows& rows, int q, int have, bool whole, bool zeros)
-    {
-        load_row(s[0], rows.s[0] + q, whole, have);
-        load_row(s[1], rows.s[1] + q, whole, have);
-        if (zeros) {
-            load_zeros(z[0], rows.z[0] + q, whole, have);
-            load_zeros(z[1], rows.z[1] + q, whole, have);
-        }
-    }
-    __device__ __forceinline__ float scale(int row, int q) const
-    {
-        if constexpr (sizeof(S) == 4) {
-            return __uint_as_float(s[row][q]);
-        } else {
-            const uint32_t w = s[row][q / 2];
-            if constexpr (std::is_same<S, __nv_bfloat16>::value)
-                return __uint_as_float(q % 2 ? w & 0xffff0000u : w << 16);
-            else
-                return __half2float(__ushort_as_half((unsigned short)(q % 2 ? w >> 16 : w & 0xffffu)));
-        }
-    }
-    // minus the zero point: 2^23 + z is a binary32 number whose low bits are z
-    __device__ __forceinline__ float minus_zero(int row, int q) const
-    {
-        return 8388608.0f - __uint_as_float(__byte_perm(z[row][q / 4], 0x4b000000u, 0x7540 | (q % 4)));
-    }
-    // the zero point as the weights' f16 subnormals, of the low nibbles
-    __device__ __forceinline__ uint32_t zero_f16(int row, int q) const
-    {
-        return ((z[row][q / 4] >> (8 * (q % 4))) & 0xffu) * 0x00010001u;
-    }
-};
-
-__device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b)
-{
-    uint32_t r;
-    asm("sub.rn.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
-    return r;
-}
-
 // Whether the zero point is subtracted from the weights (8 instructions per 32
 // channels) instead of from the sums (6 per group and eight rows).
 constexpr bool mv_subtract(int group, int nt) { return 8 * (group / 32) < 6 * nt; }
@@ -263,7 +88,7 @@ constexpr bool mv_subtract(int group, int nt) { return 8 * (group / 32) < 6 * nt
 //   c    place of the sums of x row 2t
 template <int GROUP, int NT, bool FULL, typename S>
 __device__ __forceinline__ void mv_stage(const uint8_t* st, uint32_t w, uint32_t x, uint32_t c,
-                                         const MvScales<GROUP, S>& sz, int steps, float (&acc)[NT][4])
+                                         const MvScales<GROUP, S, 2>& sz, int steps, float (&acc)[NT][4])
 {
     constexpr int kPer = GROUP / 32;       // 32-channel steps of a group
     constexpr int kGroups = kMvChunk / GROUP;
@@ -337,18 +162,6 @@ __device__ __forceinline__ void mv_stage(const uint8_t* st, uint32_t w, uint32_t
     }
 }
 
-// Where a stage's slot and phase go round the ring.
-struct MvRing {
-    int slot = 0, phase = 0;
-    __device__ __forceinline__ void next(int stages)
-    {
-        if (++slot == stages) {
-            slot = 0;
-            phase ^= 1;
-        }
-    }
-};
-
 // The unit's end: the parts of K added, the epilogue, the outputs.
 template <int NT>
 __device__ __forceinline__ void mv_store(const MatvecArgs& a, const MvUnit& u, float* s_red,
@@ -394,25 +207,26 @@ __device__ __forceinline__ void mv_store(const MatvecArgs& a, const MvUnit& u, f
         }
 }
 
-// Records of x, a warp each: eight channels a lane, brought into f16 range,
+// Records of x, by row of x (then one of zeros) or by packed row, a warp each: eight channels a lane, brought into f16 range,
 // summed by group, and stored in the order of the weights' registers, channels
 // (0,4), (1,5) 2^-4, (2,6), (3,7) 2^-4.
 template <typename T>
 __global__ void __launch_bounds__(256)
-matvec_x_kernel(const T* __restrict__ x, int64_t ldx, int x_rows, int Kd, int group,
-                uint8_t* __restrict__ records)
+matvec_x_kernel(const __grid_constant__ MatvecArgs a, bool packed, int group, uint8_t* __restrict__ records)
 {
     pdl_enter();
     const int lane = threadIdx.x % kWarp;
-    const int chunks = (Kd + kMvChunk - 1) / kMvChunk;
-    const int64_t n = (int64_t)(x_rows + 1) * chunks;
+    const int chunks = (a.Kd + kMvChunk - 1) / kMvChunk;
+    const int64_t n = (packed ? (int64_t)a.rows : (int64_t)a.x_rows + 1) * chunks;
     for (int64_t i = (int64_t)blockIdx.x * 8 + threadIdx.x / kWarp; i < n; i += (int64_t)gridDim.x * 8) {
-        const int64_t r = i / chunks;
+        int64_t r = i / chunks;
         const int k = (int)(i - r * chunks) * kMvChunk + lane * 8;
+        bool bad = false;   // told by the kernel that knows which rows count
+        if (packed) r = x_row(a, (int)r, bad);
         Pack<T, 8> h;
         float f[8] = {};
-        if (r < x_rows && k < Kd) {
-            h = *reinterpret_cast<const Pack<T, 8>*>(x + r * ldx + k);
+        if (r < a.x_rows && k < a.Kd) {
+            h = *reinterpret_cast<const Pack<T, 8>*>(static_cast<const T*>(a.x) + r * a.ldx + k);
 #pragma unroll
             for (int j = 0; j < 8; ++j) f[j] = to_f32(h.v[j]);
         }
@@ -453,7 +267,7 @@ struct MvWarp {
 // last one's, and nothing uses them.
 template <int GROUP, typename S>
 __device__ __forceinline__ void mv_rows(const MatvecArgs& a, const MvWarp& w, const MvUnit& u, int groups,
-                                        typename MvScales<GROUP, S>::Rows& rows)
+                                        typename MvScales<GROUP, S, 2>::Rows& rows)
 {
     const int n0 = min(u.n0 + w.row, a.N - 1);
     const int n1 = a.swiglu ? n0 + a.N : min(u.n0 + w.half + w.row, a.N - 1);
@@ -469,8 +283,8 @@ __device__ __forceinline__ void mv_rows(const MatvecArgs& a, const MvWarp& w, co
 template <int GROUP, int NT, typename S>
 __device__ __forceinline__ void mv_consume(const MatvecArgs& a, const MvWarp& w, const uint8_t* smem, MvRing& ring, uint64_t* full,
                                            uint64_t* empty, volatile int* abort, int ksteps, int groups,
-                                           bool more, const MvUnit& un, MvScales<GROUP, S>& now,
-                                           typename MvScales<GROUP, S>::Rows& rows, float (&acc)[NT][4])
+                                           bool more, const MvUnit& un, MvScales<GROUP, S, 2>& now,
+                                           typename MvScales<GROUP, S, 2>::Rows& rows, float (&acc)[NT][4])
 {
     constexpr int kGroups = kMvChunk / GROUP;
 #pragma unroll
@@ -481,7 +295,7 @@ __device__ __forceinline__ void mv_consume(const MatvecArgs& a, const MvWarp& w,
     const int last = w.whole ? groups - kGroups : groups - 1;    // the last group to begin a load at
     int left = a.Kd - w.part * kMvChunk, q = w.part * kGroups;
     for (int s = ksteps; s > 0; --s, left -= kMvChunk << a.lk) {
-        MvScales<GROUP, S> next = now;
+        MvScales<GROUP, S, 2> next = now;
         q = min(q + (kGroups << a.lk), last);
         if (s == 1) {
             q = min(w.part * kGroups, last);
@@ -553,14 +367,12 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__
         w.ow = part * half * 128 + w.row * 128 + (g << 4) + t * 4;
         w.ox = kMvW + (part * a.chunk_rows + g) * kMvRecord + t * 16;
         w.oc = kMvW + (part * a.chunk_rows + 2 * t) * kMvRecord + kMvChunk * 2;
-        w.whole = groups % kGroups == 0 &&
-                  reinterpret_cast<uintptr_t>(a.scales) % (kGroups * sizeof(S) < 16 ? kGroups * sizeof(S) : 16) == 0 &&
-                  reinterpret_cast<uintptr_t>(a.zeros) % kGroups == 0;
+        w.whole = MvScales<GROUP, S, 2>::aligned_groups(a, groups);
         int unit = blockIdx.x;
         if (unit < units) {
             MvUnit u = mv_unit(a, s_pre, s_beg, s_end, tiles, tile_n, unit);
-            MvScales<GROUP, S> now;
-            typename MvScales<GROUP, S>::Rows rows;
+            MvScales<GROUP, S, 2> now;
+            typename MvScales<GROUP, S, 2>::Rows rows;
             now.clear();
             mv_rows<GROUP, S>(a, w, u, groups, rows);
             const int q0 = min(part * kGroups, w.whole ? groups - kGroups : groups - 1);
@@ -637,11 +449,13 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__
 }  // namespace moedc
 
 namespace moedc_host {
+
 namespace {
 
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
+bool tensor_map(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int dims,
+                const cuuint64_t* size, const cuuint64_t* stride, const cuuint32_t* box)
 {
-    static PFN_cuTensorMapEncodeTiled_v12000 fn = [] {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
         void* p = nullptr;
         cudaDriverEntryPointQueryResult found;
         if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
@@ -649,10 +463,31 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder()
             p = nullptr;
         return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
     }();
-    return fn;
+    if (!encode) return false;
+    const cuuint32_t elem[3] = {1, 1, 1};
+    return encode(map, type, dims, const_cast<void*>(base), size, stride, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-constexpr int kMvSmem = 227 * 1024;
+}  // namespace
+
+bool matvec_weight_map(CUtensorMap* map, const void* wq, int Kd, int64_t rows, int box_rows)
+{
+    const cuuint64_t size[2] = {(cuuint64_t)Kd / 2, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)Kd / 2};
+    const cuuint32_t box[2] = {moedc::kMvChunk / 2, (cuuint32_t)box_rows};
+    return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, CU_TENSOR_MAP_SWIZZLE_128B, wq, 2, size, stride, box);
+}
+
+bool matvec_x_maps(CUtensorMap* channels, CUtensorMap* factors, const uint8_t* records, int chunks, int rows, int box_rows)
+{
+    const cuuint64_t size[3] = {moedc::kMvRecord / 2, (cuuint64_t)chunks, (cuuint64_t)rows};
+    const cuuint64_t stride[2] = {moedc::kMvRecord, (cuuint64_t)moedc::kMvRecord * chunks};
+    const cuuint32_t many[3] = {64, 1, (cuuint32_t)box_rows}, one[3] = {8, 1, (cuuint32_t)box_rows};
+    return tensor_map(channels, CU_TENSOR_MAP_DATA_TYPE_UINT16, CU_TENSOR_MAP_SWIZZLE_128B, records, 3, size, stride, many) &&
+           tensor_map(factors, CU_TENSOR_MAP_DATA_TYPE_UINT16, CU_TENSOR_MAP_SWIZZLE_NONE, records, 3, size, stride, one);
+}
+
+namespace {
 
 // Parts of K and rows of a unit: the pair with the least of
 //   rounds of units * (stages of a unit * cost of a stage + cost of a unit)
@@ -687,7 +522,7 @@ void mv_shape(moedc::MatvecArgs& a, int blocks)
 }
 
 template <int GROUP, typename S, int NTMAX>
-int launch_matvec(moedc::MatvecArgs a, const void* wq, void* out, cudaStream_t stream)
+int launch_matvec(moedc::MatvecArgs a, void* out, cudaStream_t stream)
 {
     auto* k = moedc::matvec_int4_kernel<GROUP, S, NTMAX>;
     static std::once_flag once;
@@ -704,18 +539,9 @@ int launch_matvec(moedc::MatvecArgs a, const void* wq, void* out, cudaStream_t s
     if (a.stages > moedc::kMvMaxStages) a.stages = moedc::kMvMaxStages;
     const size_t smem = (size_t)a.stages * a.stage_bytes + fixed;
 
-    const auto encode = tensor_map_encoder();
-    if (!encode) return MOEDC_ERR_CUDA;
-    const int wrows = a.swiglu ? 2 * a.N : a.N;
     const int part_rows = moedc::kMvRows >> a.lk;
     CUtensorMap map;
-    const cuuint64_t dims[2] = {(cuuint64_t)a.Kd / 2, (cuuint64_t)a.E * wrows};
-    const cuuint64_t strides[1] = {(cuuint64_t)a.Kd / 2};
-    const cuuint32_t box[2] = {moedc::kMvChunk / 2, (cuuint32_t)part_rows / 2};
-    const cuuint32_t elem[2] = {1, 1};
-    if (encode(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(wq), dims, strides, box, elem,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+    if (!matvec_weight_map(&map, a.wq, a.Kd, (int64_t)a.E * (a.swiglu ? 2 : 1) * a.N, part_rows / 2))
         return MOEDC_ERR_CUDA;
 
     const int tile_n = part_rows / (a.swiglu ? 2 : 1);
@@ -728,29 +554,28 @@ int launch_matvec(moedc::MatvecArgs a, const void* wq, void* out, cudaStream_t s
 }
 
 template <int GROUP, typename S>
-int launch_matvec_rows(const moedc::MatvecArgs& a, const void* wq, void* out, cudaStream_t stream)
+int launch_matvec_rows(const moedc::MatvecArgs& a, void* out, cudaStream_t stream)
 {
-    return a.chunk_rows == 8    ? launch_matvec<GROUP, S, 1>(a, wq, out, stream)
-           : a.chunk_rows == 16 ? launch_matvec<GROUP, S, 2>(a, wq, out, stream)
-                                : launch_matvec<GROUP, S, 4>(a, wq, out, stream);
+    return a.chunk_rows == 8    ? launch_matvec<GROUP, S, 1>(a, out, stream)
+           : a.chunk_rows == 16 ? launch_matvec<GROUP, S, 2>(a, out, stream)
+                                : launch_matvec<GROUP, S, 4>(a, out, stream);
 }
 
 template <typename S>
-int launch_matvec_group(const moedc::MatvecArgs& a, int group, const void* wq, void* out, cudaStream_t stream)
+int launch_matvec_group(const moedc::MatvecArgs& a, int group, void* out, cudaStream_t stream)
 {
-    return group == 32   ? launch_matvec_rows<32, S>(a, wq, out, stream)
-           : group == 64 ? launch_matvec_rows<64, S>(a, wq, out, stream)
-                         : launch_matvec_rows<128, S>(a, wq, out, stream);
+    return group == 32   ? launch_matvec_rows<32, S>(a, out, stream)
+           : group == 64 ? launch_matvec_rows<64, S>(a, out, stream)
+                         : launch_matvec_rows<128, S>(a, out, stream);
 }
 
 template <typename T>
-int launch_matvec_x(const void* x, int64_t ldx, int x_rows, int Kd, int group, uint8_t* records, cudaStream_t stream)
+int launch_matvec_x(const moedc::MatvecArgs& a, bool packed, int group, uint8_t* records, cudaStream_t stream)
 {
-    const int64_t n = ((int64_t)x_rows + 1) * ((Kd + moedc::kMvChunk - 1) / moedc::kMvChunk);
+    const int64_t n = (packed ? (int64_t)a.rows : (int64_t)a.x_rows + 1) * ((a.Kd + moedc::kMvChunk - 1) / moedc::kMvChunk);
     const int64_t want = (n + 7) / 8, most = 8 * (int64_t)sm_count();
     clear_stale_error();
-    launch(moedc::matvec_x_kernel<T>, (int)(want < most ? want : most), 256, 0, stream,
-           static_cast<const T*>(x), ldx, x_rows, Kd, group, records);
+    launch(moedc::matvec_x_kernel<T>, (int)(want < most ? want : most), 256, 0, stream, a, packed, group, records);
     return launch_status();
 }
 
@@ -761,7 +586,10 @@ extern "C" size_t moedc_matvec_int4_workspace_bytes(int x_rows, int Kd, int E, i
 {
     if (x_rows < 0 || Kd < 1 || E < 1 || N < 1 || rows < 1 || (flags & ~MOEDC_SWIGLU) != 0) return 0;
     if (moedc_host::matvec_small_takes(Kd, E, N, flags != 0, rows)) return 0;
-    return ((size_t)x_rows + 1) * ((Kd + (size_t)moedc::kMvChunk - 1) / moedc::kMvChunk) * moedc::kMvRecord;
+    // by row of x or, where experts have many rows, by packed row
+    size_t records = (size_t)x_rows + 1;
+    if (moedc_host::matvec_tc_takes(E, rows, 128) && (size_t)rows > records) records = (size_t)rows;
+    return records * ((Kd + (size_t)moedc::kMvChunk - 1) / moedc::kMvChunk) * moedc::kMvRecord;
 }
 
 extern "C" int moedc_matvec_int4(const void* x, int64_t ldx, int dtype, int x_rows, int Kd,
@@ -818,12 +646,16 @@ extern "C" int moedc_matvec_int4(const void* x, int64_t ldx, int dtype, int x_ro
     if (small) return launch_matvec_small(a, group, out, stream);
     uint8_t* records = static_cast<uint8_t*>(workspace);
     a.records = records;
-    mv_shape(a, sm_count());
+    // rows that can be filled: `rows` counts what alignment leaves empty as well
+    const int64_t filled = src ? (int64_t)x_rows * top_k : rows;
+    const bool tc = matvec_tc_takes(E, rows, 128) && matvec_tc_takes(E, (int)(filled < rows ? filled : rows), group);
+    if (!tc) mv_shape(a, sm_count());
     const int st = dtype == MOEDC_F16
-                       ? launch_matvec_x<__half>(x, ldx, x_rows, Kd, group, records, stream)
-                       : launch_matvec_x<__nv_bfloat16>(x, ldx, x_rows, Kd, group, records, stream);
+                       ? launch_matvec_x<__half>(a, tc, group, records, stream)
+                       : launch_matvec_x<__nv_bfloat16>(a, tc, group, records, stream);
     if (st != MOEDC_OK) return st;
-    return scale_dtype == MOEDC_F32   ? launch_matvec_group<float>(a, group, wq, out, stream)
-           : scale_dtype == MOEDC_F16 ? launch_matvec_group<__half>(a, group, wq, out, stream)
-                                      : launch_matvec_group<__nv_bfloat16>(a, group, wq, out, stream);
+    if (tc) return launch_matvec_tc(a, group, out, stream);
+    return scale_dtype == MOEDC_F32   ? launch_matvec_group<float>(a, group, out, stream)
+           : scale_dtype == MOEDC_F16 ? launch_matvec_group<__half>(a, group, out, stream)
+                                      : launch_matvec_group<__nv_bfloat16>(a, group, out, stream);
 }

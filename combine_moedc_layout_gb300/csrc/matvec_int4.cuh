@@ -1,4 +1,4 @@
-// What the two kernels of the 4-bit expert products share: arguments and units of
+// What the kernels of the 4-bit expert products share: arguments and units of
 // work.
 #pragma once
 
