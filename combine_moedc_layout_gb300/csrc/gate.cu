@@ -8,6 +8,10 @@
 //   sigmoid            dl_e = scale * d_e * s_e (1 - s_e)
 //   sigmoid over C     dl_e = scale * s_e (1 - s_e) / S * (d_e - sum_C p d)
 // and only the softmax over all experts reaches outside C.
+//
+// Few tokens cost a launch.  Many are bound by instruction issue (ALU 56%): 32768
+// tokens of 256 binary32 experts, top 8, take 22 us, their gradient 16 us, where the
+// bytes alone (34 and 71 MB) would take 5 and 11.
 #include <cfloat>
 #include <climits>
 

@@ -5,7 +5,10 @@
 //   sort         rows[row[t][k]] = x[t]
 //   unsort       y[t] = sum_k w[t][k] rows[row[t][k]]   (w = 1: sort's gradient)
 //   unsort_grad  drows[row[t][k]] = w[t][k] dy[t],  dw[t][k] = <dy[t], rows[row[t][k]]>
-// All four move rows: HBM traffic bounds them.
+// All four move rows: HBM traffic bounds them.  4096 tokens, top 8 of 256 experts, 7168
+// channels in bf16: sort 92 us by itself (under the counts before it, which it
+// overlaps, 183 us with unsort), unsort 77-79 us (529 MB, 6.7 TB/s), unsort_grad
+// 148-161 us (998 MB).
 #include <climits>
 
 #include "block_layout.cuh"
@@ -302,7 +305,8 @@ unsort_kernel(const T* __restrict__ sorted, int rows, int H, const int32_t* __re
 
 // A block takes entries; dy is read again for each of a token's, from L2.  One
 // 16-byte unit at a time keeps 32 registers and 64 warps an SM (two: 48 registers,
-// 170 us instead of 148 at 4096 tokens, top-8, 7168 channels in bf16).  The rows that no entry reaches are cleared at the end.
+// 170 us instead of 148 at 4096 tokens, top-8, 7168 channels in bf16).  The rows that no
+// entry reaches are cleared at the end.
 template <typename T, int V>
 __global__ void __launch_bounds__(kSortThreads, 8)
 unsort_grad_kernel(const T* __restrict__ dy, int64_t lddy, const T* __restrict__ sorted, int rows,
