@@ -215,9 +215,9 @@ __device__ __forceinline__ void mv_store(const MatvecArgs& a, const MvUnit& u, f
         }
 }
 
-// Records of x, by row of x (then one of zeros) or by packed row, a warp each: eight channels a lane, brought into f16 range,
-// summed by group, and stored in the order of the weights' registers, channels
-// (0,4), (1,5) 2^-4, (2,6), (3,7) 2^-4.
+// Records of x, by row of x (then one of zeros) or by packed row, a warp each: eight
+// channels a lane, brought into f16 range, summed by group, and stored in the order of
+// the weights' registers, channels (0,4), (1,5) 2^-4, (2,6), (3,7) 2^-4.
 template <typename T>
 __global__ void __launch_bounds__(256)
 matvec_x_kernel(const __grid_constant__ MatvecArgs a, bool packed, int group, uint8_t* __restrict__ records)
