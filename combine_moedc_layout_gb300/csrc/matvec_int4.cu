@@ -29,7 +29,7 @@
 // weights nor scales are ever rounded.  A row of x with an infinity or a NaN
 // gives NaN.
 //
-// 16 tokens, top 8 of 128 experts, 2 x 1024 x 6144 with SwiGLU, groups of 128: 104-107
+// 16 tokens, top 8 of 128 experts, 2 x 1024 x 6144 with SwiGLU, groups of 128: 104-111
 // us (535 MB, 5.1 TB/s); 128 tokens, top 8 of 288 experts, 2048 x 7168, groups of 64:
 // 462 us, with zero points 490-502 us (2255 MB, 4.6 TB/s).  The stream alone would take
 // 93 and 335 us, the products alone 107 and 407: unpacking and the latencies of shared
