@@ -412,7 +412,10 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__
         int issued = 0;
         bool bad = false;
         const int chunks = (a.Kd + kMvChunk - 1) / kMvChunk;
-        for (int unit = blockIdx.x; unit < units && !s_abort; unit += gridDim.x) {
+        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+            // one answer for the warp: a consumer may set the flag while its lanes are apart, and
+            // the votes below want all of them
+            if (__any_sync(0xffffffffu, s_abort != 0)) break;
             const MvUnit u = mv_unit(a, s_pre, s_beg, s_end, tiles, tile_n, unit);
             const int wrow = u.e * wrows + u.n0;
             const int r = lane >> a.lk, p = lane & (wk - 1);       // this lane's record
