@@ -18,23 +18,24 @@
 // The products run on the tensor cores with the weights as the 16-row operand
 // and eight rows of x as the other, both in f16 with binary32 sums.  The ALU,
 // which masks and shifts, issues every other clock and is the pipe that fills
-// first, so a weight costs it one mask and a quarter of a shift and nothing else:
+// first, so a weight costs it one mask and a quarter of a shift:
 // a nibble in the low bits of an f16 is the subnormal q * 2^-24 (one nibble
-// higher q * 2^-20, with x scaled by 2^-4 to match), exact as it stands.  The
-// zero point is taken out of the group's sum, sum (q - z) x = sum q x - z sum x,
-// or, where groups are short and rows many, out of the weights.
+// higher q * 2^-20, with x scaled by 2^-4 to match), exact as it stands, and the
+// zero point a subtraction of two such numbers, exact as well.  (Taken out of the
+// group's sum instead, sum q x - z sum x, it would cost less, 104 against 111 us and
+// 502 against 528 in the shapes below, but a large value of x whose weight is at the
+// zero point would then cancel in binary32 and take the small ones' bits along.)
 // x is brought into f16 per row and stage by a power of two that puts its
 // largest value into [2^14, 2^15): exact down to 2^-28 of that value, and
 // 2^-39 of it below.  The group's sum is then scaled in binary32, so neither
 // weights nor scales are ever rounded.  A row of x with an infinity or a NaN
 // gives NaN.
 //
-// 16 tokens, top 8 of 128 experts, 2 x 1024 x 6144 with SwiGLU, groups of 128: 104-111
-// us (535 MB, 5.1 TB/s); 128 tokens, top 8 of 288 experts, 2048 x 7168, groups of 64:
-// 462 us, with zero points 490-502 us (2255 MB, 4.6 TB/s).  The stream alone would take
-// 93 and 335 us, the products alone 107 and 407: unpacking and the latencies of shared
-// memory and of the matrix instructions bound it (issue 57%, ALU 48%), and the two do
-// not overlap fully.
+// 16 tokens, top 8 of 128 experts, 2 x 1024 x 6144 with SwiGLU, groups of 128: 111
+// us (535 MB, 4.8 TB/s); 128 tokens, top 8 of 288 experts, 2048 x 7168, groups of 64:
+// with zero points 528 us (2255 MB, 4.3 TB/s).  The stream alone would take 93 and 335
+// us: unpacking and the latencies of shared memory and of the matrix instructions bound
+// it.
 //
 // For few rows tcgen05 is the slower form: a product with 16 columns of x takes it
 // 120 clocks for 16 channels of 128 weight rows, and every stage four hand-overs (16
@@ -70,57 +71,24 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
 // plain loads, so that the compiler may order them between the waits as it likes
 template <typename V> __device__ __forceinline__ V lds(const uint8_t* at) { return *reinterpret_cast<const V*>(at); }
 
-// N neighbouring floats, 16 bytes at most at a time
-template <int N> __device__ __forceinline__ void lds_run(const uint8_t* at, float (&v)[N])
-{
-    if constexpr (N == 2) {
-        const float2 r = lds<float2>(at);
-        v[0] = r.x, v[1] = r.y;
-    } else {
-#pragma unroll
-        for (int i = 0; i < N; i += 4) {
-            const float4 r = lds<float4>(at + i * 4);
-            v[i] = r.x, v[i + 1] = r.y, v[i + 2] = r.z, v[i + 3] = r.w;
-        }
-    }
-}
-
-// Whether the zero point is subtracted from the weights (8 instructions per 32
-// channels) instead of from the sums (6 per group and eight rows).
-constexpr bool mv_subtract(int group, int nt) { return 8 * (group / 32) < 6 * nt; }
-
 // One stage of one warp: its 16 weight rows x 256 channels with 8 NT rows of x.
 //   w    place of row g at word t (128 bytes a row, 16-byte pieces permuted by the
 //        row's low three bits); the warp's other eight rows lie kMvW / 2 further
 //   x    place of row g's record at its words t
-//   c    place of the sums of x row 2t
+//   c    place of the factor of x row 2t
 template <int GROUP, int NT, bool FULL, typename S>
 __device__ __forceinline__ void mv_stage(const uint8_t* st, uint32_t w, uint32_t x, uint32_t c,
                                          const MvScales<GROUP, S, 2>& sz, int steps, float (&acc)[NT][4])
 {
     constexpr int kPer = GROUP / 32;       // 32-channel steps of a group
     constexpr int kGroups = kMvChunk / GROUP;
-    constexpr bool kSub = mv_subtract(GROUP, NT);
     const float none[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     float sum[NT][4];
-    // the sums of x rows 2t and 2t + 1, all groups at once
-    float u[NT][kGroups], v[NT][kGroups];
-    if (!kSub) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-            lds_run<kGroups>(st + c + i * 8 * kMvRecord, u[i]);
-            lds_run<kGroups>(st + c + i * 8 * kMvRecord + kMvRecord, v[i]);
-        }
-    }
 #pragma unroll
     for (int q = 0; q < kGroups; ++q) {
         if (!FULL && q * kPer >= steps) break;
         float tmp[NT][4];
-        uint32_t za = 0, zb = 0;
-        if (kSub) {
-            za = sz.zero_f16(0, q);
-            zb = sz.zero_f16(1, q);
-        }
+        const uint32_t za = sz.zero_f16(0, q), zb = sz.zero_f16(1, q);
 #pragma unroll
         for (int p = 0; p < kPer; ++p) {
             const int k = q * kPer + p;
@@ -128,11 +96,9 @@ __device__ __forceinline__ void mv_stage(const uint8_t* st, uint32_t w, uint32_t
             const uint32_t a = lds<uint32_t>(st + at), b = lds<uint32_t>(st + at + kMvW / 2);
             constexpr uint32_t lo = 0x000f000fu, hi = 0x00f000f0u;
             uint32_t m[8] = {a & lo, b & lo, a & hi, b & hi, (a >> 8) & lo, (b >> 8) & lo, (a >> 8) & hi, (b >> 8) & hi};
-            if (kSub) {
-                // exact: subnormals of one exponent
+            // exact: subnormals of one exponent
 #pragma unroll
-                for (int j = 0; j < 8; ++j) m[j] = sub_f16x2(m[j], (j % 2 ? zb : za) << (j & 2 ? 4 : 0));
-            }
+            for (int j = 0; j < 8; ++j) m[j] = sub_f16x2(m[j], (j % 2 ? zb : za) << (j & 2 ? 4 : 0));
 #pragma unroll
             for (int i = 0; i < NT; ++i) {
                 const uint4 r = lds<uint4>(st + x + k * 64 + i * 8 * kMvRecord);
@@ -142,16 +108,9 @@ __device__ __forceinline__ void mv_stage(const uint8_t* st, uint32_t w, uint32_t
             }
         }
         const float s0 = sz.scale(0, q), s1 = sz.scale(1, q);
-        const float z0 = kSub ? 0.0f : sz.minus_zero(0, q), z1 = kSub ? 0.0f : sz.minus_zero(1, q);
 #pragma unroll
         for (int i = 0; i < NT; ++i) {
-            float (&d)[4] = tmp[i];
-            if (!kSub) {
-                d[0] = fmaf(z0, u[i][q], d[0]);
-                d[1] = fmaf(z0, v[i][q], d[1]);
-                d[2] = fmaf(z1, u[i][q], d[2]);
-                d[3] = fmaf(z1, v[i][q], d[3]);
-            }
+            const float (&d)[4] = tmp[i];
             sum[i][0] = q ? fmaf(s0, d[0], sum[i][0]) : s0 * d[0];
             sum[i][1] = q ? fmaf(s0, d[1], sum[i][1]) : s0 * d[1];
             sum[i][2] = q ? fmaf(s1, d[2], sum[i][2]) : s1 * d[2];
@@ -161,8 +120,8 @@ __device__ __forceinline__ void mv_stage(const uint8_t* st, uint32_t w, uint32_t
     // the stage's factor of x, and the rest of the weights' 2^24
 #pragma unroll
     for (int i = 0; i < NT; ++i) {
-        const float fu = lds<float>(st + c + 32 + i * 8 * kMvRecord);
-        const float fv = lds<float>(st + c + 32 + i * 8 * kMvRecord + kMvRecord);
+        const float fu = lds<float>(st + c + i * 8 * kMvRecord);
+        const float fv = lds<float>(st + c + i * 8 * kMvRecord + kMvRecord);
         acc[i][0] = fmaf(fu, 4096.0f * sum[i][0], acc[i][0]);
         acc[i][1] = fmaf(fv, 4096.0f * sum[i][1], acc[i][1]);
         acc[i][2] = fmaf(fu, 4096.0f * sum[i][2], acc[i][2]);
@@ -216,11 +175,11 @@ __device__ __forceinline__ void mv_store(const MatvecArgs& a, const MvUnit& u, f
 }
 
 // Records of x, by row of x (then one of zeros) or by packed row, a warp each: eight
-// channels a lane, brought into f16 range, summed by group, and stored in the order of
-// the weights' registers, channels (0,4), (1,5) 2^-4, (2,6), (3,7) 2^-4.
+// channels a lane, brought into f16 range and stored in the order of the weights'
+// registers, channels (0,4), (1,5) 2^-4, (2,6), (3,7) 2^-4.
 template <typename T>
 __global__ void __launch_bounds__(256)
-matvec_x_kernel(const __grid_constant__ MatvecArgs a, bool packed, int group, uint8_t* __restrict__ records)
+matvec_x_kernel(const __grid_constant__ MatvecArgs a, bool packed, uint8_t* __restrict__ records)
 {
     pdl_enter();
     const int lane = threadIdx.x % kWarp;
@@ -244,29 +203,22 @@ matvec_x_kernel(const __grid_constant__ MatvecArgs a, bool packed, int group, ui
         // scale = 2^sc: the record's largest exponent goes to 14
         const int sc = min(127, 141 - (int)(__reduce_max_sync(0xffffffffu, top) >> 23));
         const float scale = __uint_as_float((unsigned)(sc + 127) << 23);
-        float sum = 0.0f;
         Pack<__half2, 4> o;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             __half2 b = __floats2half2_rn(f[j] * scale, f[j + 4] * scale);
-            const float2 v = __half22float2(b);
-            sum += v.x + v.y;
-            if (j & 1) b = __floats2half2_rn(v.x * 0.0625f, v.y * 0.0625f);   // the odd nibble
+            if (j & 1) b = __hmul2(b, __float2half2_rn(0.0625f));   // the odd nibble
             o.v[j] = b;
         }
-        for (int d = group / 16; d; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
         uint8_t* to = records + i * kMvRecord;
         reinterpret_cast<Pack<__half2, 4>*>(to)[lane] = o;
-        float* sums = reinterpret_cast<float*>(to + kMvChunk * 2);
-        const int per = group / 8;
-        if (lane % per == 0) sums[lane / per] = sum * 5.9604644775390625e-8f;
-        if (lane == 0) sums[8] = __uint_as_float((unsigned)(139 - sc) << 23);
+        if (lane == 0) *reinterpret_cast<float*>(to + kMvFactor) = __uint_as_float((unsigned)(139 - sc) << 23);
     }
 }
 
 // What a consumer warp carries through its units.
 struct MvWarp {
-    uint32_t ow, ox, oc;           // offsets in a stage: weights, x, sums of x
+    uint32_t ow, ox, oc;           // offsets in a stage: weights, x, factors of x
     int part, row, half;
     bool whole;                    // a row's groups of a stage are one aligned load
 };
@@ -374,7 +326,7 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__
         w.half = half;
         w.ow = part * half * 128 + w.row * 128 + (g << 4) + t * 4;
         w.ox = kMvW + (part * a.chunk_rows + g) * kMvRecord + t * 16;
-        w.oc = kMvW + (part * a.chunk_rows + 2 * t) * kMvRecord + kMvChunk * 2;
+        w.oc = kMvW + (part * a.chunk_rows + 2 * t) * kMvRecord + kMvFactor;
         w.whole = MvScales<GROUP, S, 2>::aligned_groups(a, groups);
         int unit = blockIdx.x;
         if (unit < units) {
@@ -581,12 +533,12 @@ int launch_matvec_group(const moedc::MatvecArgs& a, int group, void* out, cudaSt
 }
 
 template <typename T>
-int launch_matvec_x(const moedc::MatvecArgs& a, bool packed, int group, uint8_t* records, cudaStream_t stream)
+int launch_matvec_x(const moedc::MatvecArgs& a, bool packed, uint8_t* records, cudaStream_t stream)
 {
     const int64_t n = (packed ? (int64_t)a.rows : (int64_t)a.x_rows + 1) * ((a.Kd + moedc::kMvChunk - 1) / moedc::kMvChunk);
     const int64_t want = (n + 7) / 8, most = 8 * (int64_t)sm_count();
     clear_stale_error();
-    launch(moedc::matvec_x_kernel<T>, (int)(want < most ? want : most), 256, 0, stream, a, packed, group, records);
+    launch(moedc::matvec_x_kernel<T>, (int)(want < most ? want : most), 256, 0, stream, a, packed, records);
     return launch_status();
 }
 
@@ -662,8 +614,8 @@ extern "C" int moedc_matvec_int4(const void* x, int64_t ldx, int dtype, int x_ro
     const bool tc = matvec_tc_takes(E, rows, 128) && matvec_tc_takes(E, (int)(filled < rows ? filled : rows), group);
     if (!tc) mv_shape(a, sm_count());
     const int st = dtype == MOEDC_F16
-                       ? launch_matvec_x<__half>(a, tc, group, records, stream)
-                       : launch_matvec_x<__nv_bfloat16>(a, tc, group, records, stream);
+                       ? launch_matvec_x<__half>(a, tc, records, stream)
+                       : launch_matvec_x<__nv_bfloat16>(a, tc, records, stream);
     if (st != MOEDC_OK) return st;
     if (tc) return launch_matvec_tc(a, group, out, stream);
     return scale_dtype == MOEDC_F32   ? launch_matvec_group<float>(a, group, out, stream)

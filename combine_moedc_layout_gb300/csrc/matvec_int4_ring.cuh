@@ -13,10 +13,11 @@ namespace moedc {
 
 constexpr int kMvChunk = 256;                          // channels of a stage (of one part of K)
 constexpr unsigned long long kMvWaitNs = 200000000ull; // bound of every wait
-// A record of x: 256 channels in f16, then 2^-24 times the sum of each of up to
-// eight groups, then 2^12 / scale.  576 bytes apart, the rows that a quarter-warp
-// reads lie in different halves of the banks.
+// A record of x: 256 channels in f16, then (16-byte aligned, for TMA) 2^12 / scale.
+// 576 bytes apart, the rows that a quarter-warp reads lie in different halves of the
+// banks.
 constexpr int kMvRecord = kMvChunk * 2 + 64;
+constexpr int kMvFactor = kMvChunk * 2 + 32;
 
 // ---------------------------------------------------------------- mbarriers
 
@@ -173,11 +174,6 @@ template <int GROUP, typename S, int R> struct MvScales {
             else
                 return __half2float(__ushort_as_half((unsigned short)(q % 2 ? w >> 16 : w & 0xffffu)));
         }
-    }
-    // minus the zero point: 2^23 + z is a binary32 number whose low bits are z
-    __device__ __forceinline__ float minus_zero(int row, int q) const
-    {
-        return 8388608.0f - __uint_as_float(__byte_perm(z[row][q / 4], 0x4b000000u, 0x7540 | (q % 4)));
     }
     // the zero point as the weights' f16 subnormals, of the low nibbles
     __device__ __forceinline__ uint32_t zero_f16(int row, int q) const

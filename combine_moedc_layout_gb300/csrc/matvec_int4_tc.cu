@@ -363,7 +363,7 @@ matvec_int4_tc_kernel(const __grid_constant__ MatvecArgs a, const __grid_constan
 #pragma unroll
                     for (int c = 0; c < kMvChunk / 64; ++c)
                         tma_3d(st + c * (kTcN * 128), &xmap, c * 64, s, u.r0, full_x + ring.slot);
-                    tma_3d(st + kTcX, &fmap, kMvRecord / 2 - 16, s, u.r0, full_x + ring.slot);
+                    tma_3d(st + kTcX, &fmap, kMvFactor / 2, s, u.r0, full_x + ring.slot);
                     ring.next(kTcStages);
                     ++issued;
                 }
