@@ -458,8 +458,10 @@ MOEDC_EXPORT int moedc_unsort_grad(const void* dy, int64_t lddy, const void* sor
  *   out     [rows, N], of x's dtype; rows that belong to no expert are not written
  * offsets int32 [E + 1] and counts int32 [E] as from moedc_sort; both NULL with
  * E = 1: all rows.  group is 32, 64 or 128, Kd a multiple of it; x and wq
- * 16-byte aligned and ldx a multiple of 8.  A row of x that holds an infinity
- * or a NaN gives NaN.
+ * 16-byte aligned and ldx a multiple of 8.  Infinities and NaN of x go through
+ * the formula as they are, in the rows of their own token alone: an infinity
+ * gives an infinity of its weight's sign, or NaN where that weight is 0 or
+ * another infinity has the other sign.
  * workspace: moedc_matvec_int4_workspace_bytes of the same arguments, 16-byte
  * aligned, no initialisation (x in the order the products read it).  The query
  * returns 0, and workspace may be NULL, where the weights to read are so few

@@ -67,3 +67,25 @@ def test_large_values_at_the_zero_point_add_nothing(T, E, K, N, Kd, group, swigl
         w = int4_weights(wq[e], s[e], None if z is None else z[e], group)
         ref, err = matvec_ref(x[(m.src[rows] // K).long()], w, swiglu)
         assert_within(out[rows], ref.cuda(), err + rounding(ref, torch.bfloat16))
+
+
+@pytest.mark.parametrize("T,E,K,N,Kd,group,swiglu", SHAPES)
+def test_infinities_follow_the_formula_in_every_form(T, E, K, N, Kd, group, swiglu):
+    """inf * 0 and inf - inf are NaN, everything else of an infinity is one, and
+    only in its own token's rows."""
+    _, x, wq, s, z, m = _inputs(T, E, K, N, Kd, group, swiglu, True, T + N)
+    x[1, 7] = INF
+    x[2, Kd - 1] = -INF
+    x[3, 300] = float("nan")
+    x[4, 0], x[4, 270] = INF, -INF
+    out = _run(x, wq, s, z, m, K, swiglu)
+    for e, rows in _experts(m):
+        w = int4_weights(wq[e], s[e], z[e], group)
+        ref, err = matvec_ref(x[(m.src[rows] // K).long()], w, swiglu)
+        got = out[rows].double()
+        assert torch.equal(torch.isnan(got), torch.isnan(ref))
+        inf = torch.isinf(ref)
+        assert torch.equal(got[inf], ref[inf])
+        fine = torch.isfinite(ref)
+        bound = err[fine] + rounding(ref[fine], torch.bfloat16)
+        assert ((got[fine] - ref[fine]).abs() <= bound).all()
