@@ -6,7 +6,7 @@
 // with p = w / scale and d the weights' gradient on C,
 //   softmax            dl_e = scale * p_e * (d_e - sum_C p d), d_e = 0 outside C
 //   sigmoid            dl_e = scale * d_e * s_e (1 - s_e)
-//   sigmoid over C     dl_e = scale * s_e (1 - s_e) / S * (d_e - sum_C p d)
+//   sigmoid over C     dl_e = scale * p_e (1 - s_e) * (d_e - sum_C p d)
 // and only the softmax over all experts reaches outside C.
 //
 // Few tokens cost a launch.  Many are bound by instruction issue (ALU 56%): 32768
@@ -62,7 +62,11 @@ __device__ __forceinline__ float sigmoid_slope(float l)
     return e / ((1.0f + e) * (1.0f + e));
 }
 
-__device__ __forceinline__ float sigmoid(float l) { return 1.0f / (1.0f + expf(-l)); }
+// Far below 0, where expf(-l) would overflow, the sigmoid is expf(l) (1 + expf(l) is 1).
+__device__ __forceinline__ float sigmoid(float l)
+{
+    return l < -80.0f ? expf(l) : 1.0f / (1.0f + expf(-l));
+}
 
 // exp for the dense sums, x <= 0: 2^(x log2 e), the power by ex2.approx (results
 // below 2^-126 become 0).  Its relative error of |x| 2^-24 and some ulp is that of
@@ -74,32 +78,31 @@ __device__ __forceinline__ float exp_fast(float x)
     return y;
 }
 
-// Lane i < K holds chosen expert i (live: there is one): its p = w / scale, and
-// the sum S of the sigmoids over the chosen.  `den` and `top` are the softmax's
-// denominator and maximum over all experts, used when not renormalised.
-struct GateWeights {
-    float p, total;
-};
-__device__ __forceinline__ GateWeights gate_weights(const GateArgs& a, bool live, float l,
-                                                    float top, float den)
+// Lane i < K holds chosen expert i (live: there is one): its p = w / scale.  `den`
+// and `top` are the softmax's denominator and maximum over all experts, used when
+// not renormalised.
+__device__ __forceinline__ float gate_weight(const GateArgs& a, bool live, float l, float top, float den)
 {
-    GateWeights g{0.0f, 0.0f};
     if (a.sigmoid) {
-        const float s = live ? sigmoid(l) : 0.0f;
-        g.p = s;
-        if (a.normalize) {
-            g.total = warp_sum(s);
-            g.p = g.total > 0.0f ? s / g.total : 0.0f;
+        float s = live ? sigmoid(l) : 0.0f;
+        if (!a.normalize) return s;
+        float total = warp_sum(s);
+        if (total < 1e-30f) {
+            // all far below 0, where a sigmoid is exp(l) and loses bits as it underflows: in
+            // units of the largest.  One that is 0 in binary32 stays 0.
+            const float m = warp_max(s > 0.0f ? l : -FLT_MAX);
+            s = s > 0.0f ? expf(l - m) : 0.0f;
+            total = warp_sum(s);
         }
-    } else if (a.normalize) {
+        return total > 0.0f ? s / total : 0.0f;
+    }
+    if (a.normalize) {
         const float m = warp_max(live ? l : -FLT_MAX);
         const float ex = live ? expf(l - m) : 0.0f;
         const float sum = warp_sum(ex);
-        g.p = live ? ex / sum : 0.0f;
-    } else {
-        g.p = live ? exp_fast(l - top) / den : 0.0f;
+        return live ? ex / sum : 0.0f;
     }
-    return g;
+    return live ? exp_fast(l - top) / den : 0.0f;
 }
 
 // A lane's experts: N of them, V neighbours to an access.  Value j holds expert
@@ -238,10 +241,10 @@ gate_kernel(GateArgs a, int32_t* __restrict__ topk_idx, float* __restrict__ topk
         if (!a.sigmoid && !a.normalize) gate_softmax<N, BIAS>(l, key, top, den);
         const int mine = gate_choose<N, V>(key, a.K, lane, s_cand[warp]);
         const float lc = mine >= 0 ? gate_logit(to_f32(row[mine])) : 0.0f;
-        const GateWeights g = gate_weights(a, mine >= 0, lc, top, den);
+        const float p = gate_weight(a, mine >= 0, lc, top, den);
         if (lane < a.K) {
             topk_idx[t * a.K + lane] = mine;
-            topk_weights[t * a.K + lane] = g.p * a.scale;
+            topk_weights[t * a.K + lane] = p * a.scale;
         }
     }
 }
@@ -277,14 +280,13 @@ gate_grad_kernel(GateArgs a, const int32_t* __restrict__ topk_idx,
         }
         if (e < 0) d = 0.0f;
         if (DENSE) gate_softmax<N, BIAS>(v, key, top, den);   // v: the exponentials
-        const GateWeights g = gate_weights(a, e >= 0, l, top, den);
-        const float dot = (a.sigmoid && !a.normalize) ? 0.0f : warp_sum(g.p * d);
+        const float p = gate_weight(a, e >= 0, l, top, den);
+        const float dot = (a.sigmoid && !a.normalize) ? 0.0f : warp_sum(p * d);
         float own;
         if (a.sigmoid)
-            own = a.normalize ? (g.total > 0.0f ? sigmoid_slope(l) / g.total * (d - dot) : 0.0f)
-                              : sigmoid_slope(l) * d;
+            own = a.normalize ? p * sigmoid(-l) * (d - dot) : sigmoid_slope(l) * d;
         else
-            own = DENSE ? g.p * d : g.p * (d - dot);
+            own = DENSE ? p * d : p * (d - dot);
         if (e >= 0) atomicAdd(add + e, own * a.scale);   // distinct experts: one addition each
         __syncwarp();
         // a token that chose nothing has den = 0 and no gradient
