@@ -39,6 +39,7 @@ TOKEN_SCALE_MAX_H = 32768   # MOEDC_TOKEN_SCALE_MAX_H
 GATE_SOFTMAX = 0
 GATE_SIGMOID = 1
 GATE_NORMALIZE = 0x10       # OR into either: weights renormalised over the chosen experts
+GATE_BIAS_SCORE = 0x100     # OR into either: the choice by score + bias instead of logit + bias
 SWIGLU = 1                  # MOEDC_SWIGLU
 
 EXPORTED = ("moedc_api_version", "moedc_strerror", "moedc_layout_workspace_bytes",
@@ -506,7 +507,9 @@ def _need_shape(t: torch.Tensor, shape, name: str) -> None:
 def gate(logits: torch.Tensor, K: int, bias: torch.Tensor | None = None,
          flags: int = GATE_SOFTMAX | GATE_NORMALIZE, scale: float = 1.0, out=None):
     """Top-k router: (topk_idx int32 [T, K], topk_weights fp32 [T, K]) from
-    logits [T, E].  `out` takes an earlier call's result to write into."""
+    logits [T, E].  bias [E] moves the choice alone: it is added to the logits, or,
+    with GATE_BIAS_SCORE (auxiliary-loss-free balancing), to the scores.  `out`
+    takes an earlier call's result to write into."""
     ld = _need_rows(logits, "logits")
     dtype = _lm_dtype(logits, "logits")
     T, E = logits.shape

@@ -350,14 +350,20 @@ MOEDC_EXPORT int moedc_layout_dispatch(const void* x, const int32_t* topk_idx,
 /*
  * Top-k router: topk_idx and topk_weights from the router's logits.
  *   key[t][e] = logits[t][e] + bias[e]   (one binary32 sum; bias NULL = 0)
- * An expert can be chosen when its logit and its key are neither NaN nor -inf
- * (mask experts with -inf; a mask of the type's lowest finite value leaves the
+ * or, with MOEDC_GATE_BIAS_SCORE OR-ed into the flags,
+ *   key[t][e] = score[t][e] + bias[e]    score = softmax(l)_e over the experts that can be
+ *                                        chosen, or sigmoid(l_e), in binary32
+ * The second is the rule of auxiliary-loss-free balancing: a balance bias
+ * that was trained for it chooses other experts under the first.  Without a
+ * bias both choose by the logits.
+ * An expert can be chosen when its logit, its bias and its key are neither
+ * NaN nor -inf (mask experts with -inf; a mask of the type's lowest finite value leaves the
  * expert to be chosen last, with weight 0 next to ordinary logits).  +inf
  * counts as the largest finite binary32.  topk_idx[t] holds the K experts
  * with the largest keys, descending, ties to the lowest expert; where fewer
  * can be chosen the rest is -1 with weight 0 (the masked entry of every other
  * call).  The weights come from the logits WITHOUT the bias, which moves the
- * choice alone (load balancing), with C the chosen experts of the token:
+ * choice alone, with C the chosen experts of the token:
  *   MOEDC_GATE_SOFTMAX                         scale * softmax(l)_e over the experts that can be chosen
  *   MOEDC_GATE_SOFTMAX | MOEDC_GATE_NORMALIZE  scale * softmax(l)_e over C
  *   MOEDC_GATE_SIGMOID                         scale * sigmoid(l_e)
@@ -376,6 +382,7 @@ MOEDC_EXPORT int moedc_layout_dispatch(const void* x, const int32_t* topk_idx,
 #define MOEDC_GATE_SOFTMAX 0
 #define MOEDC_GATE_SIGMOID 1
 #define MOEDC_GATE_NORMALIZE 0x10
+#define MOEDC_GATE_BIAS_SCORE 0x100
 MOEDC_EXPORT int moedc_gate(const void* logits, int64_t ld_logits, int dtype, int T, int E, int K,
                  const float* bias, int flags, float scale, int32_t* topk_idx,
                  float* topk_weights, cudaStream_t stream);
