@@ -42,7 +42,6 @@
 // it is taken (matvec_int4_tc.cu).
 #include <climits>
 #include <cmath>
-#include <mutex>
 
 #include "matvec_int4_ring.cuh"
 
@@ -487,13 +486,8 @@ template <int GROUP, typename S, int NTMAX>
 int launch_matvec(moedc::MatvecArgs a, void* out, cudaStream_t stream)
 {
     auto* k = moedc::matvec_int4_kernel<GROUP, S, NTMAX>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [&] {
-        attr = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kMvSmem - 1024);
-    });
-    if (attr != cudaSuccess) return MOEDC_ERR_CUDA;
+    static PerDevice raised;
+    if (!raise_smem_limit(raised, (const void*)k, kMvSmem - 1024)) return MOEDC_ERR_CUDA;
     const int blocks = sm_count();
     a.stage_bytes = (moedc::kMvW + (a.chunk_rows << a.lk) * moedc::kMvRecord + 1023) / 1024 * 1024;
     const size_t fixed = moedc::kMvRed + (3 * (size_t)a.E + 1) * sizeof(int32_t);

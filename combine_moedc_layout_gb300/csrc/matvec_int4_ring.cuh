@@ -8,6 +8,7 @@
 #include <cudaTypedefs.h>
 
 #include "matvec_int4.cuh"
+#include "per_device.cuh"
 
 namespace moedc {
 
@@ -206,6 +207,16 @@ struct MvRing {
 namespace moedc_host {
 
 constexpr int kMvSmem = 227 * 1024;
+
+// `raised`: of this kernel
+inline bool raise_smem_limit(PerDevice& raised, const void* kernel, int bytes)
+{
+    int device = 0;
+    if (cudaGetDevice(&device) != cudaSuccess) return false;
+    return raised.once(device, [&] {
+        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
+    });
+}
 
 // Rows of Kd / 2 bytes, boxes of box_rows x 128 bytes in the 128-byte swizzle.  False
 // when the driver refuses.

@@ -25,8 +25,6 @@
 // epilogue share evenly; with groups of 64 the hand-overs of accumulators (some 600
 // clocks each) are the longest.  128 rows x 7168 x 7168, groups of 128: 39.6 us, 332
 // TFLOP/s, against 93 us of the warp tiles.
-#include <mutex>
-
 #include "matvec_int4_ring.cuh"
 
 namespace moedc {
@@ -456,12 +454,8 @@ template <int GROUP, typename S>
 int launch_tc(const moedc::MatvecArgs& a, void* out, cudaStream_t stream)
 {
     auto* k = moedc::matvec_int4_tc_kernel<GROUP, S>;
-    static std::once_flag once;
-    static cudaError_t attr = cudaSuccess;
-    std::call_once(once, [&] {
-        attr = cudaFuncSetAttribute((const void*)k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kTcSmem);
-    });
-    if (attr != cudaSuccess) return MOEDC_ERR_CUDA;
+    static PerDevice raised;
+    if (!raise_smem_limit(raised, (const void*)k, (int)kTcSmem)) return MOEDC_ERR_CUDA;
     CUtensorMap map;
     if (!matvec_weight_map(&map, a.wq, a.Kd, (int64_t)a.E * (a.swiglu ? 2 : 1) * a.N, moedc::kTcRows / 2))
         return MOEDC_ERR_CUDA;
