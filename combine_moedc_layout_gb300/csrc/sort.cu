@@ -421,7 +421,8 @@ int launch_sort(const moedc::SortArgs& a, const void* x, const int32_t* topk_idx
     const U* from = static_cast<const U*>(x);
     U* to = static_cast<U*>(sorted);
     const int per = moedc::kSortUnits * moedc::kWarp;
-    const int64_t items = (int64_t)a.T * (a.units ? (a.units + per - 1) / per : 1);
+    // without tokens there are the rows to clear
+    const int64_t items = a.T ? (int64_t)a.T * (a.units ? (a.units + per - 1) / per : 1) : a.rows;
     size_t smem = (3 * (size_t)a.E + 2) * sizeof(int32_t);
     clear_stale_error();
     if (!slot) {
@@ -551,7 +552,8 @@ extern "C" int moedc_sort(const void* x, int64_t ldx, int dtype, int T, int H,
         if (st != MOEDC_OK) return st;
         slot = s;
     }
-    if (!x) H = 0;
+    // without `sorted` the maps alone; without tokens every row of it is cleared all the same
+    if (!sorted || rows == 0) H = 0;
     moedc::SortArgs a{ldx, H, T, K, E, align, rows, row, src, offsets, dev_status};
     if (rows_vec(dtype, H, x ? ldx : 0, x, sorted, nullptr)) {
         a.ldx = ldx * size / 16;

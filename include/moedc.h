@@ -407,7 +407,8 @@ MOEDC_EXPORT int moedc_gate_grad(const void* logits, int64_t ld_logits, int dtyp
  * rows: rows of sorted and src.  With fewer than the routing needs, the entries
  * past the end are dropped, offsets stop at rows, and MOEDC_ERR_CAPACITY is
  * raised.  x and sorted may both be NULL: the maps alone (a product that
- * gathers its rows through src needs no copy).
+ * gathers its rows through src needs no copy).  T = 0: x may be NULL, and all
+ * rows of sorted are cleared.
  * dtype: MOEDC_BF16, MOEDC_F16 or MOEDC_F32; any H >= 1; ldx >= H elements
  * from row to row of x; sorted is contiguous.  Rows that are whole 16-byte
  * units on 16-byte boundaries move 16 bytes at a time, others by element.
