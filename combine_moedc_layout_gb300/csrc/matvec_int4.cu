@@ -574,7 +574,7 @@ extern "C" int moedc_matvec_int4(const void* x, int64_t ldx, int dtype, int x_ro
         ((int64_t)rows / 8 + E) * ((int64_t)N / 32 + 1) > INT32_MAX)
         return MOEDC_ERR_ARG;
     if (rows == 0) return MOEDC_OK;
-    if (!out || !x) return MOEDC_ERR_ARG;
+    if (!out || (x_rows > 0 && !x)) return MOEDC_ERR_ARG;   // an empty x has no address
     const bool small = matvec_small_takes(Kd, E, N, flags != 0, rows);
     if (!small && (!workspace || !aligned(workspace, 16) ||
                    workspace_bytes < moedc_matvec_int4_workspace_bytes(x_rows, Kd, E, N, flags, rows)))

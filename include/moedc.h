@@ -458,7 +458,8 @@ MOEDC_EXPORT int moedc_unsort_grad(const void* dy, int64_t lddy, const void* sor
  * silu(a) = a / (1 + exp(-a)); binary32 sums.  r' = r, or src[r] / top_k when
  * src is given (the token of a sorted row: x is then read in token order).
  * With MOEDC_SWIGLU the weights have 2N rows, gate rows 0..N-1, up rows N..2N-1.
- *   x       bf16 or f16 [x_rows, Kd], ldx elements from row to row
+ *   x       bf16 or f16 [x_rows, Kd], ldx elements from row to row; may be NULL
+ *           when x_rows = 0 (no expert has rows then)
  *   wq      uint8 [E, N or 2N, Kd / 2], element k in byte k / 2, even k in the
  *           low four bits: q in 0..15
  *   scales  [E, N or 2N, Kd / group], scale_dtype MOEDC_BF16, _F16 or _F32
