@@ -693,8 +693,10 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
     """out [R, N]: packed expert rows times 4-bit weights wq uint8 [E, N, Kd/2]
     ([N, Kd/2]: one linear layer) with scales [E, N, Kd/group]; swiglu: 2N
     weight rows, silu(gate) * up.  offsets and counts from sort(); src and
-    top_k read x in token order.  workspace: moedc_matvec_int4_workspace_bytes
-    bytes, allocated here when None and needed."""
+    top_k read x in token order.  status (int32 [1], for instance sort()'s) takes
+    data errors; without one the call waits for its kernels and raises them.
+    workspace: moedc_matvec_int4_workspace_bytes bytes, allocated here when None
+    and needed."""
     ld = _need_rows(x, "x")
     dtype = _lm_dtype(x, "x")
     if wq.dim() == 2:
@@ -728,7 +730,10 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
         out = torch.empty((R, N), dtype=x.dtype, device=x.device)
     _need(out, x.dtype, "out")
     _need_shape(out, (R, N), "out")
-    if status is None:
+    wait = status is None
+    if wait:
+        if torch.cuda.is_current_stream_capturing():
+            raise ValueError("status must be given while a graph is captured")
         status = torch.zeros(1, dtype=torch.int32, device=x.device)
     lib = _lib or load()
     flags = SWIGLU if swiglu else 0
@@ -743,4 +748,6 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
                                  _p(src), top_k, R, out.data_ptr(), _p(workspace),
                                  0 if workspace is None else workspace.numel(),
                                  status.data_ptr(), _stream(None)), "moedc_matvec_int4")
+    if wait:
+        _check(int(status), "moedc_matvec_int4")
     return out

@@ -23,3 +23,30 @@ def test_no_tokens_on_buffers_of_fixed_size(E, N, Kd, rows, gather):
     assert int(m.status) == 0
     assert (out == 7.0).all()
     assert moedc.unsort(out, m.row, torch.empty(0, 2).cuda()).shape == (0, N)
+
+
+@pytest.mark.parametrize("n", [20, 220000])          # few weights; prepared x
+def test_without_a_status_errors_are_raised(n):
+    g = torch.Generator().manual_seed(4)
+    x = torch.randn(4, 128, generator=g).to(torch.bfloat16).cuda()
+    wq, s, _ = _weights(g, 2, n, 128, 64, False, torch.bfloat16)
+    counts = torch.tensor([2, 2], dtype=torch.int32).cuda()
+    offsets = torch.tensor([0, 2, 4], dtype=torch.int32).cuda()
+    want = moedc.matvec_int4(x, wq, s, offsets=offsets, counts=counts)
+    src = torch.tensor([0, 9, 1, 2], dtype=torch.int32).cuda()
+    with pytest.raises(moedc.MoedcError) as e:
+        moedc.matvec_int4(x, wq, s, offsets=offsets, counts=counts, src=src)
+    assert e.value.code == moedc.ERR_EXPERT_RANGE
+    with pytest.raises(moedc.MoedcError) as e:
+        moedc.matvec_int4(x, wq, s, offsets=offsets, counts=counts + 1)
+    assert e.value.code == moedc.ERR_CAPACITY
+    # a status takes them instead, and nothing waits: such a call can be captured
+    status = torch.zeros(1, dtype=torch.int32).cuda()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = moedc.matvec_int4(x, wq, s, offsets=offsets, counts=counts, status=status)
+        with pytest.raises(ValueError, match="status"):
+            moedc.matvec_int4(x, wq, s, offsets=offsets, counts=counts)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(got, want) and int(status) == 0
