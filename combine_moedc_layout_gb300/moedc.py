@@ -606,8 +606,15 @@ def sort(x: torch.Tensor | None, topk_idx: torch.Tensor, E: int, align: int = 1,
         if x is not None:
             _need(out.rows, x.dtype, "out.rows")
             _need_shape(out.rows, (rows, H), "out.rows")
+        _need(out.row, torch.int32, "out.row")
         _need_shape(out.row, (T, K), "out.row")
+        _need(out.src, torch.int32, "out.src")
+        _need(out.offsets, torch.int32, "out.offsets")
+        _need_shape(out.offsets, (E + 1,), "out.offsets")
+        _need(out.counts, torch.int32, "out.counts")
         _need_shape(out.counts, (E,), "out.counts")
+        _need(out.workspace, torch.uint8, "out.workspace")
+    _need(out.status, torch.int32, "status")
     _check((_lib or load()).moedc_sort(_p(x), ld, dtype, T, H, topk_idx.data_ptr(), K, E, align,
                                        rows, _p(out.rows), out.row.data_ptr(),
                                        out.src.data_ptr(), out.offsets.data_ptr(),
@@ -735,6 +742,8 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
         if torch.cuda.is_current_stream_capturing():
             raise ValueError("status must be given while a graph is captured")
         status = torch.zeros(1, dtype=torch.int32, device=x.device)
+    else:
+        _need(status, torch.int32, "status")
     lib = _lib or load()
     flags = SWIGLU if swiglu else 0
     xr = x.shape[0]
@@ -742,6 +751,8 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
         n = _matvec_int4_bytes(xr, Kd, E, N, flags, R)
         if n:
             workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
+    else:
+        _need(workspace, torch.uint8, "workspace")
     _check(lib.moedc_matvec_int4(x.data_ptr(), ld, dtype, xr, Kd, wq.data_ptr(),
                                  scales.data_ptr(), _lm_dtype(scales, "scales"), _p(zeros),
                                  Kd // max(1, groups), E, N, flags, _p(offsets), _p(counts),
