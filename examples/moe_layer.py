@@ -102,7 +102,7 @@ class Unsort(torch.autograd.Function):
     @staticmethod
     def backward(ctx, dy):
         rows, w, row, src = ctx.saved_tensors
-        drows, dw = moedc.unsort_grad(dy, rows, row, src, w)
+        drows, dw = moedc.unsort_grad(dy.contiguous(), rows, row, src, w)
         return drows, dw, None, None
 
 
