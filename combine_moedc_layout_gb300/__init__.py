@@ -19,7 +19,7 @@ from .moedc import (BF16, FP8_E4M3, SCALES_COL_MAJOR, SCALES_PER_TOKEN, Layout, 
                     rank_dispatch, rank_layout, strerror)
 from .moedc import (F16, F32, GATE_BIAS_SCORE, GATE_NORMALIZE, GATE_SIGMOID, GATE_SOFTMAX, SWIGLU, Sorted, gate,
                     gate_grad, matvec_int4, moedc_gate, moedc_gate_grad, moedc_matvec_int4,
-                    moedc_sort, moedc_sort_rows, moedc_sort_workspace_bytes, moedc_unsort,
+                    moedc_matvec_int4_workspace_bytes, moedc_sort, moedc_sort_rows, moedc_sort_workspace_bytes, moedc_unsort,
                     moedc_unsort_grad, sort, sort_grad, unsort, unsort_grad)
 
 __all__ = ["BF16", "FP8_E4M3", "SCALES_COL_MAJOR", "SCALES_PER_TOKEN", "Layout", "MoedcError", "alloc_recv",
@@ -29,4 +29,9 @@ __all__ = ["BF16", "FP8_E4M3", "SCALES_COL_MAJOR", "SCALES_PER_TOKEN", "Layout",
            "moedc_layout_static_scratch", "moedc_layout_workspace_bytes",
            "moedc_layout_dispatch_workspace_bytes", "layout_dispatch_workspace", "moedc_rank_combine",
            "moedc_rank_dispatch", "moedc_rank_layout", "rank_combine", "rank_dispatch",
-           "rank_layout", "strerror"]
+           "rank_layout", "strerror",
+           "F16", "F32", "GATE_BIAS_SCORE", "GATE_NORMALIZE", "GATE_SIGMOID", "GATE_SOFTMAX", "SWIGLU",
+           "Sorted", "gate", "gate_grad", "matvec_int4", "moedc_gate", "moedc_gate_grad",
+           "moedc_matvec_int4", "moedc_matvec_int4_workspace_bytes", "moedc_sort", "moedc_sort_rows",
+           "moedc_sort_workspace_bytes", "moedc_unsort", "moedc_unsort_grad", "sort", "sort_grad",
+           "unsort", "unsort_grad"]
