@@ -25,10 +25,11 @@
 // group's sum instead, sum q x - z sum x, it would cost less, 104 against 111 us and
 // 502 against 528 in the shapes below, but a large value of x whose weight is at the
 // zero point would then cancel in binary32 and take the small ones' bits along.)
-// x is brought into f16 per row and stage by a power of two that puts its
-// largest value into [2^14, 2^15): exact down to 2^-28 of that value, and
-// 2^-39 of it below.  The group's sum is then scaled in binary32, so neither
-// weights nor scales are ever rounded.  An infinity or a NaN stays one in f16.
+// x is brought into f16 per row and stage by a power of two that puts its largest
+// value into [2^14, 2^15), the high nibbles' channels by another 2^-4: bf16 stays exact
+// down to 2^-27 of that value, f16, which has three bits more, to 2^-24, and what lies
+// below is off by at most 2^-35 of it.  The group's sum is then scaled in binary32, so
+// neither weights nor scales are ever rounded.  An infinity or a NaN stays one in f16.
 //
 // 16 tokens, top 8 of 128 experts, 2 x 1024 x 6144 with SwiGLU, groups of 128: 111
 // us (535 MB, 4.8 TB/s); 128 tokens, top 8 of 288 experts, 2048 x 7168, groups of 64:
@@ -452,13 +453,14 @@ namespace {
 
 // Parts of K and rows of a unit: the pair with the least of
 //   rounds of units * (stages of a unit * cost of a stage + cost of a unit)
-// where the costs are the fit of a sweep over every pair at four shapes (16
-// tokens 2 x 1024 x 6144 with SwiGLU 110 / 108 / 125 us at 1 / 2 / 4 parts and
-// 8 rows; 128 tokens 2048 x 7168 with zero points 599 / 489 / 609 us; 255 tokens
-// 2050 x 2048 at 1 part 106 / 81 / 84 us with 8 / 16 / 32 rows, at 4 parts 153 us;
-// one token 7168 x 7168 30 / 21 / 22 us).  A stage takes longer with more rows; one
-// part with zero points holds more lines of scales open than L1 keeps.  How many
-// experts have rows, and how many each, is the guess of a uniform choice.
+// where the costs are the fit of a sweep over every pair at four shapes, and name the
+// fastest pair of each or one within 4% of it (16 tokens 2 x 1024 x 6144 with SwiGLU
+// 118 / 116 / 132 us at 1 / 2 / 4 parts and 8 rows; 128 tokens 2048 x 7168 with zero
+// points 554 / 518 / 619 us; 255 tokens 2050 x 2048 at 1 part 99 / 81 / 84 us with 8 /
+// 16 / 32 rows, at 4 parts 146 us; one token 14336 x 7168 34 / 22 / 23 us).  A stage
+// takes longer with more rows; one part with zero points holds more lines of scales open
+// than L1 keeps.  How many experts have rows, and how many each, is the guess of a
+// uniform choice.
 void mv_shape(moedc::MatvecArgs& a, int blocks)
 {
     const double active = a.E * (1.0 - exp(-(double)a.rows / a.E));

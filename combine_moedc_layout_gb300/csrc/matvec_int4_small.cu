@@ -6,8 +6,9 @@
 // with the weights of several chunks in flight straight to registers (16 bytes a
 // thread and row, turned round within four threads), and add their sums
 // in shared memory.  q | 0x4300 is the bf16 number 128 + q (f16: 0x6400, 1024 + q);
-// less 128 + z it is q - z, exact in either type, so the products need no
-// preparation of x beyond its order.  The group's sum is scaled in binary32.
+// less 128 + z it is q - z, exact in either type (a widely published conversion), so
+// the products need no preparation of x beyond its order.  The group's sum is scaled in
+// binary32.
 #include "matvec_int4.cuh"
 
 namespace moedc {
@@ -250,9 +251,9 @@ int launch_small_scale(const moedc::MatvecArgs& a, void* out, cudaStream_t strea
 
 // Few weights to read, each expert's rows (eight at a time read them again, from
 // L2) counted.  Time on the GPU, this form / the one with prepared x: 2 MB 8.1 /
-// 10.3 us, 10 MB 10.3 / 12.3 us, 20 MB 12.3 / 13.0 us, 25 MB 16.5 / 16.1 us, 36 MB
-// 20.5 / 16.4 us; on the host this form saves a launch, a tensor map and the
-// workspace, some 6 us of 20.
+// 10.3 us, 18 MB 11.8 / 12.3 us (with SwiGLU 14.4 / 12.3), 20 MB 12.3 / 13.0 us, 25 MB
+// 16.4 / 16.4 us, 36 MB 20.5 / 16.4 us; on the host this form saves a launch, a tensor
+// map and the workspace, some 6 us of 20.
 bool matvec_small_takes(int Kd, int E, int N, bool swiglu, int rows)
 {
     const int64_t active = E < rows ? E : rows;

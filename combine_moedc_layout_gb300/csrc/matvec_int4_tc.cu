@@ -23,8 +23,8 @@
 //
 // A stage takes some 2300 clocks with groups of 128, which unpacking, products and
 // epilogue share evenly; with groups of 64 the hand-overs of accumulators (some 600
-// clocks each) are the longest.  128 rows x 7168 x 7168, groups of 128: 39.6 us, 332
-// TFLOP/s, against 93 us of the warp tiles.
+// clocks each) are the longest.  128 rows x 7168 x 7168, groups of 128: 39.2 us, 335
+// TFLOP/s, against 69 us of the warp tiles.
 #include "matvec_int4_ring.cuh"
 
 namespace moedc {
@@ -486,12 +486,14 @@ int launch_tc_group(const moedc::MatvecArgs& a, int group, void* out, cudaStream
 // By rows an expert, as many as there can be: us of the warp tiles / of this kernel, with
 // 8 experts of 2048 x 7168 and with 64 of them (rows not quite equal among experts):
 //   rows             12         16         20         24         32         48
-//   group 128, 8   37 / 38    47 / 39    47 / 39    47 / 39    94 / 41    95 / 42
-//   group 128, 64 239 / 214  331 / 218  378 / 221  284 / 224  457 / 230  623 / 241
-//   group 64, 8    40 / 49    62 / 49    62 / 49    63 / 51    84 / 51    85 / 53
-//   group 64, 64  251 / 284  298 / 292  318 / 298  380 / 301  392 / 308  544 / 321
-// and 32 experts of 1024 x 2048: group 128 33 / 27 at 16 and 20, group 64 31 / 33 at 20
-// and 41 / 33 at 24.  Groups of 32 (eight accumulators a stage) 82 / 104 at 32 rows and
+//   group 128, 8   36 / 37    45 / 37    46 / 39    47 / 39    70 / 39    70 / 41
+//   group 128, 64 184 / 211  231 / 215  252 / 217  273 / 219  316 / 224  440 / 233
+//   group 64, 8    39 / 48    49 / 49    49 / 49    49 / 49    79 / 51    80 / 51
+//   group 64, 64  223 / 282  273 / 289  296 / 294  298 / 296  369 / 303  511 / 315
+// and 32 experts of 1024 x 2048: group 128 26 / 25 at 16, 27 / 27 at 20, 45 / 27 at 32,
+// group 64 29 / 32 at 20, 33 / 33 at 24, 51 / 33 at 32.  Many experts of few channels are
+// the exception: 128 of 2 x 768 x 2048 with SwiGLU, group 128, 122 / 172 at 20, 174 / 200
+// at 32.  Groups of 32 (eight accumulators a stage) 82 / 104 at 32 rows and
 // 105 / 211 at 20: never.
 bool matvec_tc_takes(int E, int rows, int group)
 {

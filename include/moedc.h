@@ -472,8 +472,10 @@ MOEDC_EXPORT int moedc_unsort_grad(const void* dy, int64_t lddy, const void* sor
  * gives an infinity of its weight's sign, or NaN where that weight is 0 or
  * another infinity has the other sign.
  * workspace: moedc_matvec_int4_workspace_bytes of the same arguments, 16-byte
- * aligned, no initialisation (x in the order the products read it).  The query
- * returns 0, and workspace may be NULL, where the weights to read are so few
+ * aligned, no initialisation.  It takes x in the order the products read it, in
+ * f16 by a power of two per row and 256 channels: bf16 values are exact down to
+ * 2^-27 of the largest of the 256, f16 values to 2^-24, and smaller ones are off
+ * by at most 2^-35 of it.  The query returns 0, and workspace may be NULL, where the weights to read are so few
  * that one launch without preparation is the faster form (and for arguments
  * that the call rejects).  Calls that can run at the same time need their own.
  * Data errors (dev_status): MOEDC_ERR_EXPERT_RANGE when a row's x row lies

@@ -3,10 +3,11 @@ product is exactly zero, so the other channels' sum keeps its bound (which
 counts |q - z| |x|), in every form of the product.
 
 x is N(0, 1) in bf16 beside values of about 2^22.  In the forms that bring x
-into f16, a value below 2^-28 of the record's largest is rounded by at most
-2^-35 of it: 2^-13 for the one value in 80 that lies below 2^-6, some 10 of
-1280 channels, times at most 15 scale steps, which is 0.02 scales, a third of
-the 0.07 or more that the bound's (Kd / 8 + 64) roundings give there."""
+into f16, a value below 2^-27 of the record's largest is rounded by at most
+2^-35 of it: 2^-13 for the one value in 40 that lies below 2^-5, some 30 of
+1280 channels, times at most 15 and of either sign.  That adds up to some
+0.005 scales, a tenth of the 0.05 that the bound's (Kd / 8 + 64) roundings give
+there."""
 import pytest
 import torch
 
