@@ -33,7 +33,7 @@ struct GateArgs {
     float scale;
 };
 
-// +inf counts as the largest finite value, so that exp(l - max) stays a number
+// +inf counts as the largest finite value in the weights, so that exp(l - max) stays a number
 // (a NaN stays one)
 __device__ __forceinline__ float gate_logit(float l) { return l > FLT_MAX ? FLT_MAX : l; }
 

@@ -357,10 +357,10 @@ MOEDC_EXPORT int moedc_layout_dispatch(const void* x, const int32_t* topk_idx,
  * that was trained for it chooses other experts under the first.  Without a
  * bias both choose by the logits.
  * An expert can be chosen when its logit, its bias and its key are neither
- * NaN nor -inf (mask experts with -inf; a mask of the type's lowest finite value leaves the
- * expert to be chosen last, with weight 0 next to ordinary logits).  +inf
- * counts as the largest finite binary32.  topk_idx[t] holds the K experts
- * with the largest keys, descending, ties to the lowest expert; where fewer
+ * NaN nor -inf (mask experts with -inf; a mask of the type's lowest finite
+ * value leaves the expert to be chosen last, with weight 0 next to ordinary
+ * logits).  In the weights +inf counts as the largest finite binary32.
+ * topk_idx[t] holds the K experts with the largest keys, descending, ties to the lowest expert; where fewer
  * can be chosen the rest is -1 with weight 0 (the masked entry of every other
  * call).  The weights come from the logits WITHOUT the bias, which moves the
  * choice alone, with C the chosen experts of the token:
