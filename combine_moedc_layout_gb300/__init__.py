@@ -6,8 +6,9 @@ workloads (synth).
 
 Beside the layout, dispatch and combine it carries the language-model
 operators around them: the top-k router (gate), the rows packed by expert
-(sort, unsort), their gradients, and the experts' products with 4-bit weights
-(matvec_int4).
+(sort, unsort), their gradients, the experts' products with 4-bit weights
+(matvec_int4) and with e4m3 ones (quant_e4m3, matmul_e4m3), and the experts' layers in
+training (matmul, swiglu_grad, matmul_grad).
 """
 from .moedc import (BF16, FP8_E4M3, SCALES_COL_MAJOR, SCALES_PER_TOKEN, Layout, MoedcError, alloc_recv, combine,
                     combine_e4m3, dequant_e4m3, moedc_combine_e4m3,
@@ -21,6 +22,8 @@ from .moedc import (F16, F32, GATE_BIAS_SCORE, GATE_NORMALIZE, GATE_SIGMOID, GAT
                     gate_grad, matvec_int4, moedc_gate, moedc_gate_grad, moedc_matvec_int4,
                     moedc_matvec_int4_workspace_bytes, moedc_sort, moedc_sort_rows, moedc_sort_workspace_bytes, moedc_unsort,
                     moedc_unsort_grad, sort, sort_grad, unsort, unsort_grad)
+from .moedc import (matmul, matmul_e4m3, matmul_grad, moedc_matmul, moedc_matmul_e4m3, moedc_matmul_grad,
+                    moedc_quant_e4m3, moedc_swiglu_grad, quant_e4m3, swiglu_grad)
 
 __all__ = ["BF16", "FP8_E4M3", "SCALES_COL_MAJOR", "SCALES_PER_TOKEN", "Layout", "MoedcError", "alloc_recv",
            "combine", "combine_e4m3", "dequant_e4m3", "moedc_combine_e4m3",
@@ -34,4 +37,6 @@ __all__ = ["BF16", "FP8_E4M3", "SCALES_COL_MAJOR", "SCALES_PER_TOKEN", "Layout",
            "Sorted", "gate", "gate_grad", "matvec_int4", "moedc_gate", "moedc_gate_grad",
            "moedc_matvec_int4", "moedc_matvec_int4_workspace_bytes", "moedc_sort", "moedc_sort_rows",
            "moedc_sort_workspace_bytes", "moedc_unsort", "moedc_unsort_grad", "sort", "sort_grad",
-           "unsort", "unsort_grad"]
+           "unsort", "unsort_grad",
+           "matmul", "matmul_e4m3", "matmul_grad", "moedc_matmul", "moedc_matmul_e4m3", "moedc_matmul_grad",
+           "moedc_quant_e4m3", "moedc_swiglu_grad", "quant_e4m3", "swiglu_grad"]

@@ -1,0 +1,74 @@
+// Products of packed expert rows in e4m3 with a scale for each block of 128.
+#include "matmul_pair.cuh"
+#include "tensor_map.cuh"
+
+namespace moedc_host {
+
+int launch_mm_e4m3(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream)
+{
+    constexpr auto kType = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    constexpr auto kSwizzle = CU_TENSOR_MAP_SWIZZLE_128B;
+    CUtensorMap l, r;
+    const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
+    const cuuint64_t lsize[2] = {K, (cuuint64_t)a.x_rows}, lstride[1] = {K};
+    const cuuint32_t lbox[2] = {128, a.src ? 1u : 32u};
+    const cuuint64_t size[4] = {K, N, parts, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * parts};
+    const cuuint32_t box[4] = {128, moedc::kMmHalf, 1, 1};
+    if (!tensor_map(&l, kType, kSwizzle, x, 2, lsize, lstride, lbox) || !tensor_map(&r, kType, kSwizzle, w, 4, size, stride, box))
+        return MOEDC_ERR_CUDA;
+    const int tile = a.gated ? moedc::kMmHalf : moedc::kMmTile;
+    const int64_t units = ((int64_t)a.rows / moedc::kMmTile + (a.E < a.rows ? a.E : a.rows)) * ((a.N + (int64_t)tile - 1) / tile);
+    return launch_mm_pair<moedc::kMmE4m3>(a, units, l, r, stream);
+}
+
+}  // namespace moedc_host
+
+extern "C" int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float* xs, int scale_layout, const void* w,
+                                 const float* ws, int E, int N, int flags, const int32_t* offsets,
+                                 const int32_t* counts, const int32_t* src, int top_k, int rows, int out_dtype, void* out,
+                                 float* out_scales, int32_t* dev_status, cudaStream_t stream)
+{
+    using namespace moedc_host;
+    const bool gated = (flags & MOEDC_SWIGLU) != 0, codes = out_dtype == MOEDC_FP8_E4M3;
+    const bool slots = counts && !offsets;
+    const int mode = scale_mode(scale_layout);
+    if (Kd < 128 || Kd % 128 != 0 || N < 1 || N > INT32_MAX / 2 || E < 1 || E > MOEDC_MAX_E || x_rows < 0 || rows < 0 ||
+        (flags & ~MOEDC_SWIGLU) != 0 || (out_dtype != MOEDC_BF16 && out_dtype != MOEDC_F16 && !codes))
+        return MOEDC_ERR_ARG;
+    if ((!counts && (offsets || E != 1)) || (slots && rows % E != 0) || mode < 0 || (mode == 1 && (!slots || src)) ||
+        (src && top_k < 1) || (!src && x_rows != rows) || (codes && N % 128 != 0))
+        return MOEDC_ERR_ARG;
+    if (!w || !ws || !dev_status || !aligned(x, 16) || !aligned(w, 16) || !aligned(xs, 4) || !aligned(ws, 4) ||
+        !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(src, 4) || !aligned(out, codes ? 16 : 2) ||
+        !aligned(out_scales, 4) || !aligned(dev_status, 4))
+        return MOEDC_ERR_ARG;
+    if (((int64_t)rows / 256 + E) * (N / 128 + 1) > INT32_MAX) return MOEDC_ERR_ARG;   // units are counted in 32 bits
+    if (rows == 0 || x_rows == 0) return MOEDC_OK;
+    if (!x || !xs || !out || (codes && !out_scales)) return MOEDC_ERR_ARG;
+    moedc::MmArgs a{};
+    a.E = E;
+    a.N = N;
+    a.K = Kd;
+    a.rows = rows;
+    a.x_rows = x_rows;
+    a.slots = rows / E;
+    a.top_k = top_k;
+    a.offsets = offsets;
+    a.counts = counts;
+    a.src = src;
+    a.status = dev_status;
+    a.xs = xs;
+    a.ws = ws;
+    const int64_t G = Kd / 128;
+    a.xs_r = mode == 0 ? G : 1;
+    a.xs_g = mode == 0 ? 1 : mode == 1 ? a.slots : 0;
+    a.xs_e = (mode == 2 ? 1 : G) * a.slots;
+    a.out = out;
+    a.extra = out_scales;
+    a.gated = gated;
+    a.f16 = out_dtype == MOEDC_F16;
+    a.codes = codes;
+    a.vec = N % 8 == 0 && aligned(out, 16);
+    a.wait_extra = test_wait_extra();
+    return launch_mm_e4m3(a, x, w, stream);
+}

@@ -412,27 +412,6 @@ matvec_int4_kernel(const __grid_constant__ MatvecArgs a, const __grid_constant__
 
 namespace moedc_host {
 
-namespace {
-
-bool tensor_map(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int dims,
-                const cuuint64_t* size, const cuuint64_t* stride, const cuuint32_t* box)
-{
-    static const PFN_cuTensorMapEncodeTiled_v12000 encode = [] {
-        void* p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault,
-                                             &found) != cudaSuccess || found != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p);
-    }();
-    if (!encode) return false;
-    const cuuint32_t elem[3] = {1, 1, 1};
-    return encode(map, type, dims, const_cast<void*>(base), size, stride, box, elem, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                  swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-}  // namespace
-
 bool matvec_weight_map(CUtensorMap* map, const void* wq, int Kd, int64_t rows, int box_rows)
 {
     const cuuint64_t size[2] = {(cuuint64_t)Kd / 2, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)Kd / 2};

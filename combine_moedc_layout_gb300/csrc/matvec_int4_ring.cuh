@@ -1,82 +1,21 @@
-// What the two ring kernels of the 4-bit expert products share: bounded waits on
-// mbarriers, the records of x, scales in registers, the weights' tensor map.
+// What the two ring kernels of the 4-bit expert products share: the records of x,
+// scales in registers, the weights' tensor map.
 #pragma once
 
 #include <type_traits>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "matvec_int4.cuh"
-#include "per_device.cuh"
+#include "mbarrier.cuh"
+#include "tensor_map.cuh"
 
 namespace moedc {
 
 constexpr int kMvChunk = 256;                          // channels of a stage (of one part of K)
-constexpr unsigned long long kMvWaitNs = 200000000ull; // bound of every wait
 // A record of x: 256 channels in f16, then (16-byte aligned, for TMA) 2^12 / scale.
 // 576 bytes apart, the rows that a quarter-warp reads lie in different halves of the
 // banks.
 constexpr int kMvRecord = kMvChunk * 2 + 64;
 constexpr int kMvFactor = kMvChunk * 2 + 32;
-
-// ---------------------------------------------------------------- mbarriers
-
-__device__ __forceinline__ uint32_t smem_u32(const void* p)
-{
-    return (uint32_t)__cvta_generic_to_shared(p);
-}
-__device__ __forceinline__ void mbar_init(uint64_t* b, int count)
-{
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_u32(b)), "r"(count) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive(uint64_t* b)
-{
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(b)) : "memory");
-}
-__device__ __forceinline__ void mbar_arrive_expect(uint64_t* b, int bytes)
-{
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(b)), "r"(bytes)
-                 : "memory");
-}
-__device__ __forceinline__ bool mbar_try(uint64_t* b, int parity)
-{
-    uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n"
-                 " mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n"
-                 " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
-    return ok != 0;
-}
-__device__ __forceinline__ unsigned long long globaltimer()
-{
-    unsigned long long t;
-    asm volatile("mov.u64 %0, %%globaltimer;" : "=l"(t));
-    return t;
-}
-// Bounded: false when the wait ran out or another one of the block did
-// (*abort).  The callers then go on without waiting, so that every barrier of
-// the block is still met and the kernel ends; the status word tells.
-static __device__ __noinline__ bool mbar_wait_slow(uint64_t* b, int parity, volatile int* abort)
-{
-    // the timer is read only once the wait is a long one: reading it takes longer than
-    // most waits
-    unsigned long long t0 = 0;
-    if (*abort) return false;
-    for (int i = 0; ; ++i) {
-        if (mbar_try(b, parity)) return true;
-        if (i % 1024 != 1023) continue;
-        if (*abort) return false;
-        const unsigned long long now = globaltimer();
-        if (t0 == 0) t0 = now;
-        else if (now - t0 > kMvWaitNs) break;
-    }
-    *abort = 1;
-    return false;
-}
-__device__ __forceinline__ bool mbar_wait(uint64_t* b, int parity, volatile int* abort)
-{
-    return mbar_try(b, parity) || mbar_wait_slow(b, parity, abort);
-}
 
 // Scales and zero points of R weight rows for one stage, in registers as they come
 // from memory.
@@ -190,33 +129,11 @@ __device__ __forceinline__ uint32_t sub_f16x2(uint32_t a, uint32_t b)
     return r;
 }
 
-// Where a stage's slot and phase go round the ring.
-struct MvRing {
-    int slot = 0, phase = 0;
-    __device__ __forceinline__ void next(int stages)
-    {
-        if (++slot == stages) {
-            slot = 0;
-            phase ^= 1;
-        }
-    }
-};
-
 }  // namespace moedc
 
 namespace moedc_host {
 
 constexpr int kMvSmem = 227 * 1024;
-
-// `raised`: of this kernel
-inline bool raise_smem_limit(PerDevice& raised, const void* kernel, int bytes)
-{
-    int device = 0;
-    if (cudaGetDevice(&device) != cudaSuccess) return false;
-    return raised.once(device, [&] {
-        return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess;
-    });
-}
 
 // Rows of Kd / 2 bytes, boxes of box_rows x 128 bytes in the 128-byte swizzle.  False
 // when the driver refuses.

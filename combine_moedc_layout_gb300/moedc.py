@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 from dataclasses import dataclass
 
@@ -47,8 +48,10 @@ EXPORTED = ("moedc_api_version", "moedc_strerror", "moedc_layout_workspace_bytes
             "moedc_layout_static_scratch", "moedc_dequant_e4m3", "moedc_rank_layout",
             "moedc_rank_dispatch", "moedc_rank_combine", "moedc_combine_e4m3",
             "moedc_gate", "moedc_gate_grad", "moedc_sort_rows", "moedc_sort_workspace_bytes",
-           "moedc_sort", "moedc_unsort", "moedc_unsort_grad", "moedc_matvec_int4",
-           "moedc_matvec_int4_workspace_bytes", "moedc_layout_dispatch_workspace_bytes", "moedc_test_set_wait_extra")
+            "moedc_sort", "moedc_unsort", "moedc_unsort_grad", "moedc_matvec_int4",
+           "moedc_matvec_int4_workspace_bytes", "moedc_quant_e4m3", "moedc_matmul_e4m3",
+            "moedc_matmul", "moedc_swiglu_grad", "moedc_matmul_grad",
+            "moedc_layout_dispatch_workspace_bytes", "moedc_test_set_wait_extra")
 
 STATIC_SCRATCH_BYTES = 1 << 20   # MOEDC_STATIC_SCRATCH_BYTES
 
@@ -125,6 +128,16 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.moedc_matvec_int4.restype = I
     lib.moedc_matvec_int4_workspace_bytes.argtypes = [I, I, I, I, I, I]
     lib.moedc_matvec_int4_workspace_bytes.restype = Z
+    lib.moedc_quant_e4m3.argtypes = [P, L, I, I, I, I, I, P, P, P]
+    lib.moedc_quant_e4m3.restype = I
+    lib.moedc_matmul_e4m3.argtypes = [P, I, I, P, I, P, P, I, I, I, P, P, P, I, I, I, P, P, P, P]
+    lib.moedc_matmul_e4m3.restype = I
+    lib.moedc_matmul.argtypes = [P, L, I, I, P, I, I, I, P, P, I, P, P, P, P]
+    lib.moedc_matmul.restype = I
+    lib.moedc_swiglu_grad.argtypes = [P, L, P, I, I, I, P, P]
+    lib.moedc_swiglu_grad.restype = I
+    lib.moedc_matmul_grad.argtypes = [P, L, P, L, P, I, I, I, I, P, P, I, P, P, I, P, P]
+    lib.moedc_matmul_grad.restype = I
     lib.moedc_test_set_wait_extra.argtypes = [ctypes.c_uint]
     lib.moedc_test_set_wait_extra.restype = None
     if path is None:
@@ -296,6 +309,37 @@ def moedc_matvec_int4(x, ldx, dtype, x_rows, Kd, wq, scales, scale_dtype, zeros,
                                     scale_dtype, _p(zeros), group, E, N, flags, _p(offsets),
                                     _p(counts), _p(src), top_k, rows, _p(out), _p(workspace),
                                     workspace_bytes, _p(dev_status), _stream(stream))
+
+
+def moedc_quant_e4m3(x, ldx, dtype, E, rows, Kd, block_rows, codes, scales, stream=None) -> int:
+    return load().moedc_quant_e4m3(_p(x), ldx, dtype, E, rows, Kd, block_rows, _p(codes),
+                                   _p(scales), _stream(stream))
+
+
+def moedc_matmul_e4m3(x, x_rows, Kd, xs, scale_layout, w, ws, E, N, flags, offsets, counts, src,
+                      top_k, rows, out_dtype, out, out_scales, dev_status, stream=None) -> int:
+    return load().moedc_matmul_e4m3(_p(x), x_rows, Kd, _p(xs), scale_layout, _p(w), _p(ws), E, N,
+                                    flags, _p(offsets), _p(counts), _p(src), top_k, rows,
+                                    out_dtype, _p(out), _p(out_scales), _p(dev_status),
+                                    _stream(stream))
+
+
+def moedc_matmul(x, ldx, dtype, Kd, w, E, N, flags, offsets, counts, rows, out, products,
+                 dev_status, stream=None) -> int:
+    return load().moedc_matmul(_p(x), ldx, dtype, Kd, _p(w), E, N, flags, _p(offsets), _p(counts),
+                               rows, _p(out), _p(products), _p(dev_status), _stream(stream))
+
+
+def moedc_swiglu_grad(dh, lddh, products, dtype, rows, N, dproducts, stream=None) -> int:
+    return load().moedc_swiglu_grad(_p(dh), lddh, _p(products), dtype, rows, N, _p(dproducts),
+                                    _stream(stream))
+
+
+def moedc_matmul_grad(dout, lddout, x, ldx, w, dtype, Kd, E, N, offsets, counts, rows, dx, dw,
+                      dw_dtype, dev_status, stream=None) -> int:
+    return load().moedc_matmul_grad(_p(dout), lddout, _p(x), ldx, _p(w), dtype, Kd, E, N,
+                                    _p(offsets), _p(counts), rows, _p(dx), _p(dw), dw_dtype,
+                                    _p(dev_status), _stream(stream))
 
 
 # ---------------------------------------------------------------- conveniences
@@ -761,4 +805,257 @@ def matvec_int4(x: torch.Tensor, wq: torch.Tensor, scales: torch.Tensor,
                                  status.data_ptr(), _stream(None)), "moedc_matvec_int4")
     if wait:
         _check(int(status), "moedc_matvec_int4")
+    return out
+
+
+# ------------------------------------------------ e4m3 products, layers in training
+
+
+def _maps(offsets, counts, E: int) -> None:
+    if offsets is not None:
+        _need(offsets, torch.int32, "offsets")
+        _need_shape(offsets, (E + 1,), "offsets")
+        if counts is None:
+            raise ValueError("offsets need counts")
+    if counts is not None:
+        _need(counts, torch.int32, "counts")
+        _need_shape(counts, (E,), "counts")
+
+
+def _status(status, device):
+    """(status tensor, whether the call waits for its kernels and raises their errors)"""
+    if status is not None:
+        _need(status, torch.int32, "status")
+        return status, False
+    if torch.cuda.is_current_stream_capturing():
+        raise ValueError("status must be given while a graph is captured")
+    return torch.zeros(1, dtype=torch.int32, device=device), True
+
+
+def quant_e4m3(x: torch.Tensor, block_rows: int = 1, out=None):
+    """(codes float8_e4m3fn of x's shape, scales fp32) of rows [R, Kd] or experts'
+    weights [E, N, Kd] by dispatch's rule.  block_rows 1: a scale for each 128
+    channels of a row, [..., Kd/128]; 128: for each 128 x 128 block, [E,
+    ceil(N/128), Kd/128] ([ceil(R/128), Kd/128] for rows).  `out` takes an
+    earlier call's result to write into."""
+    if x.dim() == 3:
+        _need(x, x.dtype, "x")
+        ld = x.shape[2]
+        E, R, Kd = x.shape
+    else:
+        ld = _need_rows(x, "x")
+        E, (R, Kd) = 1, x.shape
+    dtype = _lm_dtype(x, "x")
+    if block_rows not in (1, 128):
+        raise ValueError("block_rows must be 1 or 128")
+    shape = (*x.shape[:-2], -(-R // block_rows), Kd // 128)
+    if out is None:
+        out = (torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device),
+               torch.empty(shape, dtype=torch.float32, device=x.device))
+    codes, scales = out
+    _need(codes, torch.float8_e4m3fn, "out[0]")
+    _need_shape(codes, x.shape, "out[0]")
+    _need(scales, torch.float32, "out[1]")
+    _need_shape(scales, shape, "out[1]")
+    _check((_lib or load()).moedc_quant_e4m3(x.data_ptr(), ld, dtype, E, R, Kd, block_rows,
+                                             codes.data_ptr(), scales.data_ptr(), _stream(None)),
+           "moedc_quant_e4m3")
+    return out
+
+
+_E4M3_OUT = {BF16: torch.bfloat16, F16: torch.float16, FP8_E4M3: torch.float8_e4m3fn}
+
+
+def matmul_e4m3(x: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Tensor,
+                offsets: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                src: torch.Tensor | None = None, top_k: int = 1, swiglu: bool = False,
+                out_dtype: int = BF16, scale_layout: int = 0,
+                status: torch.Tensor | None = None, out=None):
+    """out [R, N]: packed expert rows x e4m3 [R, Kd] with scales xs [R, Kd/128],
+    times e4m3 weights w [E, N, Kd] ([N, Kd]: one linear layer) with scales ws
+    [E, ceil(N/128), Kd/128]; swiglu: 2N weight rows and 2 ceil(N/128) blocks,
+    silu(gate) * up.  offsets and counts from sort(); counts alone: x [E, cap, Kd]
+    is dispatch()'s receive buffer (xs in its scale_layout) and out [E, cap, N].
+    src (and top_k): out row r is of x row src[r] // top_k.  out_dtype BF16, F16,
+    or FP8_E4M3: (codes, scales [R, N/128]), rows for the next product.  status
+    (int32 [1]) takes data errors; without one the call waits and raises them."""
+    if w.dim() == 2:
+        w, ws = w[None], ws[None]
+    e4m3 = torch.float8_e4m3fn
+    _need(x, e4m3, "x")
+    _need(w, e4m3, "w")
+    _need(xs, torch.float32, "xs")
+    _need(ws, torch.float32, "ws")
+    E, wn, Kd = w.shape
+    G = Kd // 128
+    if swiglu and wn % 2:
+        raise ValueError("swiglu needs an even number of weight rows")
+    N = wn // 2 if swiglu else wn
+    _need_shape(ws, (E, -(-N // 128) * (2 if swiglu else 1), G), "ws")
+    _maps(offsets, counts, E)
+    if src is not None:
+        _need(src, torch.int32, "src")
+    slots = counts is not None and offsets is None
+    if slots:
+        lead = (src if src is not None else x).shape[:2]
+        if len(lead) != 2 or lead[0] != E:
+            raise ValueError(f"counts alone need {'src' if src is not None else 'x'} as [{E}, cap, ...]")
+    else:
+        lead = (src if src is not None else x).shape[:1]
+    if x.dim() != (3 if slots and src is None else 2) or x.shape[-1] != Kd:
+        raise ValueError(f"x must have {Kd} channels and the dimensions of its rows, not {tuple(x.shape)}")
+    if src is not None and src.dim() != len(lead):
+        raise ValueError(f"src must be {len(lead)}-dimensional")
+    rows = math.prod(lead)
+    x_rows = math.prod(x.shape[:-1])
+    if scale_layout == SCALES_COL_MAJOR:
+        if not slots or src is not None:
+            raise ValueError("SCALES_COL_MAJOR is the receive buffer's: counts alone, no src")
+        _need_shape(xs, (E, G, lead[1]), "xs")
+    elif scale_layout == SCALES_PER_TOKEN:
+        _need_shape(xs, x.shape[:-1], "xs")
+    elif scale_layout == 0:
+        _need_shape(xs, (*x.shape[:-1], G), "xs")
+    else:
+        raise ValueError("scale_layout must be 0, SCALES_COL_MAJOR or SCALES_PER_TOKEN")
+    if out_dtype not in _E4M3_OUT:
+        raise ValueError("out_dtype must be BF16, F16 or FP8_E4M3")
+    codes = out_dtype == FP8_E4M3
+    if codes and N % 128:
+        raise ValueError("FP8_E4M3 output needs a multiple of 128 columns")
+    if out is None:
+        out = torch.empty((*lead, N), dtype=_E4M3_OUT[out_dtype], device=x.device)
+        if codes:
+            out = (out, torch.empty((*lead, N // 128), dtype=torch.float32, device=x.device))
+    y, ys = out if codes else (out, None)
+    _need(y, _E4M3_OUT[out_dtype], "out")
+    _need_shape(y, (*lead, N), "out")
+    if codes:
+        _need(ys, torch.float32, "out[1]")
+        _need_shape(ys, (*lead, N // 128), "out[1]")
+    status, wait = _status(status, x.device)
+    _check((_lib or load()).moedc_matmul_e4m3(
+        x.data_ptr(), x_rows, Kd, xs.data_ptr(), scale_layout, w.data_ptr(), ws.data_ptr(), E, N,
+        SWIGLU if swiglu else 0, _p(offsets), _p(counts), _p(src), top_k, rows, out_dtype,
+        y.data_ptr(), _p(ys), status.data_ptr(), _stream(None)), "moedc_matmul_e4m3")
+    if wait:
+        _check(int(status), "moedc_matmul_e4m3")
+    return out
+
+
+def _experts(w: torch.Tensor):
+    return w if w.dim() == 3 else w[None]
+
+
+def matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor | None = None,
+           counts: torch.Tensor | None = None, swiglu: bool = False, keep: bool = False,
+           status: torch.Tensor | None = None, out=None):
+    """out [R, N]: packed expert rows x [R, Kd] (bf16 or f16) times w [E, N, Kd]
+    ([N, Kd]: one linear layer); swiglu: 2N weight rows, silu(gate) * up, and with
+    keep (out, products [R, 2N]), which swiglu_grad() takes.  offsets and counts
+    from sort(); counts alone: expert e's rows begin at e * (R / E).  status as for
+    matmul_e4m3()."""
+    ld = _need_rows(x, "x")
+    w = _experts(w)
+    _need(w, x.dtype, "w")
+    dtype = _lm_dtype(x, "x")
+    E, wn, Kd = w.shape
+    R = x.shape[0]
+    if x.shape[1] != Kd:
+        raise ValueError(f"x must have {Kd} channels, not {x.shape[1]}")
+    if swiglu and wn % 2:
+        raise ValueError("swiglu needs an even number of weight rows")
+    if keep and not swiglu:
+        raise ValueError("keep goes with swiglu")
+    N = wn // 2 if swiglu else wn
+    _maps(offsets, counts, E)
+    if out is None:
+        out = torch.empty((R, N), dtype=x.dtype, device=x.device)
+        if keep:
+            out = (out, torch.empty((R, wn), dtype=x.dtype, device=x.device))
+    y, products = out if keep else (out, None)
+    _need(y, x.dtype, "out")
+    _need_shape(y, (R, N), "out")
+    if keep:
+        _need(products, x.dtype, "out[1]")
+        _need_shape(products, (R, wn), "out[1]")
+    status, wait = _status(status, x.device)
+    _check((_lib or load()).moedc_matmul(
+        x.data_ptr(), ld, dtype, Kd, w.data_ptr(), E, N, SWIGLU if swiglu else 0, _p(offsets),
+        _p(counts), R, y.data_ptr(), _p(products), status.data_ptr(), _stream(None)),
+        "moedc_matmul")
+    if wait:
+        _check(int(status), "moedc_matmul")
+    return out
+
+
+def swiglu_grad(dh: torch.Tensor, products: torch.Tensor,
+                out: torch.Tensor | None = None) -> torch.Tensor:
+    """dproducts [R, 2N] of matmul(swiglu=True, keep=True), from dh [R, N]; `out`
+    may be products itself."""
+    ld = _need_rows(dh, "dh")
+    dtype = _lm_dtype(dh, "dh")
+    R, N = dh.shape
+    _need(products, dh.dtype, "products")
+    _need_shape(products, (R, 2 * N), "products")
+    if out is None:
+        out = torch.empty_like(products)
+    _need(out, dh.dtype, "out")
+    _need_shape(out, (R, 2 * N), "out")
+    _check((_lib or load()).moedc_swiglu_grad(dh.data_ptr(), ld, products.data_ptr(), dtype, R, N,
+                                              out.data_ptr(), _stream(None)), "moedc_swiglu_grad")
+    return out
+
+
+def matmul_grad(dout: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | None,
+                offsets: torch.Tensor | None = None, counts: torch.Tensor | None = None,
+                dw_dtype: torch.dtype | None = None, status: torch.Tensor | None = None,
+                out=None):
+    """(dx [R, Kd], dw [E, N, Kd]) of matmul() from dout [R, N] (swiglu: from
+    swiglu_grad()).  x None: dx alone; w None: dw alone, with counts or one expert; the
+    other is None.  dw_dtype: x's type or float32.  status as for matmul_e4m3()."""
+    ld = _need_rows(dout, "dout")
+    dtype = _lm_dtype(dout, "dout")
+    R, N = dout.shape
+    if x is None and w is None:
+        raise ValueError("x or w must be given")
+    ldx = 0
+    flat = w is not None and w.dim() == 2
+    if w is not None:
+        w = _experts(w)
+        _need(w, dout.dtype, "w")
+        E, Kd = w.shape[0], w.shape[2]
+        _need_shape(w, (E, N, Kd), "w")
+    else:
+        E, Kd = counts.shape[0] if counts is not None else 1, x.shape[-1]
+    if x is not None:
+        ldx = _need_rows(x, "x")
+        if x.dtype != dout.dtype:
+            raise ValueError(f"x must be {dout.dtype}, not {x.dtype}")
+        _need_shape(x, (R, Kd), "x")
+    _maps(offsets, counts, E)
+    if out is None:
+        shape = (N, Kd) if flat else (E, N, Kd)
+        out = (torch.empty((R, Kd), dtype=dout.dtype, device=dout.device) if w is not None else None,
+               torch.empty(shape, dtype=dw_dtype or dout.dtype, device=dout.device)
+               if x is not None else None)
+    dx, dw = out
+    if (dx is None) != (w is None) or (dw is None) != (x is None):
+        raise ValueError("out must hold dx when w is given and dw when x is")
+    if dx is not None:
+        _need(dx, dout.dtype, "out[0]")
+        _need_shape(dx, (R, Kd), "out[0]")
+    if dw is not None:
+        if dw.dtype not in (dout.dtype, torch.float32) or (dw_dtype or dw.dtype) != dw.dtype:
+            raise ValueError(f"dw must be {dout.dtype} or float32, not {dw_dtype or dw.dtype}")
+        _need(dw, dw.dtype, "out[1]")
+        if dw.numel() != E * N * Kd or dw.shape[-2:] != (N, Kd):
+            raise ValueError(f"out[1] must have shape {(E, N, Kd)}, not {tuple(dw.shape)}")
+    status, wait = _status(status, dout.device)
+    _check((_lib or load()).moedc_matmul_grad(
+        dout.data_ptr(), ld, _p(x), ldx, _p(w), dtype, Kd, E, N, _p(offsets), _p(counts), R,
+        _p(dx), _p(dw), F32 if dw is not None and dw.dtype == torch.float32 else dtype,
+        status.data_ptr(), _stream(None)), "moedc_matmul_grad")
+    if wait:
+        _check(int(status), "moedc_matmul_grad")
     return out

@@ -494,6 +494,103 @@ MOEDC_EXPORT int moedc_matvec_int4(const void* x, int64_t ldx, int dtype, int x_
                  cudaStream_t stream);
 
 /*
+ * Rows or blocks to e4m3 with binary32 scales, by the rule of moedc_dispatch:
+ *   a = max |x| of the group, scale = max(a, 1e-4f) / 448 (IEEE division),
+ *   code = e4m3fn(x / scale), nearest even, saturating to +-448.
+ * x dtype MOEDC_BF16, MOEDC_F16 or MOEDC_F32, [E, rows, Kd] with ldx >= Kd
+ * elements from row to row; codes [E, rows, Kd] contiguous.
+ *   block_rows 1    groups of 128 channels of a row, scales [E, rows, Kd / 128]:
+ *                   what moedc_dispatch writes
+ *   block_rows 128  blocks of 128 rows x 128 channels (the last rows of an
+ *                   expert a smaller one), scales [E, ceil(rows / 128), Kd / 128]:
+ *                   weights of moedc_matmul_e4m3
+ * As in dispatch a NaN is left out of the maximum and stays NaN; an infinity
+ * makes its group's scale infinite, its own code NaN and the others' 0.
+ * Kd % 128 == 0; x and codes 16-byte aligned, ldx whole 16-byte units.  No data errors.
+ */
+MOEDC_EXPORT int moedc_quant_e4m3(const void* x, int64_t ldx, int dtype, int E, int rows, int Kd,
+                 int block_rows, void* codes, float* scales, cudaStream_t stream);
+
+/*
+ * Products of packed expert rows with e4m3 weights, both with a binary32 scale
+ * for each block of 128: the experts' linear layers behind an e4m3 dispatch
+ * (E = 1: one ordinary linear layer).  For every row r of expert e, n < N:
+ *   dot(r, n) = sum over g of xs[r'][g] * ws[e][n / 128][g]
+ *                             * sum over k in 128g..128g+127 of x[r'][k] * w[e][n][k]
+ *   v[r][n] = dot(r, n)                                           flags 0
+ *   v[r][n] = silu(dot(r, n)) * dot(r, N + n)                     MOEDC_SWIGLU
+ * silu(a) = a / (1 + exp(-a)); binary32 sums.  With MOEDC_SWIGLU w is
+ * [E, 2N, Kd], gate rows 0..N-1, up rows N..2N-1, and ws [E, 2, ceil(N / 128),
+ * Kd / 128]: gate blocks, up blocks, each counted from their own first row.
+ * Rows of expert e:
+ *   offsets, counts (moedc_sort)     offsets[e] .. + counts[e]
+ *   counts alone (moedc_layout)      e * (rows / E) .. + min(counts[e], rows / E):
+ *                                    the receive buffer of moedc_dispatch
+ *   neither, E = 1                   all rows
+ * r' = r, with x_rows = rows; or src[r] / top_k with src, whose rows may be
+ * gathered from any x (of moedc_sort, with its top_k; src_idx of
+ * moedc_dispatch, with top_k 1).  x_rows = 0: nothing is written.
+ *   x     e4m3 [x_rows, Kd], contiguous
+ *   xs    scale_layout 0 [x_rows, Kd / 128]; MOEDC_SCALES_PER_TOKEN [x_rows];
+ *         MOEDC_SCALES_COL_MAJOR [E, Kd / 128, rows / E] (counts alone, no src)
+ *   out   [rows, N], rows that belong to no expert are not written:
+ *         out_dtype MOEDC_BF16 or MOEDC_F16: v rounded once
+ *         MOEDC_FP8_E4M3: codes and out_scales [rows, N / 128] of v by
+ *         dispatch's rule, N % 128 == 0: rows for the next product
+ * NaN codes stay in their own row's outputs (of x) or their own column's (of w).
+ * Kd % 128 == 0; x, w and e4m3 out 16-byte aligned, out otherwise 2-byte.
+ * Data errors (dev_status): MOEDC_ERR_EXPERT_RANGE when src leads outside
+ * [0, x_rows) (the row counts as zeros), MOEDC_ERR_CAPACITY when an expert's rows
+ * pass `rows` or its slots (those are skipped), MOEDC_ERR_TIMEOUT if a bounded wait
+ * gave up (its outputs are then unspecified).
+ */
+MOEDC_EXPORT int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float* xs, int scale_layout,
+                 const void* w, const float* ws, int E, int N, int flags, const int32_t* offsets,
+                 const int32_t* counts, const int32_t* src, int top_k, int rows, int out_dtype,
+                 void* out, float* out_scales, int32_t* dev_status, cudaStream_t stream);
+
+/*
+ * The experts' layers in training: products of packed rows with 16-bit weights,
+ * the gated feed-forward block in one kernel, and their gradients.
+ *
+ * moedc_matmul, for every row r of expert e (rows as for moedc_matmul_e4m3):
+ *   p(n) = sum over k of x[r][k] * w[e][n][k], binary32
+ *   out[r][n] = round( p(n) ), n < N                              flags 0
+ *   out[r][n] = round( silu(p(n)) * p(N + n) )                    MOEDC_SWIGLU
+ * With MOEDC_SWIGLU w is [E, 2N, Kd] (gate rows, then up rows) and products,
+ * when given, takes round( p(n) ), n < 2N, as [rows, 2N]: what the gradient needs.
+ *
+ * moedc_swiglu_grad, elementwise over all rows, from dh [rows, N] (lddh elements
+ * from row to row) and products [rows, 2N]: with g = products[r][n],
+ * u = products[r][N + n], s = 1 / (1 + exp(-g)),
+ *   dproducts[r][n]     = round( dh[r][n] * u * s * (1 + g * (1 - s)) )
+ *   dproducts[r][N + n] = round( dh[r][n] * g * s )
+ * dproducts may be products itself.
+ *
+ * moedc_matmul_grad, gradients of the plain product (flags 0) with N weight rows;
+ * of the gated one with dout = dproducts and N twice as large:
+ *   dx[r][k]    = round( sum over n of dout[r][n] * w[e][n][k] )
+ *   dw[e][n][k] = round( sum over e's rows r of dout[r][n] * x[r][k] ); 0 without rows
+ * dx or dw may be NULL and is then not computed (w is read for dx alone, x for dw
+ * alone).  dw_dtype is dtype or MOEDC_F32.  Rows that belong to no expert are
+ * neither read into any result nor written.  The order of every sum is fixed:
+ * equal inputs give equal bits.
+ * dtype MOEDC_BF16 or MOEDC_F16; Kd and N multiples of 8; leading dimensions
+ * multiples of 8; matrices 16-byte aligned, all but x, dh and dout contiguous.
+ * Data errors (dev_status): MOEDC_ERR_CAPACITY and MOEDC_ERR_TIMEOUT as for
+ * moedc_matmul_e4m3.
+ */
+MOEDC_EXPORT int moedc_matmul(const void* x, int64_t ldx, int dtype, int Kd, const void* w, int E,
+                 int N, int flags, const int32_t* offsets, const int32_t* counts, int rows,
+                 void* out, void* products, int32_t* dev_status, cudaStream_t stream);
+MOEDC_EXPORT int moedc_swiglu_grad(const void* dh, int64_t lddh, const void* products, int dtype,
+                 int rows, int N, void* dproducts, cudaStream_t stream);
+MOEDC_EXPORT int moedc_matmul_grad(const void* dout, int64_t lddout, const void* x, int64_t ldx,
+                 const void* w, int dtype, int Kd, int E, int N, const int32_t* offsets,
+                 const int32_t* counts, int rows, void* dx, void* dw, int dw_dtype,
+                 int32_t* dev_status, cudaStream_t stream);
+
+/*
  * Test hook, not for production use.  With extra_arrivals = n > 0, every
  * later bounded wait of the library waits for something that never comes:
  * the cooperative launch of moedc_layout_dispatch makes its grid barriers
