@@ -132,8 +132,9 @@ extern "C" int moedc_matmul_grad(const void* dout, int64_t lddout, const void* x
     if (dx && (!w || !aligned(w, 16))) return MOEDC_ERR_ARG;
     if (dw && (ldx < Kd || ldx % 8 != 0 || !aligned(x, 16))) return MOEDC_ERR_ARG;
     if (rows == 0) {
+        if (!dw) return MOEDC_OK;
         clear_stale_error();
-        if (dw) (void)cudaMemsetAsync(dw, 0, (size_t)E * N * Kd * lm_dtype_size(dw_dtype), stream);
+        (void)cudaMemsetAsync(dw, 0, (size_t)E * N * Kd * lm_dtype_size(dw_dtype), stream);
         return launch_status();
     }
     if (!dout || (dw && !x)) return MOEDC_ERR_ARG;
