@@ -428,11 +428,9 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                 const MmUnit u = mm_unit<MODE>(a, s_pre, s_beg, s_end, tiles, unit);
                 for (int s = 0; s < u.ksteps; ++s) {
                     if ((MODE == kMmE4m3 || s == 0) && k++ >= 2) {
-                        mbar_wait_pair(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
-                        __syncwarp();
+                        mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
                     }
-                    mbar_wait_pair(ready + ring.slot, ring.phase, &s_abort);
-                    __syncwarp();
+                    mbar_wait_warp(ready + ring.slot, ring.phase, &s_abort);
                     tc_fence_after();
                     const uint32_t left = smem_u32(smem + ring.slot * kMmStage);
                     const uint64_t l = MODE == kMmDw ? tc_smem_desc_mn(left, kMmOperand / 2) : tc_smem_desc(left);
@@ -471,11 +469,13 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
             const MmUnit u = mm_unit<MODE>(a, s_pre, s_beg, s_end, tiles, unit);
             for (int s = 0; s < u.ksteps; ++s) {
                 mbar_wait_warp(full + ring.slot, ring.phase, &s_abort);
+                bool cleared = false;
                 if constexpr (MODE == kMmDw) {
                     // rows behind the expert's last one, up to the end of their 16: a row is 128
                     // bytes of each of the four boxes, in whatever order
                     const int have = u.m - s * kElems, to = min((have + 15) / 16 * 16, kElems);
-                    if (have < to) {
+                    cleared = have < to;
+                    if (cleared) {
                         for (int i = lane; i < (to - have) * 32; i += kWarp) {
                             const int box = i & 3, chunk = (i >> 2) & 7, row = have + (i >> 5);
                             *reinterpret_cast<uint4*>(smem + ring.slot * kMmStage + box * (kMmOperand / 2) + row * kMmBytes +
@@ -485,7 +485,10 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                         __syncwarp();
                     }
                 }
-                if (lane == 0) mbar_arrive_pair(ready + ring.slot, 0);
+                if (lane == 0) {
+                    if (cleared) mbar_arrive_pair_release(ready + ring.slot, 0);
+                    else mbar_arrive_pair(ready + ring.slot, 0);
+                }
                 ring.next(kMmStages);
             }
         }

@@ -81,25 +81,20 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// one arrival at the barrier of that name in block `rank` of the cluster
+// One arrival at the barrier of that name in block `rank` of the cluster.  What it orders
+// is copies and tensor-memory accesses, which their own completion and fences order; with
+// the release of a cluster's scope spelled out an arrival waits on a memory barrier of some
+// 1.2 us.
 __device__ __forceinline__ void mbar_arrive_pair(uint64_t* b, int rank)
 {
     asm volatile("{\n .reg .b32 at;\n mapa.shared::cluster.u32 at, %0, %1;\n"
+                 " mbarrier.arrive.shared::cluster.b64 _, [at];\n}\n" ::"r"(smem_u32(b)), "r"(rank) : "memory");
+}
+// the same for plain stores to shared memory before it
+__device__ __forceinline__ void mbar_arrive_pair_release(uint64_t* b, int rank)
+{
+    asm volatile("{\n .reg .b32 at;\n mapa.shared::cluster.u32 at, %0, %1;\n"
                  " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [at];\n}\n" ::"r"(smem_u32(b)), "r"(rank) : "memory");
-}
-__device__ __forceinline__ bool mbar_try_pair(uint64_t* b, int parity)
-{
-    uint32_t ok;
-    asm volatile("{\n .reg .pred p;\n"
-                 " mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n"
-                 " selp.u32 %0, 1, 0, p;\n}\n" : "=r"(ok) : "r"(smem_u32(b)), "r"(parity) : "memory");
-    return ok != 0;
-}
-// for what arrivals of the other block order; bounded as mbar_wait is
-__device__ __forceinline__ bool mbar_wait_pair(uint64_t* b, int parity, volatile int* abort)
-{
-    if (mbar_try_pair(b, parity)) return true;
-    return mbar_wait_slow(b, parity, abort) && mbar_try_pair(b, parity);
 }
 __device__ __forceinline__ void tc_alloc_pair(uint32_t* at, uint32_t columns)
 {
