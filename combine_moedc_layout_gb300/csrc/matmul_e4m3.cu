@@ -8,17 +8,18 @@ int launch_mm_e4m3(const moedc::MmArgs& a, const void* x, const void* w, cudaStr
 {
     constexpr auto kType = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     constexpr auto kSwizzle = CU_TENSOR_MAP_SWIZZLE_128B;
-    CUtensorMap l, r;
+    CUtensorMap l, r, all;   // left in boxes of 32 rows (gathered: one) and of 128
     const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
     const cuuint64_t lsize[2] = {K, (cuuint64_t)a.x_rows}, lstride[1] = {K};
-    const cuuint32_t lbox[2] = {128, a.src ? 1u : 32u};
+    const cuuint32_t lbox[2] = {128, a.src ? 1u : 32u}, allbox[2] = {128, moedc::kMmHalf};
     const cuuint64_t size[4] = {K, N, parts, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * parts};
     const cuuint32_t box[4] = {128, moedc::kMmHalf, 1, 1};
-    if (!tensor_map(&l, kType, kSwizzle, x, 2, lsize, lstride, lbox) || !tensor_map(&r, kType, kSwizzle, w, 4, size, stride, box))
+    if (!tensor_map(&l, kType, kSwizzle, x, 2, lsize, lstride, lbox) ||
+        !tensor_map(&all, kType, kSwizzle, x, 2, lsize, lstride, allbox) || !tensor_map(&r, kType, kSwizzle, w, 4, size, stride, box))
         return MOEDC_ERR_CUDA;
     const int tile = a.gated ? moedc::kMmHalf : moedc::kMmTile;
     const int64_t units = ((int64_t)a.rows / moedc::kMmTile + (a.E < a.rows ? a.E : a.rows)) * ((a.N + (int64_t)tile - 1) / tile);
-    return launch_mm_pair<moedc::kMmE4m3>(a, units, l, r, stream);
+    return launch_mm_pair<moedc::kMmE4m3>(a, units, l, r, all, stream);
 }
 
 }  // namespace moedc_host

@@ -18,8 +18,9 @@
 // of tensor memory.
 //
 // Warps: 0-7 epilogue (0-3 the first half of the columns, or of the channels, 4-7 the
-// rest), 8 TMA, 9 MMA (of the pair's first block, for both), 10 tells the first block
-// that a stage has arrived, and clears what a stage of tokens holds of the next expert.
+// rest), 8 TMA, 9 MMA (of the pair's first block, for both), 10 (kMmDw) clears what a stage
+// of tokens holds of the next expert and tells the first block that it has arrived; in the
+// other forms the copies of both blocks count at the first one's barrier.
 // Tensor memory: two sums of 256 columns.
 #pragma once
 
@@ -36,6 +37,7 @@ constexpr int kMmBytes = 128;                   // of the contracted axis in a s
 constexpr int kMmOperand = kMmHalf * kMmBytes;  // a block's share of one operand
 constexpr int kMmStage = 2 * kMmOperand;
 constexpr int kMmStages = 6;
+constexpr int kMmBuf = 8 * 2048;                 // of the epilogue's warps, for their stores
 constexpr int kMmColumns = 512;
 
 struct MmUnit {
@@ -94,28 +96,58 @@ __device__ __forceinline__ uint32_t mm_pack16(float lo, float hi, bool f16)
     return (uint32_t)__half_as_ushort(__float2half_rn(lo)) | (uint32_t)__half_as_ushort(__float2half_rn(hi)) << 16;
 }
 
-// 32 values of a row from column n on, as far as N, rounded once to 16 bits.
-__device__ __forceinline__ void mm_store32(uint16_t* row, int n, int N, bool vec, bool f16, const float* v)
+// A warp's 32 rows, 64 bytes of each lane's own one: through shared memory, so that four
+// lanes store a row's 64 bytes and no sector is written in halves.  `rows` of them and
+// `bytes` (in 16s) of each exist; the first begins at `to`.
+__device__ __forceinline__ void mm_store_rows(uint8_t* buf, const uint4 (&q)[4], uint8_t* to, int64_t stride, int rows, int bytes)
 {
-    if (vec) {
+    const int lane = threadIdx.x % kWarp;
+    __syncwarp();
 #pragma unroll
-        for (int j = 0; j < 32; j += 8) {
-            if (n + j < N)
-                *reinterpret_cast<uint4*>(row + n + j) =
-                    make_uint4(mm_pack16(v[j], v[j + 1], f16), mm_pack16(v[j + 2], v[j + 3], f16),
-                               mm_pack16(v[j + 4], v[j + 5], f16), mm_pack16(v[j + 6], v[j + 7], f16));
-        }
-    } else {
+    for (int c = 0; c < 4; ++c) *reinterpret_cast<uint4*>(buf + lane * 64 + ((c ^ ((lane >> 1) & 3)) << 4)) = q[c];
+    __syncwarp();
+    const int c = lane & 3;
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-            if (n + j < N) row[n + j] = (uint16_t)mm_pack16(v[j], 0.0f, f16);
+    for (int k = 0; k < 4; ++k) {
+        const int r = k * 8 + (lane >> 2);
+        const uint4 v = *reinterpret_cast<const uint4*>(buf + r * 64 + ((c ^ ((r >> 1) & 3)) << 4));
+        if (r < rows && c * 16 < bytes) *reinterpret_cast<uint4*>(to + r * stride + c * 16) = v;
     }
 }
-__device__ __forceinline__ void mm_store32(float* row, int n, int N, const float* v)
+
+// 32 values of each lane's row from column n on, as far as N, rounded once to 16 bits.
+// out: the first row's column 0; vec: 16-byte stores fit.
+__device__ __forceinline__ void mm_store32(uint8_t* buf, uint16_t* out, int64_t ld, int n, int N, int rows, bool vec, bool f16,
+                                           const float* v)
+{
+    if (vec) {
+        uint4 q[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float* f = v + 8 * c;
+            q[c] = make_uint4(mm_pack16(f[0], f[1], f16), mm_pack16(f[2], f[3], f16), mm_pack16(f[4], f[5], f16),
+                              mm_pack16(f[6], f[7], f16));
+        }
+        mm_store_rows(buf, q, reinterpret_cast<uint8_t*>(out + n), 2 * ld, rows, 2 * (N - n));
+    } else if ((int)(threadIdx.x % kWarp) < rows) {
+        uint16_t* row = out + threadIdx.x % kWarp * ld + n;
+#pragma unroll
+        for (int j = 0; j < 32; ++j)
+            if (n + j < N) row[j] = (uint16_t)mm_pack16(v[j], 0.0f, f16);
+    }
+}
+__device__ __forceinline__ void mm_store32(uint8_t* buf, float* out, int64_t ld, int n, int N, int rows, const float* v)
 {
 #pragma unroll
-    for (int j = 0; j < 32; j += 4)
-        if (n + j < N) *reinterpret_cast<float4*>(row + n + j) = make_float4(v[j], v[j + 1], v[j + 2], v[j + 3]);
+    for (int h = 0; h < 32; h += 16) {
+        uint4 q[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const float* f = v + h + 4 * c;
+            q[c] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        }
+        mm_store_rows(buf, q, reinterpret_cast<uint8_t*>(out + n + h), 4 * ld, rows, 4 * (N - n - h));
+    }
 }
 
 __device__ __forceinline__ float mm_silu_mul(float g, float u)
@@ -128,7 +160,7 @@ __device__ __forceinline__ float mm_silu_mul(float g, float u)
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap lmap,
-                   const __grid_constant__ CUtensorMap rmap)
+                   const __grid_constant__ CUtensorMap rmap, const __grid_constant__ CUtensorMap allmap)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int64_t s_scan[kMmThreads / kWarp];
@@ -142,7 +174,7 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
     const int rank = cluster_rank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
     const int tiles = (a.N + (a.gated ? kMmHalf : kMmTile) - 1) / (a.gated ? kMmHalf : kMmTile);
-    int32_t* s_pre = reinterpret_cast<int32_t*>(smem + kMmStages * kMmStage);
+    int32_t* s_pre = reinterpret_cast<int32_t*>(smem + kMmStages * kMmStage + kMmBuf);
     int32_t *s_beg = s_pre + a.E + 1, *s_end = s_beg + a.E;
 
     if (threadIdx.x == 0) {
@@ -175,17 +207,20 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
     if (warp < 8) {
         // ---- epilogue
         if (a.wait_extra) mbar_wait(&never, 0, &s_abort);
-        const int half = warp >> 2, row = (warp & 3) * kWarp + lane;
+        const int half = warp >> 2;
         const uint32_t d0 = tmem + ((uint32_t)((warp & 3) * kWarp) << 16);
         // the columns of the thread's four parts of 32
         const int c01 = a.gated ? half * 64 : half * 128, c23 = a.gated ? 128 + half * 64 : half * 128 + 64;
+        uint8_t* buf = smem + kMmStages * kMmStage + warp * 2048;
         MvRing accs;
         bool bad = false;
         for (int unit = pair; unit < units; unit += pairs) {
             const MmUnit u = mm_unit<MODE>(a, s_pre, s_beg, s_end, tiles, unit);
-            const bool some = MODE == kMmDw || rank * kMmHalf + (warp & 3) * kWarp < u.m;   // of the warp's rows
-            const int r = u.r0 + rank * kMmHalf + row;     // MODE != kMmDw
-            const bool mine = MODE == kMmDw ? u.m0 + rank * kMmHalf + row < a.M : rank * kMmHalf + row < u.m;
+            // the warp's first row, and how many of its 32 there are
+            const int first = rank * kMmHalf + (warp & 3) * kWarp;
+            const int have = MODE == kMmDw ? a.M - u.m0 - first : u.m - first;
+            const bool some = have > 0, mine = lane < have;
+            const int r = u.r0 + first + lane;             // MODE != kMmDw
             if constexpr (MODE == kMmE4m3) {
                 float2 acc[64];
 #pragma unroll
@@ -249,11 +284,12 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                     for (int j = 0; j < 64; ++j) v[j] = mm_silu_mul(v[j], v[64 + j]);
                 }
                 if (!a.codes) {
-                    uint16_t* o = static_cast<uint16_t*>(a.out) + (int64_t)r * a.N;
-                    if (mine) {
+                    uint16_t* o = static_cast<uint16_t*>(a.out) + (int64_t)(u.r0 + first) * a.N;
+                    if (some) {
 #pragma unroll
                         for (int c = 0; c < 4; ++c)
-                            if (c < 2 || !a.gated) mm_store32(o, u.n0 + half * (a.gated ? 64 : 128) + c * 32, a.N, a.vec, a.f16, v + c * 32);
+                            if (c < 2 || !a.gated)
+                                mm_store32(buf, o, a.N, u.n0 + half * (a.gated ? 64 : 128) + c * 32, a.N, have, a.vec, a.f16, v + c * 32);
                     }
                 } else {
                     // the rule of dispatch, of the binary32 values: 128 channels are this thread's,
@@ -263,29 +299,34 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                     for (int j = 0; j < 128; ++j)
                         if (j < 64 || !a.gated) top = fmaxf(top, fabsf(v[j]));
                     if (a.gated) {
-                        s_amax[half][row] = top;
+                        s_amax[half][(warp & 3) * kWarp + lane] = top;
                         asm volatile("bar.sync 1, 256;" ::: "memory");
-                        top = fmaxf(top, s_amax[half ^ 1][row]);
+                        top = fmaxf(top, s_amax[half ^ 1][(warp & 3) * kWarp + lane]);
                         asm volatile("bar.sync 1, 256;" ::: "memory");
                     }
                     top = fmaxf(top, 1e-4f);
                     const float sc = __fdiv_rn(top, 448.0f);
                     const int n = u.n0 + half * (a.gated ? 64 : 128);
-                    if (mine && n < a.N) {
-                        uint8_t* o = static_cast<uint8_t*>(a.out) + (int64_t)r * a.N + n;
+                    if (some && n < a.N) {
+                        uint8_t* o = static_cast<uint8_t*>(a.out) + (int64_t)(u.r0 + first) * a.N + n;
 #pragma unroll
-                        for (int j = 0; j < 128; j += 16) {
-                            if (j >= 64 && a.gated) break;
-                            uint32_t q[4];
+                        for (int h = 0; h < 128; h += 64) {
+                            if (h >= 64 && a.gated) break;
+                            uint4 q[4];
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const float* f = v + j + 4 * k;
-                                q[k] = pack_e4m3x2(__fdiv_rn(f[0], sc), __fdiv_rn(f[1], sc)) |
-                                       pack_e4m3x2(__fdiv_rn(f[2], sc), __fdiv_rn(f[3], sc)) << 16;
+                                uint32_t w[4];
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    const float* f = v + h + 16 * k + 4 * i;
+                                    w[i] = pack_e4m3x2(__fdiv_rn(f[0], sc), __fdiv_rn(f[1], sc)) |
+                                           pack_e4m3x2(__fdiv_rn(f[2], sc), __fdiv_rn(f[3], sc)) << 16;
+                                }
+                                q[k] = make_uint4(w[0], w[1], w[2], w[3]);
                             }
-                            *reinterpret_cast<uint4*>(o + j) = make_uint4(q[0], q[1], q[2], q[3]);
+                            mm_store_rows(buf, q, o + h, a.N, have, 64);
                         }
-                        if (!a.gated || half == 0)
+                        if (mine && (!a.gated || half == 0))
                             static_cast<float*>(a.extra)[(int64_t)r * (a.N / 128) + n / 128] = sc;
                     }
                 }
@@ -296,7 +337,7 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                     tc_fence_after();
                 }
                 const uint32_t d = d0 + accs.slot * kMmTile;
-                const int64_t at = MODE == kMmDw ? (int64_t)u.e * a.M + u.m0 + rank * kMmHalf + row : r;
+                const int64_t at = MODE == kMmDw ? (int64_t)u.e * a.M + u.m0 + first : u.r0 + first;
                 uint16_t* o = static_cast<uint16_t*>(a.out) + at * a.N;
                 if (MODE == kMmForward && a.gated) {
                     if (some) {
@@ -313,15 +354,13 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                                 asm volatile("" : "+f"(v[j]));
                             }
                             const int n = u.n0 + half * 64 + c * 32;
-                            if (mine) {
-                                if (a.extra) {
-                                    mm_store32(keep, n, a.N, true, a.f16, g);
-                                    mm_store32(keep + a.N, n, a.N, true, a.f16, v);
-                                }
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) v[j] = mm_silu_mul(g[j], v[j]);
-                                mm_store32(o, n, a.N, true, a.f16, v);
+                            if (a.extra) {
+                                mm_store32(buf, keep, 2 * (int64_t)a.N, n, a.N, have, true, a.f16, g);
+                                mm_store32(buf, keep + a.N, 2 * (int64_t)a.N, n, a.N, have, true, a.f16, v);
                             }
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = mm_silu_mul(g[j], v[j]);
+                            mm_store32(buf, o, a.N, n, a.N, have, true, a.f16, v);
                         }
                     }
                 } else if (some) {
@@ -338,10 +377,8 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                             for (int j = 0; j < 32; ++j) v[j] = 0.0f;   // an expert without rows
                         }
                         const int n = u.n0 + half * 128 + c * 32;
-                        if (mine) {
-                            if (MODE == kMmDw && a.f32) mm_store32(static_cast<float*>(a.out) + at * a.N, n, a.N, v);
-                            else mm_store32(o, n, a.N, true, a.f16, v);
-                        }
+                        if (MODE == kMmDw && a.f32) mm_store32(buf, static_cast<float*>(a.out) + at * a.N, a.N, n, a.N, have, v);
+                        else mm_store32(buf, o, a.N, n, a.N, have, true, a.f16, v);
                     }
                 }
                 if (any) {
@@ -369,9 +406,10 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                 for (int i = 0; i < 4; ++i)
                     if (lane * 4 + i < m) t[i] = max(mm_x_row(a, r0 + lane * 4 + i), 0);
             }
-            const int bytes = kMmOperand + (MODE == kMmDw ? kMmOperand
-                                            : gather      ? (m + 3) / 4 * 4 * kMmBytes
-                                                          : (m + 31) / 32 * 32 * kMmBytes);
+            auto left_bytes = [&](int rows) { return (gather ? (rows + 3) / 4 * 4 : (rows + 31) / 32 * 32) * kMmBytes; };
+            // kMmDw: what this block brings, counted here; else that of both, at the first block
+            const int bytes = MODE == kMmDw ? kMmStage
+                                            : 2 * kMmOperand + left_bytes(min(u.m, kMmHalf)) + left_bytes(max(u.m - kMmHalf, 0));
             for (int s = 0; s < u.ksteps; ++s) {
                 const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
                 if (__any_sync(0xffffffffu, !ok)) {
@@ -381,26 +419,34 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                 uint8_t* left = smem + ring.slot * kMmStage;
                 uint8_t* right = left + kMmOperand;
                 uint64_t* bar = full + ring.slot;
-                if (lane == 0) mbar_arrive_expect(bar, bytes);
-                __syncwarp();
-                if (gather && lane * 4 < m) tma_gather4(left + lane * 4 * kMmBytes, &lmap, s * kElems, t[0], t[1], t[2], t[3], bar);
-                if (lane == 0) {
-                    if constexpr (MODE == kMmDw) {
+                if constexpr (MODE == kMmDw) {
+                    if (lane == 0) {
+                        mbar_arrive_expect(bar, bytes);
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             tma_2d(left + h * (kMmOperand / 2), &lmap, u.m0 + rank * kMmHalf + h * 64, u.r0 + s * kElems, bar);
                             tma_2d(right + h * (kMmOperand / 2), &rmap, u.n0 + rank * kMmHalf + h * 64, u.r0 + s * kElems, bar);
                         }
-                    } else {
-                        if (!gather)
-                            for (int i = 0; i < m; i += 32) tma_2d(left + i * kMmBytes, &lmap, s * kElems, r0 + i, bar);
+                    }
+                } else {
+                    const uint32_t at = cluster_addr(bar, 0);
+                    if (lane == 0 && rank == 0) mbar_arrive_expect(bar, bytes);
+                    __syncwarp();
+                    if (gather && lane * 4 < m)
+                        tma_gather4_pair(left + lane * 4 * kMmBytes, &lmap, s * kElems, t[0], t[1], t[2], t[3], at);
+                    if (lane == 0) {
+                        if (!gather) {
+                            if (m == kMmHalf) tma_2d_pair(left, &allmap, s * kElems, r0, at);
+                            else
+                                for (int i = 0; i < m; i += 32) tma_2d_pair(left + i * kMmBytes, &lmap, s * kElems, r0 + i, at);
+                        }
                         if constexpr (MODE == kMmDx) {
 #pragma unroll
                             for (int h = 0; h < 2; ++h)
-                                tma_3d(right + h * (kMmOperand / 2), &rmap, u.n0 + rank * kMmHalf + h * 64, s * kElems, u.e, bar);
+                                tma_3d_pair(right + h * (kMmOperand / 2), &rmap, u.n0 + rank * kMmHalf + h * 64, s * kElems, u.e, at);
                         } else {
                             // [E][1 or 2][N][K]
-                            tma_4d(right, &rmap, s * kElems, u.n0 + (a.gated ? 0 : rank * kMmHalf), a.gated ? rank : 0, u.e, bar);
+                            tma_4d_pair(right, &rmap, s * kElems, u.n0 + (a.gated ? 0 : rank * kMmHalf), a.gated ? rank : 0, u.e, at);
                         }
                     }
                 }
@@ -410,10 +456,13 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
             }
         }
         // no copy may land after the block has gone, whatever else gave up
-        for (int n = max(0, issued - kMmStages); n < issued; ++n) {
+        for (int n = max(0, issued - kMmStages); n < issued && (MODE == kMmDw || rank == 0); ++n) {
             volatile int alone = 0;
             if (!mbar_wait(full + n % kMmStages, (n / kMmStages) & 1, &alone)) s_abort = 1;
         }
+        // a second block that gave up sees no barrier of its copies: they have a millisecond
+        if (s_abort)
+            for (const unsigned long long t0 = globaltimer(); globaltimer() - t0 < 1000000ull;) {}
         __syncwarp();
     } else if (warp == 9) {
         // ---- MMA, for both blocks: one elected lane issues; the warp stays together
@@ -430,7 +479,7 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                     if ((MODE == kMmE4m3 || s == 0) && k++ >= 2) {
                         mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
                     }
-                    mbar_wait_warp(ready + ring.slot, ring.phase, &s_abort);
+                    mbar_wait_warp((MODE == kMmDw ? ready : full) + ring.slot, ring.phase, &s_abort);
                     tc_fence_after();
                     const uint32_t left = smem_u32(smem + ring.slot * kMmStage);
                     const uint64_t l = MODE == kMmDw ? tc_smem_desc_mn(left, kMmOperand / 2) : tc_smem_desc(left);
@@ -462,8 +511,8 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
         volatile int alone = 0;
         if (!mbar_wait(&done, 0, &alone)) s_abort = 1;
         __syncwarp();
-    } else if (warp == 10) {
-        // ---- stages that have arrived
+    } else if (MODE == kMmDw && warp == 10) {
+        // ---- stages that have arrived in this block
         MvRing ring;
         for (int unit = pair; unit < units; unit += pairs) {
             const MmUnit u = mm_unit<MODE>(a, s_pre, s_beg, s_end, tiles, unit);
@@ -507,16 +556,16 @@ namespace moedc_host {
 
 template <int MODE>
 int launch_mm_pair(const moedc::MmArgs& a, int64_t units, const CUtensorMap& lmap, const CUtensorMap& rmap,
-                   cudaStream_t stream)
+                   const CUtensorMap& allmap, cudaStream_t stream)
 {
     auto* k = moedc::matmul_pair_kernel<MODE>;
-    const size_t smem = (size_t)moedc::kMmStages * moedc::kMmStage + (3 * (size_t)a.E + 1) * sizeof(int32_t);
+    const size_t smem = (size_t)moedc::kMmStages * moedc::kMmStage + moedc::kMmBuf + (3 * (size_t)a.E + 1) * sizeof(int32_t);
     static PerDevice raised;
-    if (!raise_smem_limit(raised, (const void*)k, moedc::kMmStages * moedc::kMmStage + (3 * MOEDC_MAX_E + 1) * 4))
+    if (!raise_smem_limit(raised, (const void*)k, moedc::kMmStages * moedc::kMmStage + moedc::kMmBuf + (3 * MOEDC_MAX_E + 1) * 4))
         return MOEDC_ERR_CUDA;
     const int pairs = sm_count() / 2;
     clear_stale_error();
-    launch(k, 2 * (int)(units < pairs ? units : pairs), moedc::kMmThreads, smem, stream, a, lmap, rmap);
+    launch(k, 2 * (int)(units < pairs ? units : pairs), moedc::kMmThreads, smem, stream, a, lmap, rmap, allmap);
     return launch_status();
 }
 

@@ -30,24 +30,26 @@ int64_t most_units(const moedc::MmArgs& a)
 
 int launch_mm_forward(const moedc::MmArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t stream)
 {
-    CUtensorMap l, r;
+    CUtensorMap l, r, all;   // left in boxes of 32 rows and of 128
     const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
     const cuuint64_t size[4] = {K, N, parts, (cuuint64_t)a.E}, stride[3] = {2 * K, 2 * K * N, 2 * K * N * parts};
     const cuuint32_t box[4] = {64, moedc::kMmHalf, 1, 1};
-    if (!map_rows(&l, x, a.K, a.rows, ldx, 32) || !tensor_map(&r, k16, kSwizzle, w, 4, size, stride, box))
+    if (!map_rows(&l, x, a.K, a.rows, ldx, 32) || !map_rows(&all, x, a.K, a.rows, ldx, moedc::kMmHalf) ||
+         !tensor_map(&r, k16, kSwizzle, w, 4, size, stride, box))
         return MOEDC_ERR_CUDA;
-    return launch_mm_pair<moedc::kMmForward>(a, most_units(a), l, r, stream);
+    return launch_mm_pair<moedc::kMmForward>(a, most_units(a), l, r, all, stream);
 }
 
 int launch_mm_dx(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* w, cudaStream_t stream)
 {
-    CUtensorMap l, r;
+    CUtensorMap l, r, all;   // left in boxes of 32 rows and of 128
     const cuuint64_t size[3] = {(cuuint64_t)a.N, (cuuint64_t)a.K, (cuuint64_t)a.E};
     const cuuint64_t stride[2] = {2 * (cuuint64_t)a.N, 2 * (cuuint64_t)a.N * a.K};
     const cuuint32_t box[3] = {64, 64, 1};
-    if (!map_rows(&l, dout, a.K, a.rows, ldd, 32) || !tensor_map(&r, k16, kSwizzle, w, 3, size, stride, box))
+    if (!map_rows(&l, dout, a.K, a.rows, ldd, 32) || !map_rows(&all, dout, a.K, a.rows, ldd, moedc::kMmHalf) ||
+         !tensor_map(&r, k16, kSwizzle, w, 3, size, stride, box))
         return MOEDC_ERR_CUDA;
-    return launch_mm_pair<moedc::kMmDx>(a, most_units(a), l, r, stream);
+    return launch_mm_pair<moedc::kMmDx>(a, most_units(a), l, r, all, stream);
 }
 
 int launch_mm_dw(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* x, int64_t ldx, cudaStream_t stream)
@@ -55,7 +57,7 @@ int launch_mm_dw(const moedc::MmArgs& a, const void* dout, int64_t ldd, const vo
     CUtensorMap l, r;
     if (!map_rows(&l, dout, a.M, a.rows, ldd, 64) || !map_rows(&r, x, a.N, a.rows, ldx, 64)) return MOEDC_ERR_CUDA;
     const int64_t units = a.E * col_tiles(a) * ((a.M + (int64_t)moedc::kMmTile - 1) / moedc::kMmTile);
-    return launch_mm_pair<moedc::kMmDw>(a, units, l, r, stream);
+    return launch_mm_pair<moedc::kMmDw>(a, units, l, r, l, stream);
 }
 
 }  // namespace moedc_host
