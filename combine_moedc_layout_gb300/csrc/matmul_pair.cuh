@@ -157,6 +157,13 @@ __device__ __forceinline__ float mm_silu_mul(float g, float u)
     return g * s * u;
 }
 
+__device__ __forceinline__ float ld_scale(const float* p)
+{
+    float v;
+    asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+    return v;
+}
+
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap lmap,
@@ -204,9 +211,16 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
     const int units = MODE == kMmDw ? a.E * tiles * ((a.M + kMmTile - 1) / kMmTile) : s_pre[a.E] * tiles;
     if (over && blockIdx.x == 0) raise_status(a.status, MOEDC_ERR_CAPACITY);
 
+    // kMmE4m3: the epilogue's threads keep 128 sums each.  The shares add up to the launch's
+    // 384 x 168 registers: 256 x 224 + 128 x 56.
+    if constexpr (MODE == kMmE4m3) {
+        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    }
     if (warp < 8) {
         // ---- epilogue
-        if (a.wait_extra) mbar_wait(&never, 0, &s_abort);
+        // (no calls in kMmE4m3's epilogue: with one the registers do not compile to a share)
+        if (a.wait_extra) mbar_wait_inline(&never, 0, &s_abort);
         const int half = warp >> 2;
         const uint32_t d0 = tmem + ((uint32_t)((warp & 3) * kWarp) << 16);
         // the columns of the thread's four parts of 32
@@ -235,42 +249,50 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                 const int b0 = a.gated ? u.n0 / 128 : min(u.n0 / 128 + half, blocks - 1);
                 const float* w0 = a.ws + ((int64_t)u.e * (a.gated ? 2 : 1) * blocks + b0) * groups;
                 const float* w1 = a.gated ? w0 + (int64_t)blocks * groups : w0;
-                // scales of four groups, and of the next four
-                float sx[4], s0[4], s1[4], nx[4], n0[4], n1[4];
+                // scales of four groups, each replaced as soon as it is used: volatile loads, as the
+                // compiler would move them to their use
+                float sx[4], s0[4], s1[4];
+                auto load = [&](int i, int g) __attribute__((always_inline)) {
+                    g = min(g, groups - 1);
+                    sx[i] = ld_scale(xs + g * a.xs_g), s0[i] = ld_scale(w0 + g), s1[i] = ld_scale(w1 + g);
+                };
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int g = min(i, groups - 1);
-                    nx[i] = __ldg(xs + g * a.xs_g), n0[i] = __ldg(w0 + g), n1[i] = __ldg(w1 + g);
-                }
+                for (int i = 0; i < 4; ++i) load(i, i);
                 for (int g0 = 0; g0 < groups; g0 += 4) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        sx[i] = nx[i], s0[i] = n0[i], s1[i] = n1[i];
-                        const int g = min(g0 + 4 + i, groups - 1);
-                        nx[i] = __ldg(xs + g * a.xs_g), n0[i] = __ldg(w0 + g), n1[i] = __ldg(w1 + g);
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
                         if (g0 + i >= groups) break;
-                        mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
+                        const float f0 = sx[i] * s0[i], f1 = sx[i] * s1[i];
+                        load(i, g0 + i + 4);
+                        mbar_wait_inline(d_full + accs.slot, accs.phase, &s_abort);
+                        __syncwarp();
                         tc_fence_after();
+                        const uint32_t d = d0 + accs.slot * kMmTile;
+                        auto release = [&]() __attribute__((always_inline)) {
+                            tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, 0);
+                        };
                         if (some) {
+                            // the next 16 columns are read while 16 are added up; the buffer is free
+                            // once the last ones are in registers
+                            float v[2][16];
+                            tc_ld16(d + c01, v[0]);
 #pragma unroll
-                            for (int c = 0; c < 4; ++c) {
-                                const float s = sx[i] * (c < 2 ? s0[i] : s1[i]);
-                                float v[32];
-                                tc_ld32(d0 + accs.slot * kMmTile + (c < 2 ? c01 + c * 32 : c23 + (c - 2) * 32), v);
+                            for (int c = 0; c < 8; ++c) {
                                 tc_wait_ld();
 #pragma unroll
-                                for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(v[j]));
+                                for (int j = 0; j < 16; ++j) asm volatile("" : "+f"(v[c & 1][j]));
+                                if (c < 7) tc_ld16(d + (c < 3 ? c01 + (c + 1) * 16 : c23 + (c - 3) * 16), v[(c + 1) & 1]);
+                                else release();
+                                const float2 s = splat2(c < 4 ? f0 : f1);
 #pragma unroll
-                                for (int j = 0; j < 16; ++j)
-                                    acc[c * 16 + j] = fma2_rn(make_float2(v[2 * j], v[2 * j + 1]), splat2(s), acc[c * 16 + j]);
+                                for (int j = 0; j < 8; ++j)
+                                    acc[c * 8 + j] = fma2_rn(make_float2(v[c & 1][2 * j], v[c & 1][2 * j + 1]), s, acc[c * 8 + j]);
                             }
+                        } else {
+                            release();
                         }
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, 0);
                         accs.next(2);
                     }
                 }

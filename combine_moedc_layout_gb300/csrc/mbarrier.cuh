@@ -64,6 +64,23 @@ __device__ __forceinline__ bool mbar_wait(uint64_t* b, int parity, volatile int*
     return mbar_try(b, parity) || mbar_wait_slow(b, parity, abort);
 }
 
+// The same without a call, for threads whose registers are full: what a call does not keep
+// would be spilled around it.
+__device__ __forceinline__ bool mbar_wait_inline(uint64_t* b, int parity, volatile int* abort)
+{
+    unsigned long long t0 = 0;
+    for (int i = 1; !mbar_try(b, parity); ++i) {
+        if (i % 1024 != 0) continue;
+        const unsigned long long now = globaltimer();
+        if (t0 == 0) t0 = now;
+        if (*abort || now - t0 > kMvWaitNs) {
+            *abort = 1;
+            return false;
+        }
+    }
+    return true;
+}
+
 // Where a stage's slot and phase go round the ring.
 struct MvRing {
     int slot = 0, phase = 0;
