@@ -23,7 +23,7 @@ from .moedc import (F16, F32, GATE_BIAS_SCORE, GATE_NORMALIZE, GATE_SIGMOID, GAT
                     moedc_matvec_int4_workspace_bytes, moedc_sort, moedc_sort_rows, moedc_sort_workspace_bytes, moedc_unsort,
                     moedc_unsort_grad, sort, sort_grad, unsort, unsort_grad)
 from .moedc import (matmul, matmul_e4m3, matmul_grad, moedc_matmul, moedc_matmul_e4m3, moedc_matmul_grad,
-                    moedc_quant_e4m3, moedc_swiglu_grad, quant_e4m3, swiglu_grad)
+                    moedc_matmul_e4m3_workspace_bytes, moedc_quant_e4m3, moedc_swiglu_grad, quant_e4m3, swiglu_grad)
 
 __all__ = ["BF16", "FP8_E4M3", "SCALES_COL_MAJOR", "SCALES_PER_TOKEN", "Layout", "MoedcError", "alloc_recv",
            "combine", "combine_e4m3", "dequant_e4m3", "moedc_combine_e4m3",
@@ -39,4 +39,5 @@ __all__ = ["BF16", "FP8_E4M3", "SCALES_COL_MAJOR", "SCALES_PER_TOKEN", "Layout",
            "moedc_sort_workspace_bytes", "moedc_unsort", "moedc_unsort_grad", "sort", "sort_grad",
            "unsort", "unsort_grad",
            "matmul", "matmul_e4m3", "matmul_grad", "moedc_matmul", "moedc_matmul_e4m3", "moedc_matmul_grad",
+           "moedc_matmul_e4m3_workspace_bytes",
            "moedc_quant_e4m3", "moedc_swiglu_grad", "quant_e4m3", "swiglu_grad"]

@@ -2,7 +2,70 @@
 #include "matmul_pair.cuh"
 #include "tensor_map.cuh"
 
+namespace moedc {
+
+// Rows of x and their scales in packed order, a warp a row; a row of nobody's is left alone,
+// one that src leads outside is zeros (and stays zero under whatever scale its own is: 0).
+constexpr int kMmCopyRows = 8;
+__global__ void __launch_bounds__(kMmCopyRows* kWarp) matmul_gather_kernel(const __grid_constant__ MmArgs a,
+                                                                          const uint8_t* __restrict__ x, int groups,
+                                                                          uint8_t* __restrict__ to, float* __restrict__ to_xs)
+{
+    extern __shared__ int32_t s_maps[];
+    __shared__ int64_t s_scan[kMmCopyRows];
+    int32_t *s_pre = s_maps, *s_beg = s_pre + a.E + 1, *s_end = s_beg + a.E;
+    pdl_enter();
+    const bool over = mm_chunks<kMmCopyRows * kWarp>(a, kMmCopyRows, 1, s_scan, s_pre, s_beg, s_end);
+    if (over && blockIdx.x == 0) raise_status(a.status, MOEDC_ERR_CAPACITY);
+    const int lane = threadIdx.x % kWarp;
+    bool bad = false;
+    for (int unit = blockIdx.x; unit < s_pre[a.E]; unit += gridDim.x) {
+        int lo = 0, hi = a.E - 1;   // last expert whose units begin at or before `unit`
+        while (lo < hi) {
+            const int mid = (lo + hi + 1) / 2;
+            if (s_pre[mid] <= unit) lo = mid; else hi = mid - 1;
+        }
+        const int r = s_beg[lo] + (unit - s_pre[lo]) * kMmCopyRows + threadIdx.x / kWarp;
+        if (r >= s_end[lo]) continue;
+        const int t = mm_x_row(a, r);
+        bad |= t < 0;
+        const uint4* from = reinterpret_cast<const uint4*>(x + (int64_t)max(t, 0) * a.K);
+        uint4* out = reinterpret_cast<uint4*>(to + (int64_t)r * a.K);
+        for (int i = lane; i < a.K / 16; i += kWarp) out[i] = t < 0 ? make_uint4(0, 0, 0, 0) : __ldg(from + i);
+        for (int g = lane; g < groups; g += kWarp)
+            to_xs[(int64_t)r * groups + g] = t < 0 ? 0.0f : __ldg(a.xs + t * a.xs_r + g * a.xs_g);
+    }
+    if (bad) raise_status(a.status, MOEDC_ERR_EXPERT_RANGE);
+}
+
+}  // namespace moedc
+
 namespace moedc_host {
+
+// Gathering the rows of a block's stage by TMA takes some 80 clocks for four of them, again
+// for every tile of columns: beyond some 25 rows it is longer than the products.  Then they
+// are brought into packed order first.
+bool matmul_gathers_first(int E, int rows)
+{
+    const int64_t active = E < rows ? E : rows;
+    return rows >= 32 * active;
+}
+
+int launch_mm_gather(moedc::MmArgs& a, const void* x, uint8_t* workspace, cudaStream_t stream)
+{
+    const int groups = a.xs_g == 0 ? 1 : a.K / 128;
+    float* xs = reinterpret_cast<float*>(workspace + (size_t)a.rows * a.K);
+    const int64_t units = (int64_t)a.rows / moedc::kMmCopyRows + a.E, most = 8 * (int64_t)sm_count();
+    clear_stale_error();
+    launch(moedc::matmul_gather_kernel, (int)(units < most ? units : most), moedc::kMmCopyRows * moedc::kWarp,
+           (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a, static_cast<const uint8_t*>(x), groups, workspace, xs);
+    a.xs = xs;
+    a.xs_r = groups;
+    a.src = nullptr;
+    a.x_rows = a.rows;
+    a.xs_e = (int64_t)a.slots * groups;
+    return launch_status();
+}
 
 int launch_mm_e4m3(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream)
 {
@@ -24,10 +87,16 @@ int launch_mm_e4m3(const moedc::MmArgs& a, const void* x, const void* w, cudaStr
 
 }  // namespace moedc_host
 
+extern "C" size_t moedc_matmul_e4m3_workspace_bytes(int Kd, int E, int rows)
+{
+    if (Kd < 128 || Kd % 128 != 0 || E < 1 || E > MOEDC_MAX_E || rows < 1) return 0;
+    return moedc_host::matmul_gathers_first(E, rows) ? (size_t)rows * Kd + (size_t)rows * (Kd / 128) * sizeof(float) : 0;
+}
+
 extern "C" int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float* xs, int scale_layout, const void* w,
                                  const float* ws, int E, int N, int flags, const int32_t* offsets,
                                  const int32_t* counts, const int32_t* src, int top_k, int rows, int out_dtype, void* out,
-                                 float* out_scales, int32_t* dev_status, cudaStream_t stream)
+                                 float* out_scales, void* workspace, size_t workspace_bytes, int32_t* dev_status, cudaStream_t stream)
 {
     using namespace moedc_host;
     const bool gated = (flags & MOEDC_SWIGLU) != 0, codes = out_dtype == MOEDC_FP8_E4M3;
@@ -41,7 +110,7 @@ extern "C" int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float*
         return MOEDC_ERR_ARG;
     if (!w || !ws || !dev_status || !aligned(x, 16) || !aligned(w, 16) || !aligned(xs, 4) || !aligned(ws, 4) ||
         !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(src, 4) || !aligned(out, codes ? 16 : 2) ||
-        !aligned(out_scales, 4) || !aligned(dev_status, 4))
+        !aligned(out_scales, 4) || !aligned(workspace, 16) || !aligned(dev_status, 4))
         return MOEDC_ERR_ARG;
     if (((int64_t)rows / 256 + E) * (N / 128 + 1) > INT32_MAX) return MOEDC_ERR_ARG;   // units are counted in 32 bits
     if (rows == 0 || x_rows == 0) return MOEDC_OK;
@@ -71,5 +140,11 @@ extern "C" int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float*
     a.codes = codes;
     a.vec = N % 8 == 0 && aligned(out, 16);
     a.wait_extra = test_wait_extra();
+    const size_t copy = src && workspace ? moedc_matmul_e4m3_workspace_bytes(Kd, E, rows) : 0;
+    if (copy && workspace_bytes >= copy) {
+        const int st = launch_mm_gather(a, x, static_cast<uint8_t*>(workspace), stream);
+        if (st != MOEDC_OK) return st;
+        x = workspace;
+    }
     return launch_mm_e4m3(a, x, w, stream);
 }

@@ -50,6 +50,7 @@ EXPORTED = ("moedc_api_version", "moedc_strerror", "moedc_layout_workspace_bytes
             "moedc_gate", "moedc_gate_grad", "moedc_sort_rows", "moedc_sort_workspace_bytes",
             "moedc_sort", "moedc_unsort", "moedc_unsort_grad", "moedc_matvec_int4",
            "moedc_matvec_int4_workspace_bytes", "moedc_quant_e4m3", "moedc_matmul_e4m3",
+            "moedc_matmul_e4m3_workspace_bytes",
             "moedc_matmul", "moedc_swiglu_grad", "moedc_matmul_grad",
             "moedc_layout_dispatch_workspace_bytes", "moedc_test_set_wait_extra")
 
@@ -130,8 +131,11 @@ def load(path: str | None = None) -> ctypes.CDLL:
     lib.moedc_matvec_int4_workspace_bytes.restype = Z
     lib.moedc_quant_e4m3.argtypes = [P, L, I, I, I, I, I, P, P, P]
     lib.moedc_quant_e4m3.restype = I
-    lib.moedc_matmul_e4m3.argtypes = [P, I, I, P, I, P, P, I, I, I, P, P, P, I, I, I, P, P, P, P]
+    lib.moedc_matmul_e4m3.argtypes = [P, I, I, P, I, P, P, I, I, I, P, P, P, I, I, I, P, P, P, Z,
+                                      P, P]
     lib.moedc_matmul_e4m3.restype = I
+    lib.moedc_matmul_e4m3_workspace_bytes.argtypes = [I, I, I]
+    lib.moedc_matmul_e4m3_workspace_bytes.restype = Z
     lib.moedc_matmul.argtypes = [P, L, I, I, P, I, I, I, P, P, I, P, P, P, P]
     lib.moedc_matmul.restype = I
     lib.moedc_swiglu_grad.argtypes = [P, L, P, I, I, I, P, P]
@@ -317,11 +321,16 @@ def moedc_quant_e4m3(x, ldx, dtype, E, rows, Kd, block_rows, codes, scales, stre
 
 
 def moedc_matmul_e4m3(x, x_rows, Kd, xs, scale_layout, w, ws, E, N, flags, offsets, counts, src,
-                      top_k, rows, out_dtype, out, out_scales, dev_status, stream=None) -> int:
+                      top_k, rows, out_dtype, out, out_scales, workspace, workspace_bytes,
+                      dev_status, stream=None) -> int:
     return load().moedc_matmul_e4m3(_p(x), x_rows, Kd, _p(xs), scale_layout, _p(w), _p(ws), E, N,
                                     flags, _p(offsets), _p(counts), _p(src), top_k, rows,
-                                    out_dtype, _p(out), _p(out_scales), _p(dev_status),
-                                    _stream(stream))
+                                    out_dtype, _p(out), _p(out_scales), _p(workspace),
+                                    workspace_bytes, _p(dev_status), _stream(stream))
+
+
+def moedc_matmul_e4m3_workspace_bytes(Kd: int, E: int, rows: int) -> int:
+    return int(load().moedc_matmul_e4m3_workspace_bytes(Kd, E, rows))
 
 
 def moedc_matmul(x, ldx, dtype, Kd, w, E, N, flags, offsets, counts, rows, out, products,
@@ -863,6 +872,11 @@ def quant_e4m3(x: torch.Tensor, block_rows: int = 1, out=None):
     return out
 
 
+@functools.lru_cache(maxsize=1024)
+def _matmul_e4m3_bytes(Kd: int, E: int, rows: int) -> int:
+    return load().moedc_matmul_e4m3_workspace_bytes(Kd, E, rows)
+
+
 _E4M3_OUT = {BF16: torch.bfloat16, F16: torch.float16, FP8_E4M3: torch.float8_e4m3fn}
 
 
@@ -870,7 +884,8 @@ def matmul_e4m3(x: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Te
                 offsets: torch.Tensor | None = None, counts: torch.Tensor | None = None,
                 src: torch.Tensor | None = None, top_k: int = 1, swiglu: bool = False,
                 out_dtype: int = BF16, scale_layout: int = 0,
-                status: torch.Tensor | None = None, out=None):
+                status: torch.Tensor | None = None, out=None,
+                workspace: torch.Tensor | None = None):
     """out [R, N]: packed expert rows x e4m3 [R, Kd] with scales xs [R, Kd/128],
     times e4m3 weights w [E, N, Kd] ([N, Kd]: one linear layer) with scales ws
     [E, ceil(N/128), Kd/128]; swiglu: 2N weight rows and 2 ceil(N/128) blocks,
@@ -878,7 +893,9 @@ def matmul_e4m3(x: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Te
     is dispatch()'s receive buffer (xs in its scale_layout) and out [E, cap, N].
     src (and top_k): out row r is of x row src[r] // top_k.  out_dtype BF16, F16,
     or FP8_E4M3: (codes, scales [R, N/128]), rows for the next product.  status
-    (int32 [1]) takes data errors; without one the call waits and raises them."""
+    (int32 [1]) takes data errors; without one the call waits and raises them.
+    workspace: moedc_matmul_e4m3_workspace_bytes bytes, for rows gathered through
+    src, allocated here when None and of use."""
     if w.dim() == 2:
         w, ws = w[None], ws[None]
     e4m3 = torch.float8_e4m3fn
@@ -934,10 +951,17 @@ def matmul_e4m3(x: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Te
         _need(ys, torch.float32, "out[1]")
         _need_shape(ys, (*lead, N // 128), "out[1]")
     status, wait = _status(status, x.device)
+    if workspace is not None:
+        _need(workspace, torch.uint8, "workspace")
+    elif src is not None:
+        n = _matmul_e4m3_bytes(Kd, E, rows)
+        if n:
+            workspace = torch.empty(n, dtype=torch.uint8, device=x.device)
     _check((_lib or load()).moedc_matmul_e4m3(
         x.data_ptr(), x_rows, Kd, xs.data_ptr(), scale_layout, w.data_ptr(), ws.data_ptr(), E, N,
         SWIGLU if swiglu else 0, _p(offsets), _p(counts), _p(src), top_k, rows, out_dtype,
-        y.data_ptr(), _p(ys), status.data_ptr(), _stream(None)), "moedc_matmul_e4m3")
+        y.data_ptr(), _p(ys), _p(workspace), 0 if workspace is None else workspace.numel(),
+        status.data_ptr(), _stream(None)), "moedc_matmul_e4m3")
     if wait:
         _check(int(status), "moedc_matmul_e4m3")
     return out

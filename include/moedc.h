@@ -538,16 +538,23 @@ MOEDC_EXPORT int moedc_quant_e4m3(const void* x, int64_t ldx, int dtype, int E, 
  *         MOEDC_FP8_E4M3: codes and out_scales [rows, N / 128] of v by
  *         dispatch's rule, N % 128 == 0: rows for the next product
  * NaN codes stay in their own row's outputs (of x) or their own column's (of w).
+ * workspace (16-byte aligned, no initialisation): with src and many rows to an
+ * expert, where moedc_matmul_e4m3_workspace_bytes is not 0, the rows are first
+ * copied into packed order there; without one (NULL, or smaller) they are gathered
+ * as the products need them.  The results are the same.  Calls that can run at the
+ * same time need their own.
  * Kd % 128 == 0; x, w and e4m3 out 16-byte aligned, out otherwise 2-byte.
  * Data errors (dev_status): MOEDC_ERR_EXPERT_RANGE when src leads outside
  * [0, x_rows) (the row counts as zeros), MOEDC_ERR_CAPACITY when an expert's rows
  * pass `rows` or its slots (those are skipped), MOEDC_ERR_TIMEOUT if a bounded wait
  * gave up (its outputs are then unspecified).
  */
+MOEDC_EXPORT size_t moedc_matmul_e4m3_workspace_bytes(int Kd, int E, int rows);
 MOEDC_EXPORT int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float* xs, int scale_layout,
                  const void* w, const float* ws, int E, int N, int flags, const int32_t* offsets,
                  const int32_t* counts, const int32_t* src, int top_k, int rows, int out_dtype,
-                 void* out, float* out_scales, int32_t* dev_status, cudaStream_t stream);
+                 void* out, float* out_scales, void* workspace, size_t workspace_bytes,
+                 int32_t* dev_status, cudaStream_t stream);
 
 /*
  * The experts' layers in training: products of packed rows with 16-bit weights,

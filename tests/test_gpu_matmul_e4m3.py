@@ -107,6 +107,11 @@ def test_gathered_rows(T, E, K):
     flat = moedc.matmul_e4m3(x.view(torch.uint8)[token].view(E4M3), xs[token], w, ws, offsets=m.offsets,
                              counts=m.counts, swiglu=True, status=m.status)
     mine = m.src >= 0
+    # gathered as the products need them, where the call would copy the rows first
+    small = torch.empty(16, dtype=torch.uint8, device="cuda")
+    z = moedc.matmul_e4m3(x, xs, w, ws, offsets=m.offsets, counts=m.counts, src=m.src, top_k=K,
+                          swiglu=True, status=m.status, workspace=small)
+    assert torch.equal(y[mine], z[mine])
     assert torch.equal(y[mine], flat[mine]) and int(m.status) == 0
     for e in range(E):
         a, c = int(m.offsets[e]), int(m.counts[e])
@@ -187,6 +192,19 @@ def test_rows_out_of_range_count_as_zeros():
     with pytest.raises(moedc.MoedcError) as err:
         moedc.matmul_e4m3(x, xs, w, ws, offsets=offsets, counts=cnt, src=src, top_k=2)
     assert err.value.code == moedc.ERR_EXPERT_RANGE
+    # where the rows are copied first
+    src = torch.arange(80, dtype=torch.int32).cuda() % 8
+    src[[7, 50]] = torch.tensor([8, -1], dtype=torch.int32).cuda()
+    offsets, cnt, _ = groups([40, 40])
+    assert moedc.moedc_matmul_e4m3_workspace_bytes(256, 2, 80) > 0
+    xs[0, 0] = float("inf")
+    status.zero_()
+    y = moedc.matmul_e4m3(x, xs, w, ws, offsets=offsets, counts=cnt, src=src, top_k=2, status=status)
+    z = moedc.matmul_e4m3(x, xs, w, ws, offsets=offsets, counts=cnt, src=src, top_k=2, status=status,
+                          workspace=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    assert int(status) == moedc.ERR_EXPERT_RANGE
+    assert (y[[7, 50]] == 0).all() and (z[[7, 50]] == 0).all()
+    assert torch.equal(torch.nan_to_num(y.float()), torch.nan_to_num(z.float()))
 
 
 def test_nan_stays_in_its_row_and_column():

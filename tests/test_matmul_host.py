@@ -32,19 +32,22 @@ def test_quant_arguments(lib):
 
 def test_e4m3_arguments(lib):
     def mm(x=F, xr=8, Kd=256, xs=F, lay=0, w=F, ws=F, E=2, N=128, flags=0, o=F, c=F, src=None, k=1, rows=8,
-           dt=moedc.BF16, out=F, outs=F, st=F):
-        return lib.moedc_matmul_e4m3(x, xr, Kd, xs, lay, w, ws, E, N, flags, o, c, src, k, rows, dt, out, outs, st, None)
+           dt=moedc.BF16, out=F, outs=F, st=F, ws_=None):
+        return lib.moedc_matmul_e4m3(x, xr, Kd, xs, lay, w, ws, E, N, flags, o, c, src, k, rows, dt, out, outs, ws_, 0, st, None)
 
     for bad in (dict(x=None), dict(x=HALF), dict(xr=-1), dict(xr=7), dict(Kd=0), dict(Kd=192), dict(xs=None),
                 dict(xs=ODD), dict(lay=3), dict(lay=moedc.SCALES_COL_MAJOR), dict(w=None), dict(w=HALF), dict(ws=None),
                 dict(ws=ODD), dict(E=0), dict(E=2000), dict(N=0), dict(flags=2), dict(c=None), dict(o=None, c=None),
                 dict(o=ODD), dict(c=ODD), dict(src=ODD), dict(src=F, k=0), dict(rows=-1), dict(o=None, rows=9, xr=9),
-                dict(dt=moedc.F32), dict(dt=9), dict(out=None), dict(out=ODD), dict(st=None), dict(st=ODD),
+                dict(dt=moedc.F32), dict(dt=9), dict(out=None), dict(out=ODD), dict(ws_=HALF), dict(st=None), dict(st=ODD),
                 dict(dt=moedc.FP8_E4M3, N=120), dict(dt=moedc.FP8_E4M3, outs=None), dict(dt=moedc.FP8_E4M3, out=HALF),
                 dict(o=None, lay=moedc.SCALES_COL_MAJOR, src=F), dict(N=2 ** 30), dict(rows=2 ** 31 - 1, xr=2 ** 31 - 1, N=2 ** 20)):
         assert mm(**bad) == moedc.ERR_ARG, bad
     assert mm(rows=0, xr=0, x=None, xs=None, out=None) == moedc.OK
     assert mm(xr=0, src=F, x=None) == moedc.OK
+    bytes_ = moedc.moedc_matmul_e4m3_workspace_bytes
+    assert bytes_(256, 2, 640) == 640 * 256 + 640 * 2 * 4
+    assert bytes_(256, 64, 640) == bytes_(200, 2, 640) == bytes_(256, 0, 640) == bytes_(256, 2, 0) == 0
 
 
 def test_layer_arguments(lib):
