@@ -212,10 +212,10 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
     if (over && blockIdx.x == 0) raise_status(a.status, MOEDC_ERR_CAPACITY);
 
     // kMmE4m3: the epilogue's threads keep 128 sums each.  The shares add up to the launch's
-    // 384 x 168 registers: 256 x 224 + 128 x 56.
+    // 384 x 168 registers: 256 x 232 + 128 x 40.
     if constexpr (MODE == kMmE4m3) {
-        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
-        else asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+        if (warp < 8) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
+        else asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     }
     if (warp < 8) {
         // ---- epilogue
@@ -274,21 +274,21 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                             if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, 0);
                         };
                         if (some) {
-                            // the next 16 columns are read while 16 are added up; the buffer is free
+                            // the next 32 columns are read while 32 are added up; the buffer is free
                             // once the last ones are in registers
-                            float v[2][16];
-                            tc_ld16(d + c01, v[0]);
+                            float v[2][32];
+                            tc_ld32(d + c01, v[0]);
 #pragma unroll
-                            for (int c = 0; c < 8; ++c) {
+                            for (int c = 0; c < 4; ++c) {
                                 tc_wait_ld();
 #pragma unroll
-                                for (int j = 0; j < 16; ++j) asm volatile("" : "+f"(v[c & 1][j]));
-                                if (c < 7) tc_ld16(d + (c < 3 ? c01 + (c + 1) * 16 : c23 + (c - 3) * 16), v[(c + 1) & 1]);
+                                for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(v[c & 1][j]));
+                                if (c < 3) tc_ld32(d + (c < 1 ? c01 + 32 : c23 + (c - 1) * 32), v[(c + 1) & 1]);
                                 else release();
-                                const float2 s = splat2(c < 4 ? f0 : f1);
+                                const float2 s = splat2(c < 2 ? f0 : f1);
 #pragma unroll
-                                for (int j = 0; j < 8; ++j)
-                                    acc[c * 8 + j] = fma2_rn(make_float2(v[c & 1][2 * j], v[c & 1][2 * j + 1]), s, acc[c * 8 + j]);
+                                for (int j = 0; j < 16; ++j)
+                                    acc[c * 16 + j] = fma2_rn(make_float2(v[c & 1][2 * j], v[c & 1][2 * j + 1]), s, acc[c * 16 + j]);
                             }
                         } else {
                             release();
