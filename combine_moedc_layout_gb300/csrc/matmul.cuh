@@ -8,8 +8,8 @@
 
 namespace moedc {
 
-// out = x W^T (kMmForward, kMmE4m3), dx = dout W (kMmDx), dW = dout^T x (kMmDw)
-enum MmMode { kMmForward, kMmDx, kMmDw, kMmE4m3 };
+// out = x W^T, dx = dout W, dW = dout^T x
+enum MmMode { kMmForward, kMmDx, kMmDw };
 
 struct MmArgs {
     int E;
@@ -21,15 +21,15 @@ struct MmArgs {
     int top_k;
     const int32_t *offsets, *counts, *src;
     int32_t* status;
-    // kMmE4m3: scale of row r (row i of expert e's slots) and channels 128 g ..: xs[r * xs_r +
+    // e4m3: scale of row r (row i of expert e's slots) and channels 128 g ..: xs[r * xs_r +
     // g * xs_g] (xs[e * xs_e + i * xs_r + g * xs_g]); ws [E][1 or 2][blocks][K / 128]
     const float *xs, *ws;
     int64_t xs_e, xs_r, xs_g;
     void* out;
-    void* extra;        // gated: both products (kMmForward), the codes' scales (kMmE4m3)
+    void* extra;        // gated: both products (kMmForward); the codes' scales (e4m3)
     bool gated, f16;    // f16: 16-bit outputs are f16 (else bf16)
     bool f32;           // kMmDw: binary32 output
-    bool codes;         // kMmE4m3: e4m3 output
+    bool codes;         // e4m3 output
     bool vec;           // 16-byte stores fit the output
     unsigned wait_extra;
 };
@@ -47,6 +47,22 @@ __device__ __forceinline__ void mm_expert_rows(const MmArgs& a, int e, int& beg,
     }
     beg = (int)(b < n ? b : 0);
     end = (int)(b < n ? n : 0);
+}
+
+// Row of x of packed row r; -1 where there is none.
+__device__ __forceinline__ int mm_x_row(const MmArgs& a, int r)
+{
+    if (!a.src) return r;
+    const int i = __ldg(a.src + r);
+    const int t = i < 0 ? -1 : i / a.top_k;
+    return t < a.x_rows ? t : -1;
+}
+
+__device__ __forceinline__ float mm_silu_mul(float g, float u)
+{
+    float s, rest;
+    sigmoid_both(g, s, rest);
+    return g * s * u;
 }
 
 // By the whole block: the rows of every expert, and the chunks of chunk_rows rows of the
@@ -98,11 +114,13 @@ __device__ __forceinline__ bool mm_chunks(const MmArgs& a, int chunk_rows, int t
 
 namespace moedc_host {
 
-// By pairs of SMs on tcgen05 (matmul_pair.cuh).  x: kMmForward and kMmE4m3 the rows, kMmDx
-// and kMmDw dout; w: the weights, kMmDw x.  Leading dimensions in elements.
+// By pairs of SMs on tcgen05 (matmul_pair.cuh).  Leading dimensions in elements.
 int launch_mm_forward(const moedc::MmArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t stream);
 int launch_mm_dx(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* w, cudaStream_t stream);
 int launch_mm_dw(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* x, int64_t ldx, cudaStream_t stream);
-int launch_mm_e4m3(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream);
+// e4m3, by single SMs: the tokens on the tile's rows (matmul_rows.cu), no src
+int launch_mm_rows(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream);
+// the weights on the tile's rows (matmul_stream.cu): few rows to an expert
+int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream);
 
 }  // namespace moedc_host

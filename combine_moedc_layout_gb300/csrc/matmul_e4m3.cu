@@ -1,6 +1,5 @@
 // Products of packed expert rows in e4m3 with a scale for each block of 128.
-#include "matmul_pair.cuh"
-#include "tensor_map.cuh"
+#include "matmul.cuh"
 
 namespace moedc {
 
@@ -42,6 +41,10 @@ __global__ void __launch_bounds__(kMmCopyRows* kWarp) matmul_gather_kernel(const
 
 namespace moedc_host {
 
+#ifndef MOEDC_STREAM_ROWS
+#define MOEDC_STREAM_ROWS 64
+#endif
+
 // Gathering the rows of a block's stage by TMA takes some 80 clocks for four of them, again
 // for every tile of columns: beyond some 25 rows it is longer than the products.  Then they
 // are brought into packed order first.
@@ -65,24 +68,6 @@ int launch_mm_gather(moedc::MmArgs& a, const void* x, uint8_t* workspace, cudaSt
     a.x_rows = a.rows;
     a.xs_e = (int64_t)a.slots * groups;
     return launch_status();
-}
-
-int launch_mm_e4m3(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream)
-{
-    constexpr auto kType = CU_TENSOR_MAP_DATA_TYPE_UINT8;
-    constexpr auto kSwizzle = CU_TENSOR_MAP_SWIZZLE_128B;
-    CUtensorMap l, r, all;   // left in boxes of 32 rows (gathered: one) and of 128
-    const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
-    const cuuint64_t lsize[2] = {K, (cuuint64_t)a.x_rows}, lstride[1] = {K};
-    const cuuint32_t lbox[2] = {128, a.src ? 1u : 32u}, allbox[2] = {128, moedc::kMmHalf};
-    const cuuint64_t size[4] = {K, N, parts, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * parts};
-    const cuuint32_t box[4] = {128, moedc::kMmHalf, 1, 1};
-    if (!tensor_map(&l, kType, kSwizzle, x, 2, lsize, lstride, lbox) ||
-        !tensor_map(&all, kType, kSwizzle, x, 2, lsize, lstride, allbox) || !tensor_map(&r, kType, kSwizzle, w, 4, size, stride, box))
-        return MOEDC_ERR_CUDA;
-    const int tile = a.gated ? moedc::kMmHalf : moedc::kMmTile;
-    const int64_t units = ((int64_t)a.rows / moedc::kMmTile + (a.E < a.rows ? a.E : a.rows)) * ((a.N + (int64_t)tile - 1) / tile);
-    return launch_mm_pair<moedc::kMmE4m3>(a, units, l, r, all, stream);
 }
 
 }  // namespace moedc_host
@@ -112,7 +97,7 @@ extern "C" int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float*
         !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(src, 4) || !aligned(out, codes ? 16 : 2) ||
         !aligned(out_scales, 4) || !aligned(workspace, 16) || !aligned(dev_status, 4))
         return MOEDC_ERR_ARG;
-    if (((int64_t)rows / 256 + E) * (N / 128 + 1) > INT32_MAX) return MOEDC_ERR_ARG;   // units are counted in 32 bits
+    if (((int64_t)rows / 128 + E) * (N / 128 + 1) > INT32_MAX) return MOEDC_ERR_ARG;   // units are counted in 32 bits
     if (rows == 0 || x_rows == 0) return MOEDC_OK;
     if (!x || !xs || !out || (codes && !out_scales)) return MOEDC_ERR_ARG;
     moedc::MmArgs a{};
@@ -146,5 +131,7 @@ extern "C" int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float*
         if (st != MOEDC_OK) return st;
         x = workspace;
     }
-    return launch_mm_e4m3(a, x, w, stream);
+    const int64_t active = E < rows ? E : rows;
+    if (a.src || rows <= MOEDC_STREAM_ROWS * active) return launch_mm_stream(a, x, w, stream);
+    return launch_mm_rows(a, x, w, stream);
 }

@@ -1,0 +1,420 @@
+// e4m3 products for few rows to an expert, where the stream of the weights is the bound.
+//
+// The weights lie on the rows of the tile and the tokens on its columns, as many (in
+// sixteens) as there are: a block multiplies 256 weight rows, in two tiles of 128 (with
+// `gated` the gate and the up rows of 128 channels), by up to 128 tokens.  A stage, 128
+// channels, is 32 KB of weights and 2 KB for each 16 tokens; three or four stages under way
+// on each SM keep HBM busy.
+//
+// Each stage has sums of its own, two buffers of tensor memory in turn.  A thread of the
+// epilogue owns a weight row of both tiles and half of the tokens, and adds
+//   xs[token] ws[block] * sum
+// into 128 registers; the factors come from shared memory, where one warp puts them four
+// groups ahead.
+//
+// Warps: 0-7 epilogue (0-3 the first 64 tokens, 4-7 the others), 8 TMA, 9 MMA, 10 factors.
+#include "matmul.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.cuh"
+
+namespace moedc {
+
+constexpr int kMsThreads = 11 * kWarp;
+constexpr int kMsRows = 128;                        // of a tile of weights
+constexpr int kMsTokens = 128;
+constexpr int kMsHalf = kMsTokens / 2;
+constexpr int kMsGroup = 128;                       // channels, and bytes, of a stage
+constexpr int kMsTile = kMsRows * kMsGroup;
+constexpr int kMsStage = 2 * kMsTile + kMsTokens * kMsGroup;
+constexpr int kMsStages = 4;
+constexpr int kMsFactors = 4 * 2 * kMsTokens;       // floats of four groups
+constexpr int kMsFactorBufs = 3;
+constexpr int kMsColumns = 512;
+
+struct MsUnit {
+    int e, r0, m, n0;
+};
+
+__device__ __forceinline__ MsUnit ms_unit(const MmArgs& a, const int32_t* s_pre, const int32_t* s_beg, const int32_t* s_end,
+                                          int tiles, int unit)
+{
+    int lo = 0, hi = a.E - 1;   // last expert whose units begin at or before `unit`
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if ((int64_t)s_pre[mid] * tiles <= unit) lo = mid; else hi = mid - 1;
+    }
+    const int chunks = s_pre[lo + 1] - s_pre[lo];
+    const int in = unit - s_pre[lo] * tiles, t = in / chunks;   // chunks of one tile are neighbours
+    MsUnit u;
+    u.e = lo;
+    u.n0 = t * (a.gated ? kMsRows : 2 * kMsRows);
+    u.r0 = s_beg[lo] + (in - t * chunks) * kMsTokens;
+    u.m = min(kMsTokens, s_end[lo] - u.r0);
+    return u;
+}
+
+__global__ void __launch_bounds__(kMsThreads, 1)
+matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap wmap,
+                     const __grid_constant__ CUtensorMap xmap)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int64_t s_scan[kMsThreads / kWarp];
+    __shared__ uint64_t full[kMsStages], empty[kMsStages], d_full[2], d_empty[2], f_full[kMsFactorBufs], f_empty[kMsFactorBufs];
+    __shared__ uint64_t done, never;
+    __shared__ float s_top[2][2][4][kMsHalf], s_scale[2][2][kMsHalf];
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+    const int tile_n = a.gated ? kMsRows : 2 * kMsRows;
+    const int tiles = (a.N + tile_n - 1) / tile_n, groups = a.K / kMsGroup;
+    float* s_factors = reinterpret_cast<float*>(smem + kMsStages * kMsStage);
+    int32_t* s_pre = reinterpret_cast<int32_t*>(s_factors + kMsFactorBufs * kMsFactors);
+    int32_t *s_beg = s_pre + a.E + 1, *s_end = s_beg + a.E;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMsStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(d_full + b, 1);
+            mbar_init(d_empty + b, 8);
+        }
+        for (int b = 0; b < kMsFactorBufs; ++b) {
+            mbar_init(f_full + b, 1);
+            mbar_init(f_empty + b, 8);
+        }
+        mbar_init(&done, 1);
+        mbar_init(&never, 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(&s_tmem)),
+                     "n"(kMsColumns) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tc_fence_before();
+    }
+    pdl_enter();
+    const bool over = mm_chunks<kMsThreads>(a, kMsTokens, tiles, s_scan, s_pre, s_beg, s_end);   // ends with a barrier
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    const int units = s_pre[a.E] * tiles;
+    if (over && blockIdx.x == 0) raise_status(a.status, MOEDC_ERR_CAPACITY);
+
+    if (warp < 8) {
+        // ---- epilogue
+        if (a.wait_extra) mbar_wait(&never, 0, &s_abort);
+        const int half = warp >> 2, quad = warp & 3, row = quad * kWarp + lane, j0 = half * kMsHalf;
+        const uint32_t d0 = tmem + ((uint32_t)(quad * kWarp) << 16) + j0;
+        MvRing accs, facs;
+        bool bad = false;
+        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+            const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
+            const int mine = u.m - j0;                      // tokens of this warp
+            float2 acc[2][kMsHalf / 2];
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int j = 0; j < kMsHalf / 2; ++j) acc[t][j] = make_float2(0.0f, 0.0f);
+            for (int g = 0; g < groups; ++g) {
+                if (g % 4 == 0) mbar_wait_inline(f_full + facs.slot, facs.phase, &s_abort);
+                mbar_wait_inline(d_full + accs.slot, accs.phase, &s_abort);
+                __syncwarp();
+                tc_fence_after();
+                const float* f = s_factors + facs.slot * kMsFactors + (g % 4) * (2 * kMsTokens) + j0;
+                const uint32_t d = d0 + accs.slot * (2 * kMsTokens);
+#pragma unroll
+                for (int c = 0; c < kMsHalf; c += 16) {
+                    if (c < mine) {
+                        float v[2][16];
+                        tc_ld16(d + c, v[0]);
+                        tc_ld16(d + kMsTokens + c, v[1]);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) asm volatile("" : "+f"(v[t][j]));
+#pragma unroll
+                            for (int j = 0; j < 16; j += 4) {
+                                const float4 s = *reinterpret_cast<const float4*>(f + t * kMsTokens + c + j);
+                                float2* o = acc[t] + (c + j) / 2;
+                                o[0] = fma2_rn(make_float2(v[t][j], v[t][j + 1]), make_float2(s.x, s.y), o[0]);
+                                o[1] = fma2_rn(make_float2(v[t][j + 2], v[t][j + 3]), make_float2(s.z, s.w), o[1]);
+                            }
+                        }
+                    }
+                }
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(d_empty + accs.slot);
+                    if (g % 4 == 3 || g == groups - 1) mbar_arrive(f_empty + facs.slot);
+                }
+                accs.next(2);
+                if (g % 4 == 3 || g == groups - 1) facs.next(kMsFactorBufs);
+            }
+            // tokens that src leads outside of x: zeros
+            if (a.src) {
+#pragma unroll
+                for (int c = 0; c < kMsHalf; c += kWarp) {
+                    const bool out = c + lane < mine && mm_x_row(a, u.r0 + j0 + c + lane) < 0;
+                    const unsigned lost = __ballot_sync(0xffffffffu, out);
+                    bad |= out;
+                    if (lost) {
+#pragma unroll
+                        for (int j = 0; j < kWarp; j += 2)
+#pragma unroll
+                            for (int t = 0; t < 2; ++t) {
+                                float2& o = acc[t][(c + j) / 2];
+                                if (lost >> j & 1) o.x = 0.0f;
+                                if (lost >> (j + 1) & 1) o.y = 0.0f;
+                            }
+                    }
+                }
+            }
+            if (a.gated) {
+#pragma unroll
+                for (int j = 0; j < kMsHalf / 2; ++j) {
+                    if (2 * j >= mine) break;
+                    acc[0][j].x = mm_silu_mul(acc[0][j].x, acc[1][j].x);
+                    acc[0][j].y = mm_silu_mul(acc[0][j].y, acc[1][j].y);
+                }
+            }
+            const int n = u.n0 + row;
+            const int64_t at = (int64_t)(u.r0 + j0) * a.N + n;
+            if (!a.codes) {
+                // a warp's lanes are 32 neighbouring channels of a token
+                uint16_t* o = static_cast<uint16_t*>(a.out) + at;
+#pragma unroll
+                for (int j = 0; j < kMsHalf; ++j) {
+                    if (j >= mine) break;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t == 1 && a.gated) break;
+                        const float v = j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x;
+                        if (n + t * kMsRows < a.N)
+                            o[(int64_t)j * a.N + t * kMsRows] =
+                                a.f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                    }
+                }
+            } else {
+                // the rule of dispatch, of the binary32 values: a token's 128 channels are the
+                // lanes of four warps.  Magnitudes order as their bits do; NaN is left out.
+#pragma unroll
+                for (int j = 0; j < kMsHalf; ++j) {
+                    if (j >= mine) break;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t == 1 && a.gated) break;
+                        const float v = fabsf(j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x);
+                        const unsigned top = __reduce_max_sync(0xffffffffu, v == v ? __float_as_uint(v) : 0u);
+                        if (lane == 0) s_top[half][t][quad][j] = __uint_as_float(top);
+                    }
+                }
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+                {
+                    const int t = row / kMsHalf, j = row % kMsHalf;   // 128 threads: both tiles' 64 tokens
+                    if (j < mine && !(t == 1 && a.gated)) {
+                        const float(&p)[4][kMsHalf] = s_top[half][t];
+                        const float top = fmaxf(fmaxf(p[0][j], p[1][j]), fmaxf(p[2][j], p[3][j]));
+                        const float sc = __fdiv_rn(fmaxf(top, 1e-4f), 448.0f);
+                        s_scale[half][t][j] = sc;
+                        const int b = u.n0 / 128 + t;
+                        if (b < a.N / 128) static_cast<float*>(a.extra)[(int64_t)(u.r0 + j0 + j) * (a.N / 128) + b] = sc;
+                    }
+                }
+                asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
+                uint8_t* o = static_cast<uint8_t*>(a.out) + at;
+#pragma unroll
+                for (int j = 0; j < kMsHalf; ++j) {
+                    if (j >= mine) break;
+#pragma unroll
+                    for (int t = 0; t < 2; ++t) {
+                        if (t == 1 && a.gated) break;
+                        const float v = j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x;
+                        if (n + t * kMsRows < a.N)
+                            o[(int64_t)j * a.N + t * kMsRows] = (uint8_t)pack_e4m3x2(__fdiv_rn(v, s_scale[half][t][j]), 0.0f);
+                    }
+                }
+            }
+        }
+        if (bad) raise_status(a.status, MOEDC_ERR_EXPERT_RANGE);
+    } else if (warp == 8) {
+        // ---- TMA: two tiles of weights; the tokens in sixteens, or four by four where they
+        // are gathered
+        MvRing ring;
+        int issued = 0;
+        bool stop = false;
+        for (int unit = blockIdx.x; unit < units && !stop; unit += gridDim.x) {
+            const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
+            int t[4] = {0, 0, 0, 0};
+            if (a.src) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (lane * 4 + i < u.m) t[i] = max(mm_x_row(a, u.r0 + lane * 4 + i), 0);
+            }
+            const int bytes = 2 * kMsTile + (a.src ? (u.m + 3) / 4 * 4 : (u.m + 15) / 16 * 16) * kMsGroup;
+            for (int g = 0; g < groups; ++g) {
+                const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
+                if (__any_sync(0xffffffffu, !ok)) {
+                    stop = true;
+                    break;
+                }
+                uint8_t* st = smem + ring.slot * kMsStage;
+                uint64_t* bar = full + ring.slot;
+                if (lane == 0) {
+                    mbar_arrive_expect(bar, bytes);
+                    // [E][1 or 2][N][K]
+                    tma_4d(st, &wmap, g * kMsGroup, u.n0, 0, u.e, bar);
+                    tma_4d(st + kMsTile, &wmap, g * kMsGroup, u.n0 + (a.gated ? 0 : kMsRows), a.gated ? 1 : 0, u.e, bar);
+                }
+                __syncwarp();
+                st += 2 * kMsTile;
+                if (a.src) {
+                    if (lane * 4 < u.m) tma_gather4(st + lane * 4 * kMsGroup, &xmap, g * kMsGroup, t[0], t[1], t[2], t[3], bar);
+                } else if (lane * 16 < u.m) {
+                    tma_2d(st + lane * 16 * kMsGroup, &xmap, g * kMsGroup, u.r0 + lane * 16, bar);
+                }
+                __syncwarp();
+                ring.next(kMsStages);
+                ++issued;
+            }
+        }
+        // no copy may land after the block has gone, whatever else gave up
+        for (int n = max(0, issued - kMsStages); n < issued; ++n) {
+            volatile int alone = 0;
+            if (!mbar_wait(full + n % kMsStages, (n / kMsStages) & 1, &alone)) s_abort = 1;
+        }
+        __syncwarp();
+    } else if (warp == 9) {
+        // ---- MMA: one elected lane issues; the warp stays together
+        const bool leader = tc_elect();
+        MvRing ring, accs;
+        int k = 0;
+        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+            const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
+            // columns: as many tokens as there are, by 16
+            const uint32_t idesc = (1u << 4) | ((uint32_t)((u.m + 15) / 16 * 2) << 17) | ((uint32_t)(kMsRows / 16) << 24);
+            for (int g = 0; g < groups; ++g) {
+                if (k++ >= 2) mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
+                mbar_wait_warp(full + ring.slot, ring.phase, &s_abort);
+                tc_fence_after();
+                const uint32_t st = smem_u32(smem + ring.slot * kMsStage);
+                const uint64_t w = tc_smem_desc(st), x = tc_smem_desc(st + 2 * kMsTile);
+                if (leader) {
+#pragma unroll
+                    for (int t = 0; t < 2; ++t)
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)   // 32 channels each; a descriptor counts in 16 bytes
+                            tc_mma_e4m3(tmem + accs.slot * (2 * kMsTokens) + t * kMsTokens, w + t * (kMsTile / 16) + p * 2, x + p * 2,
+                                        idesc, p != 0);
+                    tc_commit(empty + ring.slot);
+                    tc_commit(d_full + accs.slot);
+                }
+                __syncwarp();
+                accs.next(2);
+                ring.next(kMsStages);
+            }
+        }
+        // tensor memory is given back only when the last product is through
+        if (leader) tc_commit(&done);
+        __syncwarp();
+        volatile int alone = 0;
+        if (!mbar_wait(&done, 0, &alone)) s_abort = 1;
+        __syncwarp();
+    } else {
+        // ---- factors: four groups of a token are one load where they are 16 aligned bytes
+        MvRing facs;
+        const bool quads = a.xs_g == 1 && groups % 4 == 0 && reinterpret_cast<uintptr_t>(a.xs) % 16 == 0;
+        const int blocks = (a.N + 127) / 128;
+        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+            const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
+            const float* xs[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                const int r = u.r0 + min(q * kWarp + lane, u.m - 1);
+                xs[q] = a.xs + (a.offsets || !a.counts || a.src ? max(mm_x_row(a, r), 0) * a.xs_r
+                                                                : u.e * a.xs_e + (r - u.e * a.slots) * a.xs_r);
+            }
+            const int b0 = u.n0 / 128;
+            const float* w0 = a.ws + ((int64_t)u.e * (a.gated ? 2 : 1) * blocks + b0) * groups;
+            const float* w1 = w0 + (int64_t)(a.gated ? blocks : b0 + 1 < blocks) * groups;
+            float s[4][4], v0[4], v1[4];
+            auto load = [&](int g0) __attribute__((always_inline)) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int g = min(g0 + i, groups - 1);
+                    v0[i] = __ldg(w0 + g), v1[i] = __ldg(w1 + g);
+                }
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q * kWarp >= u.m) break;
+                    if (quads) {
+                        const float4 v = __ldg(reinterpret_cast<const float4*>(xs[q] + min(g0, groups - 4)));
+                        s[q][0] = v.x, s[q][1] = v.y, s[q][2] = v.z, s[q][3] = v.w;
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) s[q][i] = __ldg(xs[q] + min(g0 + i, groups - 1) * a.xs_g);
+                    }
+                }
+            };
+            load(0);
+            for (int g0 = 0; g0 < groups; g0 += 4) {
+                mbar_wait_warp(f_empty + facs.slot, facs.phase ^ 1, &s_abort);
+                float* f = s_factors + facs.slot * kMsFactors + lane;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    if (q * kWarp >= u.m) break;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        f[i * (2 * kMsTokens) + q * kWarp] = s[q][i] * v0[i];
+                        f[i * (2 * kMsTokens) + kMsTokens + q * kWarp] = s[q][i] * v1[i];
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(f_full + facs.slot);
+                facs.next(kMsFactorBufs);
+                load(min(g0 + 4, groups - 1));
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "n"(kMsColumns) : "memory");
+    if (threadIdx.x == 0 && s_abort) raise_status(a.status, MOEDC_ERR_TIMEOUT);
+}
+
+}  // namespace moedc
+
+namespace moedc_host {
+
+int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream)
+{
+    constexpr auto kType = CU_TENSOR_MAP_DATA_TYPE_UINT8;
+    constexpr auto kSwizzle = CU_TENSOR_MAP_SWIZZLE_128B;
+    CUtensorMap wmap, xmap;
+    const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
+    const cuuint64_t xsize[2] = {K, (cuuint64_t)a.x_rows}, xstride[1] = {K};
+    const cuuint32_t xbox[2] = {128, a.src ? 1u : 16u};
+    const cuuint64_t size[4] = {K, N, parts, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * parts};
+    const cuuint32_t box[4] = {128, moedc::kMsRows, 1, 1};
+    if (!tensor_map(&xmap, kType, kSwizzle, x, 2, xsize, xstride, xbox) || !tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box))
+        return MOEDC_ERR_CUDA;
+    auto* k = moedc::matmul_stream_kernel;
+    constexpr size_t kFixed = moedc::kMsStages * moedc::kMsStage + moedc::kMsFactorBufs * moedc::kMsFactors * sizeof(float);
+    static PerDevice raised;
+    if (!raise_smem_limit(raised, (const void*)k, (int)kFixed + (3 * MOEDC_MAX_E + 1) * 4)) return MOEDC_ERR_CUDA;
+    const int tile = a.gated ? moedc::kMsRows : 2 * moedc::kMsRows;
+    const int64_t units = ((int64_t)a.rows / moedc::kMsTokens + (a.E < a.rows ? a.E : a.rows)) * ((a.N + (int64_t)tile - 1) / tile);
+    const int blocks = sm_count();
+    clear_stale_error();
+    launch(k, (int)(units < blocks ? units : blocks), moedc::kMsThreads, kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a,
+           wmap, xmap);
+    return launch_status();
+}
+
+}  // namespace moedc_host

@@ -111,23 +111,28 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t* bar)
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
                  "h"((uint16_t)3) : "memory");
 }
-template <bool E4M3>
 __device__ __forceinline__ void tc_mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
-    if constexpr (E4M3)
-        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-                     " tcgen05.mma.cta_group::2.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-                     "r"((uint32_t)add) : "memory");
-    else
-        asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
-                     " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
-                     "r"((uint32_t)add) : "memory");
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+                 "r"((uint32_t)add) : "memory");
 }
 // Operand whose contracted axis is its rows, in the 128-byte swizzle: rows of 64 elements of
 // the other axis, eight of them 1024 bytes, the next 64 elements `next` bytes on
 __device__ __forceinline__ uint64_t tc_smem_desc_mn(uint32_t addr, uint32_t next)
 {
     return (uint64_t)((addr >> 4) & 0x3fffu) | ((uint64_t)(next >> 4) << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
+}
+__device__ __forceinline__ void tma_4d(void* to, const CUtensorMap* map, int x, int y, int z, int w, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+                     smem_u32(to)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(smem_u32(bar)) : "memory");
+}
+// four rows, each by its number; the map's boxes are one row high
+__device__ __forceinline__ void tma_gather4(void* to, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3, uint64_t* bar)
+{
+    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
+                     smem_u32(to)), "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(smem_u32(bar)) : "memory");
 }
 // Copies whose bytes are counted at a barrier of either block of the pair, by its cluster
 // address; they land in this block.
@@ -152,11 +157,12 @@ __device__ __forceinline__ void tma_4d_pair(void* to, const CUtensorMap* map, in
     asm volatile("cp.async.bulk.tensor.4d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
                      smem_u32(to)), "l"(map), "r"(x), "r"(y), "r"(z), "r"(w), "r"(bar) : "memory");
 }
-// four rows, each by its number; the map's boxes are one row high
-__device__ __forceinline__ void tma_gather4_pair(void* to, const CUtensorMap* map, int x, int r0, int r1, int r2, int r3, uint32_t bar)
+// one block's e4m3 products, both operands in shared memory
+__device__ __forceinline__ void tc_mma_e4m3(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {
-    asm volatile("cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(
-                     smem_u32(to)), "l"(map), "r"(x), "r"(r0), "r"(r1), "r"(r2), "r"(r3), "r"(bar) : "memory");
+    asm volatile("{\n .reg .pred p;\n setp.ne.u32 p, %4, 0;\n"
+                 " tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n}\n" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+                 "r"((uint32_t)add) : "memory");
 }
 
 }  // namespace moedc

@@ -63,12 +63,15 @@ CASES = [
 
 @pytest.mark.parametrize("out", ["bf16", "f16", "e4m3"])
 @pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("counts,N,Kd,align", CASES)
-def test_packed_rows(counts, N, Kd, align, swiglu, out):
+def test_packed_rows(counts, N, Kd, align, swiglu, out, many):
+    """`many`: rows of nobody behind the groups, so that the call expects many rows to an expert
+    and takes its other form."""
     if out == "e4m3":
         N = -(-N // 128) * 128
     g = torch.Generator().manual_seed(len(counts) + N)
-    offsets, cnt, rows = groups(counts, align, tail=5)
+    offsets, cnt, rows = groups(counts, align, tail=300 * len(counts) if many else 5)
     w, ws = weights(g, len(counts), N, Kd, swiglu)
     x, xs = rows_of(g, rows, Kd)
     mine = owned(offsets, cnt, rows)
