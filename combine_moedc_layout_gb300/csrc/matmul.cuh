@@ -8,14 +8,14 @@
 
 namespace moedc {
 
-// out = x W^T, dx = dout W, dW = dout^T x
-enum MmMode { kMmForward, kMmDx, kMmDw };
+// out = x W^T, dx = dout W (of matmul_pair.cu)
+enum MmMode { kMmForward, kMmDx };
 
 struct MmArgs {
     int E;
     int N;              // columns of the output (with `gated`, of each of the two products)
-    int K;              // elements of a row of x that a product adds up (kMmDw: rows of an expert)
-    int M;              // kMmDw: rows of the output
+    int K;              // elements of a row of x that a product adds up 
+    int M;              // dW: rows of the output
     int rows, x_rows;
     int slots;          // rows of an expert's slots where there are no offsets
     int top_k;
@@ -26,9 +26,9 @@ struct MmArgs {
     const float *xs, *ws;
     int64_t xs_e, xs_r, xs_g;
     void* out;
-    void* extra;        // gated: both products (kMmForward); the codes' scales (e4m3)
+    void* extra;        // gated: both products; the codes' scales (e4m3)
     bool gated, f16;    // f16: 16-bit outputs are f16 (else bf16)
-    bool f32;           // kMmDw: binary32 output
+    bool f32;           // dW: binary32 output
     bool codes;         // e4m3 output
     bool vec;           // 16-byte stores fit the output
     unsigned wait_extra;
@@ -114,7 +114,7 @@ __device__ __forceinline__ bool mm_chunks(const MmArgs& a, int chunk_rows, int t
 
 namespace moedc_host {
 
-// By pairs of SMs on tcgen05 (matmul_pair.cuh).  Leading dimensions in elements.
+// By pairs of SMs (matmul_pair.cu, matmul_dw.cu).  Leading dimensions in elements.
 int launch_mm_forward(const moedc::MmArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t stream);
 int launch_mm_dx(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* w, cudaStream_t stream);
 int launch_mm_dw(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* x, int64_t ldx, cudaStream_t stream);

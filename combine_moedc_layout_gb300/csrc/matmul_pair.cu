@@ -1,0 +1,310 @@
+// Products of packed expert rows with 16-bit weights, and the rows' gradient, on the
+// 5th-generation tensor cores, by pairs of SMs.
+//
+// The weights lie on the rows of the tile and the tokens on its columns, as many (in
+// 32s, up to 256) as there are, so that experts of uneven sizes cost what they hold.  A
+// pair (a cluster of two blocks) computes a tile of 256 weight rows with one instruction
+// stream: block r of the pair brings rows 128 r .. of the weights and half of the tokens into
+// its shared memory, and holds its rows' sums in its tensor memory.  So each operand byte is
+// fetched once for a tile, and each SM's share is at most 32 KB for 512 clocks of products (a
+// stage: 64 elements of the contracted axis).
+//
+//   kMmForward   out = x W^T: the rows are those of W, K-major.  With `gated` they are gate and
+//                up rows of the same channels in turn, so that a thread finds the other product
+//                of its channel in the neighbouring lane
+//   kMmDx        dx = dout W: the rows are W's columns; the contracted axis is its rows
+//
+// Warps: 0-7 epilogue (0-3 every other 32 tokens, 4-7 the others), 8 TMA, 9 MMA (of the
+// pair's first block, for both; the copies of both count at its barrier).  Tensor memory: two
+// sums of 256 columns.
+#include "matmul.cuh"
+#include "tcgen05.cuh"
+#include "tensor_map.cuh"
+
+namespace moedc {
+
+constexpr int kMpThreads = 10 * kWarp;
+constexpr int kMpTile = 256;                    // weight rows of the pair; tokens
+constexpr int kMpHalf = kMpTile / 2;
+constexpr int kMpElems = 64;                    // of the contracted axis in a stage
+constexpr int kMpBytes = 128;
+constexpr int kMpOperand = kMpHalf * kMpBytes;  // a block's share of one operand
+constexpr int kMpStage = 2 * kMpOperand;
+constexpr int kMpStages = 6;
+constexpr int kMpColumns = 512;
+
+struct MpUnit {
+    int e, r0, m, n0;
+    int cols;           // of the product: m in 32s, as a pair's products go
+};
+
+__device__ __forceinline__ MpUnit mp_unit(const MmArgs& a, const int32_t* s_pre, const int32_t* s_beg, const int32_t* s_end,
+                                          int tiles, int unit)
+{
+    int lo = 0, hi = a.E - 1;   // last expert whose units begin at or before `unit`
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2;
+        if ((int64_t)s_pre[mid] * tiles <= unit) lo = mid; else hi = mid - 1;
+    }
+    const int chunks = s_pre[lo + 1] - s_pre[lo];
+    const int in = unit - s_pre[lo] * tiles, t = in / chunks;   // chunks of one tile are neighbours
+    // an expert's chunks are equal ones: chunks - 1 of them are fewer rows than it has, as a
+    // chunk is at most 256 and all of its rows more than chunks - 1 times that
+    const int rows = s_end[lo] - s_beg[lo];
+    const int size = ((rows + chunks - 1) / chunks + 31) / 32 * 32;
+    MpUnit u;
+    u.e = lo;
+    u.n0 = t * (a.gated ? kMpHalf : kMpTile);
+    u.r0 = s_beg[lo] + (in - t * chunks) * size;
+    u.m = min(size, s_end[lo] - u.r0);
+    u.cols = (u.m + 31) / 32 * 32;
+    return u;
+}
+
+__device__ __forceinline__ uint16_t mp_round(float v, bool f16)
+{
+    return f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+}
+__device__ __forceinline__ uint32_t mp_round2(float lo, float hi, bool f16)
+{
+    return (uint32_t)mp_round(lo, f16) | (uint32_t)mp_round(hi, f16) << 16;
+}
+
+template <int MODE>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMpThreads, 1)
+matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap wmap,
+                   const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap allmap)
+{
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ int64_t s_scan[kMpThreads / kWarp];
+    __shared__ uint64_t full[kMpStages], empty[kMpStages], d_full[2], d_empty[2], done, never;
+    __shared__ uint32_t s_tmem;
+    __shared__ volatile int s_abort;
+
+    const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
+    const int rank = cluster_rank();
+    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    const int tile_n = a.gated ? kMpHalf : kMpTile;
+    const int tiles = (a.N + tile_n - 1) / tile_n, ksteps = (a.K + kMpElems - 1) / kMpElems;
+    int32_t* s_pre = reinterpret_cast<int32_t*>(smem + kMpStages * kMpStage);
+    int32_t *s_beg = s_pre + a.E + 1, *s_end = s_beg + a.E;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < kMpStages; ++s) {
+            mbar_init(full + s, 1);
+            mbar_init(empty + s, 1);
+        }
+        for (int b = 0; b < 2; ++b) {
+            mbar_init(d_full + b, 1);
+            mbar_init(d_empty + b, 16);
+        }
+        mbar_init(&done, 1);
+        mbar_init(&never, 1);
+        s_abort = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) {
+        tc_alloc_pair(&s_tmem, kMpColumns);
+        tc_fence_before();
+    }
+    pdl_enter();
+    const bool over = mm_chunks<kMpThreads>(a, kMpTile, tiles, s_scan, s_pre, s_beg, s_end);
+    cluster_sync();   // the other block's barriers stand
+    tc_fence_after();
+    const uint32_t tmem = *reinterpret_cast<volatile uint32_t*>(&s_tmem);
+    const int units = s_pre[a.E] * tiles;
+    if (over && blockIdx.x == 0) raise_status(a.status, MOEDC_ERR_CAPACITY);
+
+    if (warp < 8) {
+        // ---- epilogue
+        if (a.wait_extra) mbar_wait(&never, 0, &s_abort);
+        const int half = warp >> 2, row = rank * kMpHalf + (warp & 3) * kWarp + lane, odd = lane & 1;
+        const uint32_t d0 = tmem + ((uint32_t)((warp & 3) * kWarp) << 16);
+        MvRing accs;
+        for (int unit = pair; unit < units; unit += pairs) {
+            const MpUnit u = mp_unit(a, s_pre, s_beg, s_end, tiles, unit);
+            mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
+            tc_fence_after();
+            const uint32_t d = d0 + accs.slot * kMpTile;
+            // The thread's channel; neighbouring lanes trade a token for a token, so that each has
+            // two channels of one (with `gated`: gate and up of one), the even lane of the first
+            const int n = u.n0 + (a.gated ? row / 2 : row - odd);
+            const bool in = n < a.N;
+            uint16_t* o = static_cast<uint16_t*>(a.out) + (int64_t)u.r0 * a.N + n;
+            uint16_t* keep = static_cast<uint16_t*>(a.extra);
+            if (keep) keep += (int64_t)u.r0 * 2 * a.N + odd * a.N + n;
+            for (int c = half * 32; c < u.m; c += 64) {
+                float v[32];
+                tc_ld32(d + c, v);
+                tc_wait_ld();
+#pragma unroll
+                for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(v[j]));
+#pragma unroll
+                for (int j = 0; j < 32; j += 2) {
+                    const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
+                    const int t = c + j + odd;
+                    if (a.gated) {
+                        const float g = odd ? got : v[j], up = odd ? v[j + 1] : got;
+                        if (keep && in) {
+                            if (c + j < u.m) keep[(int64_t)(c + j) * 2 * a.N] = mp_round(v[j], a.f16);
+                            if (c + j + 1 < u.m) keep[(int64_t)(c + j + 1) * 2 * a.N] = mp_round(v[j + 1], a.f16);
+                        }
+                        if (t < u.m && in) o[(int64_t)t * a.N] = mp_round(mm_silu_mul(g, up), a.f16);
+                    } else if (t < u.m && in) {
+                        *reinterpret_cast<uint32_t*>(o + (int64_t)t * a.N) =
+                            odd ? mp_round2(got, v[j + 1], a.f16) : mp_round2(v[j], got, a.f16);
+                    }
+                }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, 0);
+            accs.next(2);
+        }
+    } else if (warp == 8) {
+        // ---- TMA: this block's weight rows, its half of the tokens
+        MvRing ring;
+        int issued = 0;
+        bool stop = false;
+        for (int unit = pair; unit < units && !stop; unit += pairs) {
+            const MpUnit u = mp_unit(a, s_pre, s_beg, s_end, tiles, unit);
+            const int mine = u.cols / 2, r0 = u.r0 + rank * mine;
+            const int bytes = 2 * (kMpOperand + (mine > 32 ? kMpHalf : 32) * kMpBytes);   // of both blocks
+            for (int s = 0; s < ksteps; ++s) {
+                const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
+                if (__any_sync(0xffffffffu, !ok)) {
+                    stop = true;
+                    break;
+                }
+                uint8_t* w = smem + ring.slot * kMpStage;
+                uint8_t* x = w + kMpOperand;
+                if (lane == 0) {
+                    const uint32_t at = cluster_addr(full + ring.slot, 0);
+                    if (rank == 0) mbar_arrive_expect(full + ring.slot, bytes);
+                    if constexpr (MODE == kMmDx) {
+#pragma unroll
+                        for (int h = 0; h < 2; ++h)
+                            tma_3d_pair(w + h * (kMpOperand / 2), &wmap, u.n0 + rank * kMpHalf + h * 64, s * kMpElems, u.e, at);
+                    } else if (a.gated) {
+                        // [E][N][gate or up][K]
+                        tma_4d_pair(w, &wmap, s * kMpElems, 0, u.n0 + rank * (kMpHalf / 2), u.e, at);
+                    } else {
+                        tma_4d_pair(w, &wmap, s * kMpElems, 0, u.n0 + rank * kMpHalf, u.e, at);
+                    }
+                    tma_2d_pair(x, mine > 32 ? &allmap : &xmap, s * kMpElems, r0, at);
+                }
+                __syncwarp();
+                ring.next(kMpStages);
+                ++issued;
+            }
+        }
+        // no copy may land after the block has gone, whatever else gave up
+        for (int n = max(0, issued - kMpStages); n < issued && rank == 0; ++n) {
+            volatile int alone = 0;
+            if (!mbar_wait(full + n % kMpStages, (n / kMpStages) & 1, &alone)) s_abort = 1;
+        }
+        // a second block that gave up sees no barrier of its copies: they have a millisecond
+        if (s_abort)
+            for (const unsigned long long t0 = globaltimer(); globaltimer() - t0 < 1000000ull;) {}
+        __syncwarp();
+    } else {
+        // ---- MMA, for both blocks: one elected lane issues; the warp stays together
+        if (rank == 0) {
+            const bool leader = tc_elect();
+            MvRing ring, accs;
+            int k = 0;
+            const uint32_t type = (a.f16 ? 0u : (1u << 7) | (1u << 10)) | (MODE == kMmDx ? 1u << 15 : 0u);
+            for (int unit = pair; unit < units; unit += pairs) {
+                const MpUnit u = mp_unit(a, s_pre, s_beg, s_end, tiles, unit);
+                const uint32_t idesc = (1u << 4) | type | ((uint32_t)(u.cols / 8) << 17) | ((uint32_t)(kMpTile / 16) << 24);
+                for (int s = 0; s < ksteps; ++s) {
+                    if (s == 0 && k++ >= 2) mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
+                    mbar_wait_warp(full + ring.slot, ring.phase, &s_abort);
+                    tc_fence_after();
+                    const uint32_t st = smem_u32(smem + ring.slot * kMpStage);
+                    const uint64_t w = MODE == kMmDx ? tc_smem_desc_mn(st, kMpOperand / 2) : tc_smem_desc(st);
+                    const uint64_t x = tc_smem_desc(st + kMpOperand);
+                    if (leader) {
+#pragma unroll
+                        for (int p = 0; p < 4; ++p)
+                            // a descriptor counts in 16 bytes: 32 of a row, or 16 rows of 128
+                            tc_mma_pair(tmem + accs.slot * kMpTile, w + p * (MODE == kMmDx ? 128 : 2), x + p * 2, idesc, p != 0 || s != 0);
+                        tc_commit_pair(empty + ring.slot);
+                        if (s == ksteps - 1) tc_commit_pair(d_full + accs.slot);
+                    }
+                    __syncwarp();
+                    if (s == ksteps - 1) accs.next(2);
+                    ring.next(kMpStages);
+                }
+            }
+            // tensor memory is given back only when the last product is through
+            if (leader) tc_commit_pair(&done);
+            __syncwarp();
+        }
+        volatile int alone = 0;
+        if (!mbar_wait(&done, 0, &alone)) s_abort = 1;
+        __syncwarp();
+    }
+    tc_fence_before();
+    __syncwarp();
+    cluster_sync();
+    tc_fence_after();
+    if (warp == 9) tc_free_pair(tmem, kMpColumns);
+    if (threadIdx.x == 0 && s_abort) raise_status(a.status, MOEDC_ERR_TIMEOUT);
+}
+
+}  // namespace moedc
+
+namespace moedc_host {
+
+bool map_rows16(CUtensorMap* map, const void* base, int64_t width, int64_t rows, int64_t ld, int box_rows)
+{
+    const cuuint64_t size[2] = {(cuuint64_t)width, (cuuint64_t)rows}, stride[1] = {(cuuint64_t)ld * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)box_rows};
+    return tensor_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, CU_TENSOR_MAP_SWIZZLE_128B, base, 2, size, stride, box);
+}
+
+namespace {
+
+// x: the rows, in boxes of 32 and of 128
+template <int MODE>
+int launch_mm_pair(const moedc::MmArgs& a, const CUtensorMap& w, const void* x, int64_t ldx, cudaStream_t stream)
+{
+    CUtensorMap rows, all;
+    if (!map_rows16(&rows, x, a.K, a.rows, ldx, 32) || !map_rows16(&all, x, a.K, a.rows, ldx, moedc::kMpHalf)) return MOEDC_ERR_CUDA;
+    auto* k = moedc::matmul_pair_kernel<MODE>;
+    constexpr size_t kFixed = moedc::kMpStages * moedc::kMpStage;
+    static PerDevice raised;
+    if (!raise_smem_limit(raised, (const void*)k, (int)kFixed + (3 * MOEDC_MAX_E + 1) * 4)) return MOEDC_ERR_CUDA;
+    const int tile = a.gated ? moedc::kMpHalf : moedc::kMpTile;
+    const int64_t units = ((int64_t)a.rows / moedc::kMpTile + (a.E < a.rows ? a.E : a.rows)) * ((a.N + (int64_t)tile - 1) / tile);
+    const int pairs = sm_count() / 2;
+    clear_stale_error();
+    launch(k, 2 * (int)(units < pairs ? units : pairs), moedc::kMpThreads, kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a, w,
+           rows, all);
+    return launch_status();
+}
+
+}  // namespace
+
+int launch_mm_forward(const moedc::MmArgs& a, const void* x, int64_t ldx, const void* w, cudaStream_t stream)
+{
+    CUtensorMap map;
+    const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
+    const cuuint64_t size[4] = {K, parts, N, (cuuint64_t)a.E}, stride[3] = {2 * K * N, 2 * K, 2 * K * N * parts};
+    const cuuint32_t box[4] = {64, (cuuint32_t)parts, (cuuint32_t)(moedc::kMpHalf / parts), 1};
+    if (!tensor_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, CU_TENSOR_MAP_SWIZZLE_128B, w, 4, size, stride, box)) return MOEDC_ERR_CUDA;
+    return launch_mm_pair<moedc::kMmForward>(a, map, x, ldx, stream);
+}
+
+int launch_mm_dx(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* w, cudaStream_t stream)
+{
+    CUtensorMap map;
+    const cuuint64_t size[3] = {(cuuint64_t)a.N, (cuuint64_t)a.K, (cuuint64_t)a.E};
+    const cuuint64_t stride[2] = {2 * (cuuint64_t)a.N, 2 * (cuuint64_t)a.N * a.K};
+    const cuuint32_t box[3] = {64, 64, 1};
+    if (!tensor_map(&map, CU_TENSOR_MAP_DATA_TYPE_UINT16, CU_TENSOR_MAP_SWIZZLE_128B, w, 3, size, stride, box)) return MOEDC_ERR_CUDA;
+    return launch_mm_pair<moedc::kMmDx>(a, map, dout, ldd, stream);
+}
+
+}  // namespace moedc_host

@@ -11,4 +11,8 @@ namespace moedc_host {
 bool tensor_map(CUtensorMap* map, CUtensorMapDataType type, CUtensorMapSwizzle swizzle, const void* base, int dims,
                 const cuuint64_t* size, const cuuint64_t* stride, const cuuint32_t* box);
 
+// [rows][width] of 16-bit elements, ld elements from row to row, in boxes of 64 elements x
+// box_rows in the 128-byte swizzle (matmul_pair.cu).
+bool map_rows16(CUtensorMap* map, const void* base, int64_t width, int64_t rows, int64_t ld, int box_rows);
+
 }  // namespace moedc_host
