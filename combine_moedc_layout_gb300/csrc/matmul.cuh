@@ -110,6 +110,19 @@ __device__ __forceinline__ bool mm_chunks(const MmArgs& a, int chunk_rows, int t
     return over;
 }
 
+// Order of an expert's units: eight tiles of columns for one chunk of rows, for the next
+// chunk, then the next eight.  What is written at one time lies together in the rows of the
+// output (chunk after chunk for one tile: 167 us against 147 for 8192 x 4096 x 4096), and
+// operands of both sides are in L2 for their next use.
+constexpr int kMmTogether = 8;
+__device__ __forceinline__ void mm_order(int in, int tiles, int chunks, int& tile, int& chunk)
+{
+    const int group = in / (kMmTogether * chunks), rest = in - group * (kMmTogether * chunks);
+    const int width = min(kMmTogether, tiles - group * kMmTogether);
+    chunk = rest / width;
+    tile = group * kMmTogether + rest - chunk * width;
+}
+
 }  // namespace moedc
 
 namespace moedc_host {

@@ -40,9 +40,10 @@ __device__ __forceinline__ DwUnit dw_unit(const MmArgs& a, const int32_t* s_beg,
 {
     DwUnit u;
     u.e = unit / (tiles * mtiles);
-    const int in = unit - u.e * tiles * mtiles, t = in / mtiles;
+    int t, c;
+    mm_order(unit - u.e * tiles * mtiles, tiles, mtiles, t, c);
     u.n0 = t * kMmTile;
-    u.m0 = (in - t * mtiles) * kMmTile;
+    u.m0 = c * kMmTile;
     u.r0 = s_beg[u.e];
     u.m = s_end[u.e] - u.r0;
     u.ksteps = (u.m + kMmElems - 1) / kMmElems;

@@ -47,7 +47,8 @@ __device__ __forceinline__ MpUnit mp_unit(const MmArgs& a, const int32_t* s_pre,
         if ((int64_t)s_pre[mid] * tiles <= unit) lo = mid; else hi = mid - 1;
     }
     const int chunks = s_pre[lo + 1] - s_pre[lo];
-    const int in = unit - s_pre[lo] * tiles, t = in / chunks;   // chunks of one tile are neighbours
+    int t, c;
+    mm_order(unit - s_pre[lo] * tiles, tiles, chunks, t, c);
     // an expert's chunks are equal ones: chunks - 1 of them are fewer rows than it has, as a
     // chunk is at most 256 and all of its rows more than chunks - 1 times that
     const int rows = s_end[lo] - s_beg[lo];
@@ -55,7 +56,7 @@ __device__ __forceinline__ MpUnit mp_unit(const MmArgs& a, const int32_t* s_pre,
     MpUnit u;
     u.e = lo;
     u.n0 = t * (a.gated ? kMpHalf : kMpTile);
-    u.r0 = s_beg[lo] + (in - t * chunks) * size;
+    u.r0 = s_beg[lo] + c * size;
     u.m = min(size, s_end[lo] - u.r0);
     u.cols = (u.m + 31) / 32 * 32;
     return u;
@@ -191,6 +192,7 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                     } else {
                         tma_4d_pair(w, &wmap, s * kMpElems, 0, u.n0 + rank * kMpHalf, u.e, at);
                     }
+                    // one box, as each costs some 200 clocks: rows past the chunk's are of no account
                     tma_2d_pair(x, mine > 32 ? &allmap : &xmap, s * kMpElems, r0, at);
                 }
                 __syncwarp();

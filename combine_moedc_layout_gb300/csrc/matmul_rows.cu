@@ -41,11 +41,12 @@ __device__ __forceinline__ MrUnit mr_unit(const MmArgs& a, const int32_t* s_pre,
         if ((int64_t)s_pre[mid] * tiles <= unit) lo = mid; else hi = mid - 1;
     }
     const int chunks = s_pre[lo + 1] - s_pre[lo];
-    const int in = unit - s_pre[lo] * tiles, t = in / chunks;   // chunks of one tile are neighbours
+    int t, c;
+    mm_order(unit - s_pre[lo] * tiles, tiles, chunks, t, c);
     MrUnit u;
     u.e = lo;
     u.n0 = t * (a.gated ? kMrCols / 2 : kMrCols);
-    u.r0 = s_beg[lo] + (in - t * chunks) * kMrRows;
+    u.r0 = s_beg[lo] + c * kMrRows;
     u.m = min(kMrRows, s_end[lo] - u.r0);
     return u;
 }
@@ -236,7 +237,7 @@ matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
         bool stop = false;
         for (int unit = blockIdx.x; unit < units && !stop; unit += gridDim.x) {
             const MrUnit u = mr_unit(a, s_pre, s_beg, s_end, tiles, unit);
-            const int bytes = kMrCols * kMrGroup + (u.m + 31) / 32 * 32 * kMrGroup;
+            const int bytes = kMrCols * kMrGroup + (u.m > 32 ? kMrRows : 32) * kMrGroup;
             for (int g = 0; g < groups; ++g) {
                 const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
                 if (__any_sync(0xffffffffu, !ok)) {
@@ -251,9 +252,8 @@ matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                     tma_4d(st, &wmap, g * kMrGroup, u.n0, 0, u.e, bar);
                     tma_4d(st + kMrCols / 2 * kMrGroup, &wmap, g * kMrGroup, u.n0 + (a.gated ? 0 : kMrCols / 2), a.gated ? 1 : 0, u.e, bar);
                     st += kMrCols * kMrGroup;
-                    if (u.m == kMrRows) tma_2d(st, &allmap, g * kMrGroup, u.r0, bar);
-                    else
-                        for (int i = 0; i < u.m; i += 32) tma_2d(st + i * kMrGroup, &xmap, g * kMrGroup, u.r0 + i, bar);
+                    // one box, as each costs some 200 clocks: rows past the chunk's are of no account
+                    tma_2d(st, u.m > 32 ? &allmap : &xmap, g * kMrGroup, u.r0, bar);
                 }
                 __syncwarp();
                 ring.next(kMrStages);

@@ -55,7 +55,7 @@ __device__ __forceinline__ MsUnit ms_unit(const MmArgs& a, const int32_t* s_pre,
 
 __global__ void __launch_bounds__(kMsThreads, 1)
 matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap wmap,
-                     const __grid_constant__ CUtensorMap xmap)
+                     const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap allmap)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int64_t s_scan[kMsThreads / kWarp];
@@ -242,8 +242,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
         }
         if (bad) raise_status(a.status, MOEDC_ERR_EXPERT_RANGE);
     } else if (warp == 8) {
-        // ---- TMA: two tiles of weights; the tokens in sixteens, or four by four where they
-        // are gathered
+        // ---- TMA: two tiles of weights; the tokens, four by four where they are gathered
         MvRing ring;
         int issued = 0;
         bool stop = false;
@@ -255,7 +254,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
                 for (int i = 0; i < 4; ++i)
                     if (lane * 4 + i < u.m) t[i] = max(mm_x_row(a, u.r0 + lane * 4 + i), 0);
             }
-            const int bytes = 2 * kMsTile + (a.src ? (u.m + 3) / 4 * 4 : (u.m + 15) / 16 * 16) * kMsGroup;
+            const int bytes = 2 * kMsTile + (a.src ? (u.m + 3) / 4 * 4 : u.m > 16 ? kMsTokens : 16) * kMsGroup;
             for (int g = 0; g < groups; ++g) {
                 const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
                 if (__any_sync(0xffffffffu, !ok)) {
@@ -274,8 +273,9 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
                 st += 2 * kMsTile;
                 if (a.src) {
                     if (lane * 4 < u.m) tma_gather4(st + lane * 4 * kMsGroup, &xmap, g * kMsGroup, t[0], t[1], t[2], t[3], bar);
-                } else if (lane * 16 < u.m) {
-                    tma_2d(st + lane * 16 * kMsGroup, &xmap, g * kMsGroup, u.r0 + lane * 16, bar);
+                } else if (lane == 0) {
+                    // one box, as each costs some 200 clocks: rows past the chunk's are of no account
+                    tma_2d(st, u.m > 16 ? &allmap : &xmap, g * kMsGroup, u.r0, bar);
                 }
                 __syncwarp();
                 ring.next(kMsStages);
@@ -396,13 +396,14 @@ int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaS
 {
     constexpr auto kType = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     constexpr auto kSwizzle = CU_TENSOR_MAP_SWIZZLE_128B;
-    CUtensorMap wmap, xmap;
+    CUtensorMap wmap, xmap, all;   // x in boxes of 16 rows (gathered: one) and of 128
     const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
     const cuuint64_t xsize[2] = {K, (cuuint64_t)a.x_rows}, xstride[1] = {K};
-    const cuuint32_t xbox[2] = {128, a.src ? 1u : 16u};
+    const cuuint32_t xbox[2] = {128, a.src ? 1u : 16u}, allbox[2] = {128, moedc::kMsTokens};
     const cuuint64_t size[4] = {K, N, parts, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * parts};
     const cuuint32_t box[4] = {128, moedc::kMsRows, 1, 1};
-    if (!tensor_map(&xmap, kType, kSwizzle, x, 2, xsize, xstride, xbox) || !tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box))
+    if (!tensor_map(&xmap, kType, kSwizzle, x, 2, xsize, xstride, xbox) ||
+        !tensor_map(&all, kType, kSwizzle, x, 2, xsize, xstride, allbox) || !tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box))
         return MOEDC_ERR_CUDA;
     auto* k = moedc::matmul_stream_kernel;
     constexpr size_t kFixed = moedc::kMsStages * moedc::kMsStage + moedc::kMsFactorBufs * moedc::kMsFactors * sizeof(float);
@@ -413,7 +414,7 @@ int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaS
     const int blocks = sm_count();
     clear_stale_error();
     launch(k, (int)(units < blocks ? units : blocks), moedc::kMsThreads, kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a,
-           wmap, xmap);
+           wmap, xmap, all);
     return launch_status();
 }
 
