@@ -238,10 +238,7 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
                     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
                 }
-                if (lane == 0) {
-                    if (cleared) mbar_arrive_pair_release(ready + ring.slot, 0);
-                    else mbar_arrive_pair(ready + ring.slot, 0);
-                }
+                if (lane == 0) mbar_arrive_pair(ready + ring.slot, 0);
                 ring.next(kMmStages);
             }
         }

@@ -74,7 +74,7 @@ __device__ __forceinline__ uint32_t mp_round2(float lo, float hi, bool f16)
 template <int MODE>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMpThreads, 1)
 matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap wmap,
-                   const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap allmap)
+                   const __grid_constant__ BoxMaps xmaps)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int64_t s_scan[kMpThreads / kWarp];
@@ -170,7 +170,8 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
         for (int unit = pair; unit < units && !stop; unit += pairs) {
             const MpUnit u = mp_unit(a, s_pre, s_beg, s_end, tiles, unit);
             const int mine = u.cols / 2, r0 = u.r0 + rank * mine;
-            const int bytes = 2 * (kMpOperand + (mine > 32 ? kMpHalf : 32) * kMpBytes);   // of both blocks
+            const int box = (mine + 31) / 32;                             // in 32 rows
+            const int bytes = 2 * (kMpOperand + box * 32 * kMpBytes);     // of both blocks
             for (int s = 0; s < ksteps; ++s) {
                 const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
                 if (__any_sync(0xffffffffu, !ok)) {
@@ -192,8 +193,8 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                     } else {
                         tma_4d_pair(w, &wmap, s * kMpElems, 0, u.n0 + rank * kMpHalf, u.e, at);
                     }
-                    // one box, as each costs some 200 clocks: rows past the chunk's are of no account
-                    tma_2d_pair(x, mine > 32 ? &allmap : &xmap, s * kMpElems, r0, at);
+                    // rows past the chunk's are of no account
+                    tma_2d_pair(x, xmaps.by + (box - 1), s * kMpElems, r0, at);
                 }
                 __syncwarp();
                 ring.next(kMpStages);
@@ -268,12 +269,14 @@ bool map_rows16(CUtensorMap* map, const void* base, int64_t width, int64_t rows,
 
 namespace {
 
-// x: the rows, in boxes of 32 and of 128
+// x: the rows
 template <int MODE>
 int launch_mm_pair(const moedc::MmArgs& a, const CUtensorMap& w, const void* x, int64_t ldx, cudaStream_t stream)
 {
-    CUtensorMap rows, all;
-    if (!map_rows16(&rows, x, a.K, a.rows, ldx, 32) || !map_rows16(&all, x, a.K, a.rows, ldx, moedc::kMpHalf)) return MOEDC_ERR_CUDA;
+    moedc::BoxMaps rows{};
+    // a block's half of a chunk, in 32s
+    for (int i = 0; i < 4 && (i == 0 || a.rows > 64 * i); ++i)
+        if (!map_rows16(rows.by + i, x, a.K, a.rows, ldx, 32 * (i + 1))) return MOEDC_ERR_CUDA;
     auto* k = moedc::matmul_pair_kernel<MODE>;
     constexpr size_t kFixed = moedc::kMpStages * moedc::kMpStage;
     static PerDevice raised;
@@ -283,7 +286,7 @@ int launch_mm_pair(const moedc::MmArgs& a, const CUtensorMap& w, const void* x, 
     const int pairs = sm_count() / 2;
     clear_stale_error();
     launch(k, 2 * (int)(units < pairs ? units : pairs), moedc::kMpThreads, kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a, w,
-           rows, all);
+           rows);
     return launch_status();
 }
 

@@ -59,8 +59,8 @@ __device__ __forceinline__ float ld_scale(const float* p)
 }
 
 __global__ void __launch_bounds__(kMrThreads, 1)
-matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap xmap,
-                   const __grid_constant__ CUtensorMap allmap, const __grid_constant__ CUtensorMap wmap)
+matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap wmap,
+                   const __grid_constant__ BoxMaps xmaps)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int64_t s_scan[kMrThreads / kWarp];
@@ -237,7 +237,8 @@ matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
         bool stop = false;
         for (int unit = blockIdx.x; unit < units && !stop; unit += gridDim.x) {
             const MrUnit u = mr_unit(a, s_pre, s_beg, s_end, tiles, unit);
-            const int bytes = kMrCols * kMrGroup + (u.m > 32 ? kMrRows : 32) * kMrGroup;
+            const int box = (u.m + 31) / 32;   // in 32 rows
+            const int bytes = (kMrCols + box * 32) * kMrGroup;
             for (int g = 0; g < groups; ++g) {
                 const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
                 if (__any_sync(0xffffffffu, !ok)) {
@@ -252,8 +253,8 @@ matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                     tma_4d(st, &wmap, g * kMrGroup, u.n0, 0, u.e, bar);
                     tma_4d(st + kMrCols / 2 * kMrGroup, &wmap, g * kMrGroup, u.n0 + (a.gated ? 0 : kMrCols / 2), a.gated ? 1 : 0, u.e, bar);
                     st += kMrCols * kMrGroup;
-                    // one box, as each costs some 200 clocks: rows past the chunk's are of no account
-                    tma_2d(st, u.m > 32 ? &allmap : &xmap, g * kMrGroup, u.r0, bar);
+                    // rows past the chunk's are of no account
+                    tma_2d(st, xmaps.by + (box - 1), g * kMrGroup, u.r0, bar);
                 }
                 __syncwarp();
                 ring.next(kMrStages);
@@ -314,16 +315,17 @@ int launch_mm_rows(const moedc::MmArgs& a, const void* x, const void* w, cudaStr
 {
     constexpr auto kType = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     constexpr auto kSwizzle = CU_TENSOR_MAP_SWIZZLE_128B;
-    CUtensorMap xmap, all, wmap;   // x in boxes of 32 rows and of 128
+    CUtensorMap wmap;
+    moedc::BoxMaps xmaps{};
     const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
     const cuuint64_t xsize[2] = {K, (cuuint64_t)a.x_rows}, xstride[1] = {K};
-    const cuuint32_t xbox[2] = {128, 32}, allbox[2] = {128, moedc::kMrRows};
     const cuuint64_t size[4] = {K, N, parts, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * parts};
     const cuuint32_t box[4] = {128, moedc::kMrCols / 2, 1, 1};
-    if (!tensor_map(&xmap, kType, kSwizzle, x, 2, xsize, xstride, xbox) ||
-        !tensor_map(&all, kType, kSwizzle, x, 2, xsize, xstride, allbox) ||
-        !tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box))
-        return MOEDC_ERR_CUDA;
+    if (!tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box)) return MOEDC_ERR_CUDA;
+    for (int i = 0; i < 4; ++i) {
+        const cuuint32_t xbox[2] = {128, (cuuint32_t)(32 * (i + 1))};
+        if (!tensor_map(xmaps.by + i, kType, kSwizzle, x, 2, xsize, xstride, xbox)) return MOEDC_ERR_CUDA;
+    }
     auto* k = moedc::matmul_rows_kernel;
     constexpr size_t kFixed = moedc::kMrStages * moedc::kMrStage + moedc::kMrBuf;
     static PerDevice raised;
@@ -333,7 +335,7 @@ int launch_mm_rows(const moedc::MmArgs& a, const void* x, const void* w, cudaStr
     const int blocks = sm_count();
     clear_stale_error();
     launch(k, (int)(units < blocks ? units : blocks), moedc::kMrThreads, kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a,
-           xmap, all, wmap);
+           wmap, xmaps);
     return launch_status();
 }
 

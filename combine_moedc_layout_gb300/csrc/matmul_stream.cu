@@ -55,7 +55,7 @@ __device__ __forceinline__ MsUnit ms_unit(const MmArgs& a, const int32_t* s_pre,
 
 __global__ void __launch_bounds__(kMsThreads, 1)
 matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap wmap,
-                     const __grid_constant__ CUtensorMap xmap, const __grid_constant__ CUtensorMap allmap)
+                     const __grid_constant__ BoxMaps xmaps)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int64_t s_scan[kMsThreads / kWarp];
@@ -254,7 +254,8 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
                 for (int i = 0; i < 4; ++i)
                     if (lane * 4 + i < u.m) t[i] = max(mm_x_row(a, u.r0 + lane * 4 + i), 0);
             }
-            const int bytes = 2 * kMsTile + (a.src ? (u.m + 3) / 4 * 4 : u.m > 16 ? kMsTokens : 16) * kMsGroup;
+            const int box = u.m <= 16 ? 0 : u.m <= 32 ? 1 : u.m <= 64 ? 2 : 3;   // 16 << box rows
+            const int bytes = 2 * kMsTile + (a.src ? (u.m + 3) / 4 * 4 : 16 << box) * kMsGroup;
             for (int g = 0; g < groups; ++g) {
                 const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
                 if (__any_sync(0xffffffffu, !ok)) {
@@ -272,10 +273,10 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
                 __syncwarp();
                 st += 2 * kMsTile;
                 if (a.src) {
-                    if (lane * 4 < u.m) tma_gather4(st + lane * 4 * kMsGroup, &xmap, g * kMsGroup, t[0], t[1], t[2], t[3], bar);
+                    if (lane * 4 < u.m) tma_gather4(st + lane * 4 * kMsGroup, xmaps.by, g * kMsGroup, t[0], t[1], t[2], t[3], bar);
                 } else if (lane == 0) {
-                    // one box, as each costs some 200 clocks: rows past the chunk's are of no account
-                    tma_2d(st, u.m > 16 ? &allmap : &xmap, g * kMsGroup, u.r0, bar);
+                    // rows past the chunk's are of no account
+                    tma_2d(st, xmaps.by + box, g * kMsGroup, u.r0, bar);
                 }
                 __syncwarp();
                 ring.next(kMsStages);
@@ -396,15 +397,18 @@ int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaS
 {
     constexpr auto kType = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     constexpr auto kSwizzle = CU_TENSOR_MAP_SWIZZLE_128B;
-    CUtensorMap wmap, xmap, all;   // x in boxes of 16 rows (gathered: one) and of 128
+    CUtensorMap wmap;
+    moedc::BoxMaps xmaps{};
     const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
     const cuuint64_t xsize[2] = {K, (cuuint64_t)a.x_rows}, xstride[1] = {K};
-    const cuuint32_t xbox[2] = {128, a.src ? 1u : 16u}, allbox[2] = {128, moedc::kMsTokens};
     const cuuint64_t size[4] = {K, N, parts, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * parts};
     const cuuint32_t box[4] = {128, moedc::kMsRows, 1, 1};
-    if (!tensor_map(&xmap, kType, kSwizzle, x, 2, xsize, xstride, xbox) ||
-        !tensor_map(&all, kType, kSwizzle, x, 2, xsize, xstride, allbox) || !tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box))
-        return MOEDC_ERR_CUDA;
+    if (!tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box)) return MOEDC_ERR_CUDA;
+    // gathered rows: one map, a row high; else as many as the rows can need
+    for (int i = 0; i < 4 && (i == 0 || (!a.src && a.rows > 8 << i)); ++i) {
+        const cuuint32_t xbox[2] = {128, a.src ? 1u : 16u << i};
+        if (!tensor_map(xmaps.by + i, kType, kSwizzle, x, 2, xsize, xstride, xbox)) return MOEDC_ERR_CUDA;
+    }
     auto* k = moedc::matmul_stream_kernel;
     constexpr size_t kFixed = moedc::kMsStages * moedc::kMsStage + moedc::kMsFactorBufs * moedc::kMsFactors * sizeof(float);
     static PerDevice raised;
@@ -414,7 +418,7 @@ int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaS
     const int blocks = sm_count();
     clear_stale_error();
     launch(k, (int)(units < blocks ? units : blocks), moedc::kMsThreads, kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a,
-           wmap, xmap, all);
+           wmap, xmaps);
     return launch_status();
 }
 

@@ -81,20 +81,15 @@ __device__ __forceinline__ void cluster_sync()
 {
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
-// One arrival at the barrier of that name in block `rank` of the cluster.  What it orders
-// is copies and tensor-memory accesses, which their own completion and fences order; with
-// the release of a cluster's scope spelled out an arrival waits on a memory barrier of some
+// One arrival at the barrier of that name in block `rank` of the cluster.  What it announces
+// is copies, tensor-memory accesses, and stores to the arriving block's own shared memory
+// behind a proxy fence, all of which have their own completion or fence before it; with the
+// release of a cluster's scope spelled out an arrival waits on a memory barrier of some
 // 1.2 us.
 __device__ __forceinline__ void mbar_arrive_pair(uint64_t* b, int rank)
 {
     asm volatile("{\n .reg .b32 at;\n mapa.shared::cluster.u32 at, %0, %1;\n"
                  " mbarrier.arrive.shared::cluster.b64 _, [at];\n}\n" ::"r"(smem_u32(b)), "r"(rank) : "memory");
-}
-// the same for plain stores to shared memory before it
-__device__ __forceinline__ void mbar_arrive_pair_release(uint64_t* b, int rank)
-{
-    asm volatile("{\n .reg .b32 at;\n mapa.shared::cluster.u32 at, %0, %1;\n"
-                 " mbarrier.arrive.release.cluster.shared::cluster.b64 _, [at];\n}\n" ::"r"(smem_u32(b)), "r"(rank) : "memory");
 }
 __device__ __forceinline__ void tc_alloc_pair(uint32_t* at, uint32_t columns)
 {

@@ -4,6 +4,16 @@
 
 #include "common.cuh"
 
+namespace moedc {
+
+// One matrix in boxes of four heights: a stage's rows are one copy, as each costs some 200
+// clocks beside its bytes.
+struct BoxMaps {
+    CUtensorMap by[4];
+};
+
+}  // namespace moedc
+
 namespace moedc_host {
 
 // A tiled map of `dims` dimensions, the innermost first; stride in bytes, of all but the
