@@ -142,29 +142,26 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
         }
     } else if (warp == 8) {
         // ---- TMA: this block's rows of the left operand, its half of the right one
+        // (one lane waits and issues)
         MvRing ring;
         int issued = 0;
-        bool stop = false;
+        bool stop = !tc_elect();
         for (int unit = pair; unit < units && !stop; unit += pairs) {
             const DwUnit u = dw_unit(a, s_beg, s_end, tiles, mtiles, unit);
             for (int s = 0; s < u.ksteps; ++s) {
-                const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
-                if (__any_sync(0xffffffffu, !ok)) {
+                if (!mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort)) {
                     stop = true;
                     break;
                 }
                 uint8_t* left = smem + ring.slot * kMmStage;
                 uint8_t* right = left + kMmOperand;
                 uint64_t* bar = full + ring.slot;
-                if (lane == 0) {
-                    mbar_arrive_expect(bar, kMmStage);
+                mbar_arrive_expect(bar, kMmStage);
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        tma_2d(left + h * (kMmOperand / 2), &lmap, u.m0 + rank * kMmHalf + h * 64, u.r0 + s * kMmElems, bar);
-                        tma_2d(right + h * (kMmOperand / 2), &rmap, u.n0 + rank * kMmHalf + h * 64, u.r0 + s * kMmElems, bar);
-                    }
+                for (int h = 0; h < 2; ++h) {
+                    tma_2d(left + h * (kMmOperand / 2), &lmap, u.m0 + rank * kMmHalf + h * 64, u.r0 + s * kMmElems, bar);
+                    tma_2d(right + h * (kMmOperand / 2), &rmap, u.n0 + rank * kMmHalf + h * 64, u.r0 + s * kMmElems, bar);
                 }
-                __syncwarp();
                 ring.next(kMmStages);
                 ++issued;
             }

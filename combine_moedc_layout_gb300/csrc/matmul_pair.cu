@@ -164,39 +164,36 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
         }
     } else if (warp == 8) {
         // ---- TMA: this block's weight rows, its half of the tokens
+        // (one lane waits and issues: with the warp together 161 us against 150 for 8192 x 4096 x 4096)
         MvRing ring;
         int issued = 0;
-        bool stop = false;
+        bool stop = !tc_elect();
         for (int unit = pair; unit < units && !stop; unit += pairs) {
             const MpUnit u = mp_unit(a, s_pre, s_beg, s_end, tiles, unit);
             const int mine = u.cols / 2, r0 = u.r0 + rank * mine;
             const int box = (mine + 31) / 32;                             // in 32 rows
             const int bytes = 2 * (kMpOperand + box * 32 * kMpBytes);     // of both blocks
             for (int s = 0; s < ksteps; ++s) {
-                const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
-                if (__any_sync(0xffffffffu, !ok)) {
+                if (!mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort)) {
                     stop = true;
                     break;
                 }
                 uint8_t* w = smem + ring.slot * kMpStage;
                 uint8_t* x = w + kMpOperand;
-                if (lane == 0) {
-                    const uint32_t at = cluster_addr(full + ring.slot, 0);
-                    if (rank == 0) mbar_arrive_expect(full + ring.slot, bytes);
-                    if constexpr (MODE == kMmDx) {
+                const uint32_t at = cluster_addr(full + ring.slot, 0);
+                if (rank == 0) mbar_arrive_expect(full + ring.slot, bytes);
+                if constexpr (MODE == kMmDx) {
 #pragma unroll
-                        for (int h = 0; h < 2; ++h)
-                            tma_3d_pair(w + h * (kMpOperand / 2), &wmap, u.n0 + rank * kMpHalf + h * 64, s * kMpElems, u.e, at);
-                    } else if (a.gated) {
-                        // [E][N][gate or up][K]
-                        tma_4d_pair(w, &wmap, s * kMpElems, 0, u.n0 + rank * (kMpHalf / 2), u.e, at);
-                    } else {
-                        tma_4d_pair(w, &wmap, s * kMpElems, 0, u.n0 + rank * kMpHalf, u.e, at);
-                    }
-                    // rows past the chunk's are of no account
-                    tma_2d_pair(x, xmaps.by + (box - 1), s * kMpElems, r0, at);
+                    for (int h = 0; h < 2; ++h)
+                        tma_3d_pair(w + h * (kMpOperand / 2), &wmap, u.n0 + rank * kMpHalf + h * 64, s * kMpElems, u.e, at);
+                } else if (a.gated) {
+                    // [E][N][gate or up][K]
+                    tma_4d_pair(w, &wmap, s * kMpElems, 0, u.n0 + rank * (kMpHalf / 2), u.e, at);
+                } else {
+                    tma_4d_pair(w, &wmap, s * kMpElems, 0, u.n0 + rank * kMpHalf, u.e, at);
                 }
-                __syncwarp();
+                // rows past the chunk's are of no account
+                tma_2d_pair(x, xmaps.by + (box - 1), s * kMpElems, r0, at);
                 ring.next(kMpStages);
                 ++issued;
             }

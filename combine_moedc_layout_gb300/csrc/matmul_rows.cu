@@ -232,31 +232,28 @@ matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
         }
     } else if (warp == 8) {
         // ---- TMA
+        // (one lane waits and issues)
         MvRing ring;
         int issued = 0;
-        bool stop = false;
+        bool stop = !tc_elect();
         for (int unit = blockIdx.x; unit < units && !stop; unit += gridDim.x) {
             const MrUnit u = mr_unit(a, s_pre, s_beg, s_end, tiles, unit);
             const int box = (u.m + 31) / 32;   // in 32 rows
             const int bytes = (kMrCols + box * 32) * kMrGroup;
             for (int g = 0; g < groups; ++g) {
-                const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
-                if (__any_sync(0xffffffffu, !ok)) {
+                if (!mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort)) {
                     stop = true;
                     break;
                 }
                 uint8_t* st = smem + ring.slot * kMrStage;
                 uint64_t* bar = full + ring.slot;
-                if (lane == 0) {
-                    mbar_arrive_expect(bar, bytes);
-                    // [E][1 or 2][N][K]
-                    tma_4d(st, &wmap, g * kMrGroup, u.n0, 0, u.e, bar);
-                    tma_4d(st + kMrCols / 2 * kMrGroup, &wmap, g * kMrGroup, u.n0 + (a.gated ? 0 : kMrCols / 2), a.gated ? 1 : 0, u.e, bar);
-                    st += kMrCols * kMrGroup;
-                    // rows past the chunk's are of no account
-                    tma_2d(st, xmaps.by + (box - 1), g * kMrGroup, u.r0, bar);
-                }
-                __syncwarp();
+                mbar_arrive_expect(bar, bytes);
+                // [E][1 or 2][N][K]
+                tma_4d(st, &wmap, g * kMrGroup, u.n0, 0, u.e, bar);
+                tma_4d(st + kMrCols / 2 * kMrGroup, &wmap, g * kMrGroup, u.n0 + (a.gated ? 0 : kMrCols / 2), a.gated ? 1 : 0, u.e, bar);
+                st += kMrCols * kMrGroup;
+                // rows past the chunk's are of no account
+                tma_2d(st, xmaps.by + (box - 1), g * kMrGroup, u.r0, bar);
                 ring.next(kMrStages);
                 ++issued;
             }

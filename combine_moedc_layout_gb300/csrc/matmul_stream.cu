@@ -243,46 +243,46 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
         if (bad) raise_status(a.status, MOEDC_ERR_EXPERT_RANGE);
     } else if (warp == 8) {
         // ---- TMA: two tiles of weights; the tokens, four by four where they are gathered
+        // (one lane waits and issues, but where each lane gathers four of the rows)
         MvRing ring;
         int issued = 0;
-        bool stop = false;
+        const bool gather = a.src != nullptr, first = gather ? lane == 0 : tc_elect();
+        bool stop = !gather && !first;
         for (int unit = blockIdx.x; unit < units && !stop; unit += gridDim.x) {
             const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
             int t[4] = {0, 0, 0, 0};
-            if (a.src) {
+            if (gather) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (lane * 4 + i < u.m) t[i] = max(mm_x_row(a, u.r0 + lane * 4 + i), 0);
             }
             const int box = u.m <= 16 ? 0 : u.m <= 32 ? 1 : u.m <= 64 ? 2 : 3;   // 16 << box rows
-            const int bytes = 2 * kMsTile + (a.src ? (u.m + 3) / 4 * 4 : 16 << box) * kMsGroup;
+            const int bytes = 2 * kMsTile + (gather ? (u.m + 3) / 4 * 4 : 16 << box) * kMsGroup;
             for (int g = 0; g < groups; ++g) {
-                const bool ok = mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
-                if (__any_sync(0xffffffffu, !ok)) {
-                    stop = true;
-                    break;
-                }
+                stop = !mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
+                if (gather) stop = __any_sync(0xffffffffu, stop);
+                if (stop) break;
                 uint8_t* st = smem + ring.slot * kMsStage;
                 uint64_t* bar = full + ring.slot;
-                if (lane == 0) {
+                if (first) {
                     mbar_arrive_expect(bar, bytes);
                     // [E][1 or 2][N][K]
                     tma_4d(st, &wmap, g * kMsGroup, u.n0, 0, u.e, bar);
                     tma_4d(st + kMsTile, &wmap, g * kMsGroup, u.n0 + (a.gated ? 0 : kMsRows), a.gated ? 1 : 0, u.e, bar);
-                }
-                __syncwarp();
-                st += 2 * kMsTile;
-                if (a.src) {
-                    if (lane * 4 < u.m) tma_gather4(st + lane * 4 * kMsGroup, xmaps.by, g * kMsGroup, t[0], t[1], t[2], t[3], bar);
-                } else if (lane == 0) {
                     // rows past the chunk's are of no account
-                    tma_2d(st, xmaps.by + box, g * kMsGroup, u.r0, bar);
+                    if (!gather) tma_2d(st + 2 * kMsTile, xmaps.by + box, g * kMsGroup, u.r0, bar);
                 }
-                __syncwarp();
+                if (gather) {
+                    __syncwarp();
+                    if (lane * 4 < u.m)
+                        tma_gather4(st + 2 * kMsTile + lane * 4 * kMsGroup, xmaps.by, g * kMsGroup, t[0], t[1], t[2], t[3], bar);
+                    __syncwarp();
+                }
                 ring.next(kMsStages);
                 ++issued;
             }
         }
+        __syncwarp();
         // no copy may land after the block has gone, whatever else gave up
         for (int n = max(0, issued - kMsStages); n < issued; ++n) {
             volatile int alone = 0;
