@@ -3,10 +3,9 @@
 //
 // Bound by HBM: every element is read once and kept in registers between the maximum and
 // the codes.  A thread owns 16 neighbouring channels, so that eight lanes hold a group of
-// 128 and store 128 bytes of codes; for blocks, 256 threads hold the 128 rows, each of them
-// four.
-#include "lm_common.cuh"
-#include "dispatch_item.cuh"
+// 128 and store 128 bytes of codes; for blocks, 512 threads hold the 128 rows, each of them
+// two.  The quotients, not HBM, were the bound while each was a division.
+#include "quotient.cuh"
 
 namespace moedc {
 
@@ -27,6 +26,16 @@ template <typename T> struct Quant16 {
     }
     __device__ __forceinline__ float top() const
     {
+        if constexpr (sizeof(T) == 2) {
+            // two at a time; the maximum leaves NaN out as fmaxf does
+            using T2 = typename std::conditional<std::is_same<T, __half>::value, __half2, __nv_bfloat162>::type;
+            const uint32_t w[8] = {u[0].x, u[0].y, u[0].z, u[0].w, u[1].x, u[1].y, u[1].z, u[1].w};
+            T2 m = __habs2(*reinterpret_cast<const T2*>(w));
+#pragma unroll
+            for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const T2*>(w + i)));
+            // (a 0 for the first one's NaN)
+            return fmaxf(fmaxf(0.0f, to_f32(m.x)), to_f32(m.y));
+        }
         float t = 0.0f;
 #pragma unroll
         for (int i = 0; i < units; ++i) {
@@ -39,6 +48,8 @@ template <typename T> struct Quant16 {
     }
     __device__ __forceinline__ uint4 codes(float sc) const
     {
+        using Q = Quotient<sizeof(T) == 4 ? 2 : 1>;
+        const Q by = Q::by(sc);
         uint32_t q[4];
 #pragma unroll
         for (int i = 0; i < units; ++i) {
@@ -46,7 +57,7 @@ template <typename T> struct Quant16 {
             Unit<T, per>::widen(u[i], f);
 #pragma unroll
             for (int j = 0; j < per; j += 4)
-                q[(i * per + j) / 4] = quant_pair(f[j], f[j + 1], sc) | quant_pair(f[j + 2], f[j + 3], sc) << 16;
+                q[(i * per + j) / 4] = by.codes(f[j], f[j + 1]) | by.codes(f[j + 2], f[j + 3]) << 16;
         }
         return make_uint4(q[0], q[1], q[2], q[3]);
     }
@@ -83,12 +94,15 @@ __global__ void __launch_bounds__(256) quant_rows_kernel(const T* __restrict__ x
     }
 }
 
+constexpr int kQuantBlock = 512;
+
 template <typename T>
-__global__ void __launch_bounds__(256) quant_blocks_kernel(const T* __restrict__ x, int64_t ld, int64_t blocks, int rows,
+__global__ void __launch_bounds__(kQuantBlock, sizeof(T) == 4 ? 2 : 3) quant_blocks_kernel(const T* __restrict__ x, int64_t ld, int64_t blocks, int rows,
                                                            int Kd, uint8_t* __restrict__ codes, float* __restrict__ scales)
 {
     pdl_enter();
-    __shared__ float s_top[2][8];
+    constexpr int kRows = kQuantBlock / 8, kEach = 128 / kRows;   // rows at once, of a thread
+    __shared__ float s_top[2][kQuantBlock / kWarp];
     const int groups = Kd / 128, down = (rows + 127) / 128;
     int turn = 0;
     for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x, turn ^= 1) {
@@ -97,25 +111,25 @@ __global__ void __launch_bounds__(256) quant_blocks_kernel(const T* __restrict__
         const int64_t e = rest / down;
         const int r0 = (int)(rest - e * down) * 128 + threadIdx.x / 8;
         const int c = g * 128 + threadIdx.x % 8 * 16;
-        Quant16<T> v[4];
+        Quant16<T> v[kEach];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            if (r0 + 32 * i < rows) v[i].load(x + (e * rows + r0 + 32 * i) * ld + c);
+        for (int i = 0; i < kEach; ++i) {
+            if (r0 + kRows * i < rows) v[i].load(x + (e * rows + r0 + kRows * i) * ld + c);
             else v[i].clear();
         }
         float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) top = fmaxf(top, v[i].top());
+        for (int i = 0; i < kEach; ++i) top = fmaxf(top, v[i].top());
         top = warp_max(top);
         // two sets in turn: a warp may be at the next block while another reads this one's
         if (threadIdx.x % kWarp == 0) s_top[turn][threadIdx.x / kWarp] = top;
         __syncthreads();
 #pragma unroll
-        for (int w = 0; w < 8; ++w) top = fmaxf(top, s_top[turn][w]);
+        for (int w = 0; w < kQuantBlock / kWarp; ++w) top = fmaxf(top, s_top[turn][w]);
         const float sc = __fdiv_rn(fmaxf(top, 1e-4f), 448.0f);
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
-            if (r0 + 32 * i < rows) *reinterpret_cast<uint4*>(codes + (e * rows + r0 + 32 * i) * Kd + c) = v[i].codes(sc);
+        for (int i = 0; i < kEach; ++i)
+            if (r0 + kRows * i < rows) *reinterpret_cast<uint4*>(codes + (e * rows + r0 + kRows * i) * Kd + c) = v[i].codes(sc);
         if (threadIdx.x == 0) scales[b] = sc;
     }
 }
@@ -137,7 +151,7 @@ void launch_quant(const void* x, int64_t ld, int E, int rows, int Kd, int block_
                static_cast<uint8_t*>(codes), scales);
     } else {
         const int64_t blocks = (int64_t)E * ((rows + 127) / 128) * (Kd / 128), most = 16 * sms;
-        launch(moedc::quant_blocks_kernel<T>, (int)(blocks < most ? blocks : most), 256, 0, stream, p, ld, blocks, rows, Kd,
+        launch(moedc::quant_blocks_kernel<T>, (int)(blocks < most ? blocks : most), moedc::kQuantBlock, 0, stream, p, ld, blocks, rows, Kd,
                static_cast<uint8_t*>(codes), scales);
     }
 }

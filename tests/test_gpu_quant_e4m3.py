@@ -1,4 +1,7 @@
 """Rows and blocks to e4m3: bit for bit the rule in binary32, and what dispatch writes."""
+import os
+import subprocess
+
 import pytest
 import torch
 
@@ -101,3 +104,25 @@ def test_reused_buffers_empty_and_refused():
     for bad in (x[:, :200], x.flatten()[1:1 + 768].view(3, 256), x[:, 1:129]):
         with pytest.raises(moedc.MoedcError):
             moedc.quant_e4m3(bad)
+
+
+def test_quotients_are_the_divisions(tmp_path):
+    """Every mantissa of a divisor with every one of a bf16 and an f16 dividend, and 2^33
+    binary32 pairs; the program is built here, not into the library."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    root = os.path.dirname(here)
+    exe = str(tmp_path / "quotient_sweep")
+    subprocess.run(["nvcc", "-gencode", "arch=compute_103a,code=sm_103a", "-O3", "-std=c++17",
+                    "--expt-relaxed-constexpr", "-I" + os.path.join(root, "include"),
+                    "-I" + os.path.join(root, "combine_moedc_layout_gb300", "csrc"),
+                    os.path.join(here, "cuda", "quotient_sweep.cu"), "-o", exe], check=True, capture_output=True)
+    done = subprocess.run([exe], capture_output=True, text=True, timeout=60)
+    assert done.returncode == 0, done.stdout + done.stderr
+
+
+def test_zeros_keep_their_sign_as_in_dispatch():
+    x = torch.tensor([0.0, -0.0, 1e-30, -1e-30] * 32).to(torch.bfloat16).reshape(1, 128).cuda()
+    lay = moedc.layout(torch.zeros(1, 1, dtype=torch.int32).cuda(), 1, 1, 1)
+    recv, _, _ = moedc.dispatch(x, torch.zeros(1, 1, dtype=torch.int32).cuda(), lay, 1, 1, moedc.FP8_E4M3)
+    assert torch.equal(moedc.quant_e4m3(x)[0].view(torch.uint8), recv[0].view(torch.uint8))
+    assert torch.equal(moedc.quant_e4m3(x, block_rows=128)[0].view(torch.uint8), recv[0].view(torch.uint8))
