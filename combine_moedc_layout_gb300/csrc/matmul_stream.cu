@@ -12,6 +12,10 @@
 // into 128 registers; the factors come from shared memory, where one warp puts them four
 // groups ahead.
 //
+// Where there are too few tiles for the SMs, a cluster of blocks shares one: each block takes
+// a part of the channels, in fours of groups, and sends its sums to the first one's shared
+// memory, which adds them in the blocks' order.
+//
 // Warps: 0-7 epilogue (0-3 the first 64 tokens, 4-7 the others), 8 TMA, 9 MMA, 10 factors.
 #include "matmul.cuh"
 #include "tcgen05.cuh"
@@ -54,7 +58,7 @@ __device__ __forceinline__ MsUnit ms_unit(const MmArgs& a, const int32_t* s_pre,
 }
 
 __global__ void __launch_bounds__(kMsThreads, 1)
-matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap wmap,
+matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_constant__ CUtensorMap wmap,
                      const __grid_constant__ BoxMaps xmaps)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -68,6 +72,10 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     const int tile_n = a.gated ? kMsRows : 2 * kMsRows;
     const int tiles = (a.N + tile_n - 1) / tile_n, groups = a.K / kMsGroup;
+    // with parts > 1 a cluster has one tile at most
+    const int part = parts > 1 ? cluster_rank() : 0, first_unit = blockIdx.x / parts, unit_step = gridDim.x / parts;
+    const int quads_all = (groups + 3) / 4;
+    const int g_beg = quads_all * part / parts * 4, g_end = min(quads_all * (part + 1) / parts * 4, groups);
     float* s_factors = reinterpret_cast<float*>(smem + kMsStages * kMsStage);
     int32_t* s_pre = reinterpret_cast<int32_t*>(s_factors + kMsFactorBufs * kMsFactors);
     int32_t *s_beg = s_pre + a.E + 1, *s_end = s_beg + a.E;
@@ -110,7 +118,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
         const uint32_t d0 = tmem + ((uint32_t)(quad * kWarp) << 16) + j0;
         MvRing accs, facs;
         bool bad = false;
-        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        for (int unit = first_unit; unit < units; unit += unit_step) {
             const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
             const int mine = u.m - j0;                      // tokens of this warp
             float2 acc[2][kMsHalf / 2];
@@ -118,7 +126,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
             for (int t = 0; t < 2; ++t)
 #pragma unroll
                 for (int j = 0; j < kMsHalf / 2; ++j) acc[t][j] = make_float2(0.0f, 0.0f);
-            for (int g = 0; g < groups; ++g) {
+            for (int g = g_beg; g < g_end; ++g) {
                 if (g % 4 == 0) mbar_wait_inline(f_full + facs.slot, facs.phase, &s_abort);
                 mbar_wait_inline(d_full + accs.slot, accs.phase, &s_abort);
                 __syncwarp();
@@ -150,10 +158,39 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
                 __syncwarp();
                 if (lane == 0) {
                     mbar_arrive(d_empty + accs.slot);
-                    if (g % 4 == 3 || g == groups - 1) mbar_arrive(f_empty + facs.slot);
+                    if (g % 4 == 3 || g == g_end - 1) mbar_arrive(f_empty + facs.slot);
                 }
                 accs.next(2);
-                if (g % 4 == 3 || g == groups - 1) facs.next(kMsFactorBufs);
+                if (g % 4 == 3 || g == g_end - 1) facs.next(kMsFactorBufs);
+            }
+            if (parts > 1) {
+                cluster_sync();     // no block's products read its stages any more
+                float* sums = reinterpret_cast<float*>(smem);   // [part - 1][tile][token][row]
+                const int cols = (u.m + 15) / 16 * 16;
+                if (part > 0) {
+                    const uint32_t to = cluster_addr(sums + ((part - 1) * 2 * cols + j0) * kMsRows + row, 0);
+#pragma unroll
+                    for (int j = 0; j < kMsHalf; ++j) {
+                        if (j >= mine) break;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t)
+                            st_cluster(to + (t * cols + j) * (kMsRows * 4), j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x);
+                    }
+                }
+                cluster_sync();
+                if (part > 0) continue;
+                for (int p = 1; p < parts; ++p) {
+                    const float* from = sums + ((p - 1) * 2 * cols + j0) * kMsRows + row;
+#pragma unroll
+                    for (int j = 0; j < kMsHalf; ++j) {
+                        if (j >= mine) break;
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            float& s = j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x;
+                            s += from[(t * cols + j) * kMsRows];
+                        }
+                    }
+                }
             }
             // tokens that src leads outside of x: zeros
             if (a.src) {
@@ -248,7 +285,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
         int issued = 0;
         const bool gather = a.src != nullptr, first = gather ? lane == 0 : tc_elect();
         bool stop = !gather && !first;
-        for (int unit = blockIdx.x; unit < units && !stop; unit += gridDim.x) {
+        for (int unit = first_unit; unit < units && !stop; unit += unit_step) {
             const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
             int t[4] = {0, 0, 0, 0};
             if (gather) {
@@ -258,7 +295,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
             }
             const int box = u.m <= 16 ? 0 : u.m <= 32 ? 1 : u.m <= 64 ? 2 : 3;   // 16 << box rows
             const int bytes = 2 * kMsTile + (gather ? (u.m + 3) / 4 * 4 : 16 << box) * kMsGroup;
-            for (int g = 0; g < groups; ++g) {
+            for (int g = g_beg; g < g_end; ++g) {
                 stop = !mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
                 if (gather) stop = __any_sync(0xffffffffu, stop);
                 if (stop) break;
@@ -294,11 +331,11 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
         const bool leader = tc_elect();
         MvRing ring, accs;
         int k = 0;
-        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        for (int unit = first_unit; unit < units; unit += unit_step) {
             const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
             // columns: as many tokens as there are, by 16
             const uint32_t idesc = (1u << 4) | ((uint32_t)((u.m + 15) / 16 * 2) << 17) | ((uint32_t)(kMsRows / 16) << 24);
-            for (int g = 0; g < groups; ++g) {
+            for (int g = g_beg; g < g_end; ++g) {
                 if (k++ >= 2) mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
                 mbar_wait_warp(full + ring.slot, ring.phase, &s_abort);
                 tc_fence_after();
@@ -330,7 +367,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
         MvRing facs;
         const bool quads = a.xs_g == 1 && groups % 4 == 0 && reinterpret_cast<uintptr_t>(a.xs) % 16 == 0;
         const int blocks = (a.N + 127) / 128;
-        for (int unit = blockIdx.x; unit < units; unit += gridDim.x) {
+        for (int unit = first_unit; unit < units; unit += unit_step) {
             const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
             const float* xs[4];
 #pragma unroll
@@ -361,8 +398,8 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
                     }
                 }
             };
-            load(0);
-            for (int g0 = 0; g0 < groups; g0 += 4) {
+            load(g_beg);
+            for (int g0 = g_beg; g0 < g_end; g0 += 4) {
                 mbar_wait_warp(f_empty + facs.slot, facs.phase ^ 1, &s_abort);
                 float* f = s_factors + facs.slot * kMsFactors + lane;
 #pragma unroll
@@ -380,6 +417,12 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ C
                 load(min(g0 + 4, groups - 1));
             }
         }
+    }
+    if (parts > 1 && (warp >= 8 || first_unit >= units)) {
+        // (the epilogue's warps are at theirs above)
+        __syncwarp();
+        cluster_sync();
+        cluster_sync();
     }
     tc_fence_before();
     __syncthreads();
@@ -399,9 +442,9 @@ int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaS
     constexpr auto kSwizzle = CU_TENSOR_MAP_SWIZZLE_128B;
     CUtensorMap wmap;
     moedc::BoxMaps xmaps{};
-    const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
+    const cuuint64_t K = a.K, N = a.N, both = a.gated ? 2 : 1;
     const cuuint64_t xsize[2] = {K, (cuuint64_t)a.x_rows}, xstride[1] = {K};
-    const cuuint64_t size[4] = {K, N, parts, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * parts};
+    const cuuint64_t size[4] = {K, N, both, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * both};
     const cuuint32_t box[4] = {128, moedc::kMsRows, 1, 1};
     if (!tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box)) return MOEDC_ERR_CUDA;
     // gathered rows: one map, a row high; else as many as the rows can need
@@ -416,9 +459,16 @@ int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaS
     const int tile = a.gated ? moedc::kMsRows : 2 * moedc::kMsRows;
     const int64_t units = ((int64_t)a.rows / moedc::kMsTokens + (a.E < a.rows ? a.E : a.rows)) * ((a.N + (int64_t)tile - 1) / tile);
     const int blocks = sm_count();
+    // parts: as many as there are SMs for, eight groups each at least, their sums in the stages
+    int parts = 1;
+    const int64_t most = a.rows < moedc::kMsTokens ? a.rows : moedc::kMsTokens;
+    const int64_t sums = (most + 15) / 16 * 16 * 2 * moedc::kMsRows * sizeof(float);
+    while (parts < 8 && units * (parts + 1) <= blocks && a.K / moedc::kMsGroup >= 8 * (parts + 1) &&
+           parts * sums <= moedc::kMsStages * moedc::kMsStage)
+        ++parts;
     clear_stale_error();
-    launch(k, (int)(units < blocks ? units : blocks), moedc::kMsThreads, kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a,
-           wmap, xmaps);
+    launch_cluster(k, parts, (int)(units * parts < blocks ? units * parts : blocks / parts * parts), moedc::kMsThreads,
+                   kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a, parts, wmap, xmaps);
     return launch_status();
 }
 

@@ -96,7 +96,7 @@ def test_packed_rows(counts, N, Kd, align, swiglu, out, many):
         assert torch.equal(p[mine].float(), q[mine].float())
 
 
-@pytest.mark.parametrize("T,E,K", [(1, 8, 2), (9, 12, 3), (130, 4, 2), (600, 3, 1)])
+@pytest.mark.parametrize("T,E,K", [(1, 2, 1), (1, 8, 2), (9, 12, 3), (130, 4, 2), (600, 3, 1)])
 def test_gathered_rows(T, E, K):
     g = torch.Generator().manual_seed(T)
     N, Kd = 256, 384
@@ -223,6 +223,33 @@ def test_nan_stays_in_its_row_and_column():
     assert torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], want[~nan])
     codes, _ = moedc.matmul_e4m3(x, xs, w[0], ws[0], out_dtype=moedc.FP8_E4M3)
     assert torch.equal(torch.isnan(codes.float()), nan)
+
+
+@pytest.mark.parametrize("out", ["bf16", "e4m3"])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("rows,E,N,Kd", [(1, 1, 640, 2048), (3, 1, 7168, 7168), (16, 1, 256, 8192), (17, 1, 384, 2304),
+                                         (64, 1, 512, 4096), (65, 1, 512, 4096), (128, 1, 256, 3200), (5, 3, 256, 2688),
+                                         (2, 1, 128, 1920)])
+def test_tiles_shared_by_a_cluster(rows, E, N, Kd, swiglu, out):
+    """Few tiles: the channels are split among the blocks of a cluster, unevenly where their
+    groups do not divide."""
+    g = torch.Generator().manual_seed(rows + N)
+    w, ws = weights(g, E, N, Kd, swiglu)
+    x, xs = rows_of(g, rows, Kd)
+    counts = [rows - 2 * (E // 2)] + [2 if i % 2 else 0 for i in range(E - 1)]
+    offsets, cnt, _ = groups(counts)
+    status = _status()
+    got = moedc.matmul_e4m3(x, xs, w, ws, offsets=offsets, counts=cnt, swiglu=swiglu, out_dtype=OUT[out], status=status)
+    again = moedc.matmul_e4m3(x, xs, w, ws, offsets=offsets, counts=cnt, swiglu=swiglu, out_dtype=OUT[out], status=status)
+    assert int(status) == 0
+    for e, c in enumerate(counts):
+        a = int(offsets[e])
+        if not c:
+            continue
+        v, err = product(wide_x(x[a:a + c], xs[a:a + c]), wide_w(w[e], ws[e], swiglu), swiglu)
+        check((got[0][a:a + c], got[1][a:a + c]) if out == "e4m3" else got[a:a + c], v, err, out)
+    for p, q in zip(got if out == "e4m3" else [got], again if out == "e4m3" else [again]):
+        assert torch.equal(p.float(), q.float())
 
 
 def test_large_scales_and_small_ones():
