@@ -72,7 +72,6 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     const int tile_n = a.gated ? kMsRows : 2 * kMsRows;
     const int tiles = (a.N + tile_n - 1) / tile_n, groups = a.K / kMsGroup;
-    // with parts > 1 a cluster has one tile at most
     const int part = parts > 1 ? cluster_rank() : 0, first_unit = blockIdx.x / parts, unit_step = gridDim.x / parts;
     const int quads_all = (groups + 3) / 4;
     const int g_beg = quads_all * part / parts * 4, g_end = min(quads_all * (part + 1) / parts * 4, groups);
@@ -111,6 +110,16 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
     const int units = s_pre[a.E] * tiles;
     if (over && blockIdx.x == 0) raise_status(a.status, MOEDC_ERR_CAPACITY);
 
+    // every warp of a cluster comes by the three barriers of a tile, those that have nothing
+    // to do between them as well
+    auto tile_done = [&]() __attribute__((always_inline)) {
+        if (parts > 1) {
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
+            cluster_sync();
+        }
+    };
     if (warp < 8) {
         // ---- epilogue
         if (a.wait_extra) mbar_wait(&never, 0, &s_abort);
@@ -164,33 +173,38 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                 if (g % 4 == 3 || g == g_end - 1) facs.next(kMsFactorBufs);
             }
             if (parts > 1) {
-                cluster_sync();     // no block's products read its stages any more
-                float* sums = reinterpret_cast<float*>(smem);   // [part - 1][tile][token][row]
+                cluster_sync();     // 1: no block's products read its stages any more
+                float* sums = reinterpret_cast<float*>(smem);   // [part - 1][tile][token / 4][row][token % 4]
                 const int cols = (u.m + 15) / 16 * 16;
+                // four tokens of a row together: each store at another block costs some 40 clocks
                 if (part > 0) {
-                    const uint32_t to = cluster_addr(sums + ((part - 1) * 2 * cols + j0) * kMsRows + row, 0);
+                    const uint32_t to = cluster_addr(sums + ((part - 1) * 2 * cols + j0) * kMsRows + row * 4, 0);
 #pragma unroll
-                    for (int j = 0; j < kMsHalf; ++j) {
-                        if (j >= mine) break;
+                    for (int j = 0; j < kMsHalf; j += 4) {
+                        if (j >= mine) break;       // whole fours: `cols` has room for them
 #pragma unroll
                         for (int t = 0; t < 2; ++t)
-                            st_cluster(to + (t * cols + j) * (kMsRows * 4), j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x);
+                            st_cluster(to + (t * cols + j) * (kMsRows * 4), acc[t][j / 2], acc[t][j / 2 + 1]);
                     }
                 }
-                cluster_sync();
-                if (part > 0) continue;
-                for (int p = 1; p < parts; ++p) {
-                    const float* from = sums + ((p - 1) * 2 * cols + j0) * kMsRows + row;
+                cluster_sync();     // 2: the sums are there
+                for (int p = 1; p < parts && part == 0; ++p) {
+                    const float* from = sums + ((p - 1) * 2 * cols + j0) * kMsRows + row * 4;
 #pragma unroll
-                    for (int j = 0; j < kMsHalf; ++j) {
+                    for (int j = 0; j < kMsHalf; j += 4) {
                         if (j >= mine) break;
 #pragma unroll
                         for (int t = 0; t < 2; ++t) {
-                            float& s = j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x;
-                            s += from[(t * cols + j) * kMsRows];
+                            const float4 s = *reinterpret_cast<const float4*>(from + (t * cols + j) * kMsRows);
+                            acc[t][j / 2].x += s.x, acc[t][j / 2].y += s.y;
+                            acc[t][j / 2 + 1].x += s.z, acc[t][j / 2 + 1].y += s.w;
                         }
                     }
                 }
+                // (the next tile's copies come to where these were)
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                cluster_sync();     // 3: the sums have been read
+                if (part > 0) continue;
             }
             // tokens that src leads outside of x: zeros
             if (a.src) {
@@ -225,16 +239,18 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                 // a warp's lanes are 32 neighbouring channels of a token
                 uint16_t* o = static_cast<uint16_t*>(a.out) + at;
 #pragma unroll
-                for (int j = 0; j < kMsHalf; ++j) {
-                    if (j >= mine) break;
+                for (int c = 0; c < kMsHalf; c += 8) {
+                    if (c >= mine) break;
 #pragma unroll
-                    for (int t = 0; t < 2; ++t) {
-                        if (t == 1 && a.gated) break;
-                        const float v = j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x;
-                        if (n + t * kMsRows < a.N)
-                            o[(int64_t)j * a.N + t * kMsRows] =
-                                a.f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
-                    }
+                    for (int j = c; j < c + 8; ++j)
+#pragma unroll
+                        for (int t = 0; t < 2; ++t) {
+                            if (t == 1 && a.gated) break;
+                            const float v = j & 1 ? acc[t][j / 2].y : acc[t][j / 2].x;
+                            if (j < mine && n + t * kMsRows < a.N)
+                                o[(int64_t)j * a.N + t * kMsRows] =
+                                    a.f16 ? __half_as_ushort(__float2half_rn(v)) : __bfloat16_as_ushort(__float2bfloat16_rn(v));
+                        }
                 }
             } else {
                 // the rule of dispatch, of the binary32 values: a token's 128 channels are the
@@ -285,7 +301,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
         int issued = 0;
         const bool gather = a.src != nullptr, first = gather ? lane == 0 : tc_elect();
         bool stop = !gather && !first;
-        for (int unit = first_unit; unit < units && !stop; unit += unit_step) {
+        for (int unit = first_unit; unit < units; unit += unit_step) {
             const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
             int t[4] = {0, 0, 0, 0};
             if (gather) {
@@ -295,7 +311,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
             }
             const int box = u.m <= 16 ? 0 : u.m <= 32 ? 1 : u.m <= 64 ? 2 : 3;   // 16 << box rows
             const int bytes = 2 * kMsTile + (gather ? (u.m + 3) / 4 * 4 : 16 << box) * kMsGroup;
-            for (int g = g_beg; g < g_end; ++g) {
+            for (int g = g_beg; g < g_end && !stop; ++g) {
                 stop = !mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
                 if (gather) stop = __any_sync(0xffffffffu, stop);
                 if (stop) break;
@@ -318,6 +334,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                 ring.next(kMsStages);
                 ++issued;
             }
+            tile_done();
         }
         __syncwarp();
         // no copy may land after the block has gone, whatever else gave up
@@ -355,6 +372,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                 accs.next(2);
                 ring.next(kMsStages);
             }
+            tile_done();
         }
         // tensor memory is given back only when the last product is through
         if (leader) tc_commit(&done);
@@ -416,13 +434,8 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                 facs.next(kMsFactorBufs);
                 load(min(g0 + 4, groups - 1));
             }
+            tile_done();
         }
-    }
-    if (parts > 1 && (warp >= 8 || first_unit >= units)) {
-        // (the epilogue's warps are at theirs above)
-        __syncwarp();
-        cluster_sync();
-        cluster_sync();
     }
     tc_fence_before();
     __syncthreads();
@@ -435,6 +448,13 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
 }  // namespace moedc
 
 namespace moedc_host {
+
+// most tiles that are split into as many parts
+#ifndef MOEDC_PARTS_8
+#define MOEDC_PARTS_8 14
+#define MOEDC_PARTS_4 36
+#define MOEDC_PARTS_2 72
+#endif
 
 int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream)
 {
@@ -459,15 +479,18 @@ int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaS
     const int tile = a.gated ? moedc::kMsRows : 2 * moedc::kMsRows;
     const int64_t units = ((int64_t)a.rows / moedc::kMsTokens + (a.E < a.rows ? a.E : a.rows)) * ((a.N + (int64_t)tile - 1) / tile);
     const int blocks = sm_count();
-    // parts: as many as there are SMs for, eight groups each at least, their sums in the stages
-    int parts = 1;
+    // parts of the channels: a cluster of four or eight needs its SMs in one of the GPU's
+    // groups of them, which holds two or three of the former.  One token x 7168 channels,
+    // 28 tiles: 29.1 us in one part, 18.1 in two, 14.1 in four, 19.8 in eight (a second wave);
+    // 14 tiles: 28.8, 17.8, 13.0, 10.7; 56 tiles: 29.8, 22.7, 26.8.
     const int64_t most = a.rows < moedc::kMsTokens ? a.rows : moedc::kMsTokens;
     const int64_t sums = (most + 15) / 16 * 16 * 2 * moedc::kMsRows * sizeof(float);
-    while (parts < 8 && units * (parts + 1) <= blocks && a.K / moedc::kMsGroup >= 8 * (parts + 1) &&
-           parts * sums <= moedc::kMsStages * moedc::kMsStage)
-        ++parts;
+    auto fits = [&](int p, int64_t tiles) {
+        return units <= tiles && a.K / moedc::kMsGroup >= 4 * p && (p - 1) * sums <= moedc::kMsStages * moedc::kMsStage;
+    };
+    const int parts = fits(8, MOEDC_PARTS_8) ? 8 : fits(4, MOEDC_PARTS_4) ? 4 : fits(2, MOEDC_PARTS_2) ? 2 : 1;
     clear_stale_error();
-    launch_cluster(k, parts, (int)(units * parts < blocks ? units * parts : blocks / parts * parts), moedc::kMsThreads,
+    launch_cluster(k, parts, (int)(units * parts < blocks ? units * parts : blocks), moedc::kMsThreads,
                    kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a, parts, wmap, xmaps);
     return launch_status();
 }

@@ -137,9 +137,9 @@ __device__ __forceinline__ uint32_t cluster_addr(const void* p, int rank)
     asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
     return r;
 }
-__device__ __forceinline__ void st_cluster(uint32_t at, float v)
+__device__ __forceinline__ void st_cluster(uint32_t at, float2 v, float2 w)
 {
-    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(at), "f"(v) : "memory");
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at), "f"(v.x), "f"(v.y), "f"(w.x), "f"(w.y) : "memory");
 }
 __device__ __forceinline__ void tma_2d_pair(void* to, const CUtensorMap* map, int x, int y, uint32_t bar)
 {

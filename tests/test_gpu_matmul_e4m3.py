@@ -252,6 +252,23 @@ def test_tiles_shared_by_a_cluster(rows, E, N, Kd, swiglu, out):
         assert torch.equal(p.float(), q.float())
 
 
+def test_overlapping_groups_in_clusters():
+    """Groups that share rows make more tiles than the call can know of; each is computed."""
+    g = torch.Generator().manual_seed(13)
+    w, ws = weights(g, 6, 256, 2048, False)
+    x, xs = rows_of(g, 3, 2048)
+    offsets = torch.zeros(7, dtype=torch.int32).cuda()
+    cnt = torch.full((6,), 3, dtype=torch.int32).cuda()
+    status = _status()
+    y = moedc.matmul_e4m3(x, xs, w, ws, offsets=offsets, counts=cnt, status=status)
+    # whichever expert came last
+    best = torch.full((3, 256), float("inf"), dtype=torch.float64, device="cuda")
+    for e in range(6):
+        v, err = product(wide_x(x, xs), wide_w(w[e], ws[e], False), False)
+        best = torch.minimum(best, (y.double() - v).abs() - err - rounding(v.abs() + err, torch.bfloat16))
+    assert (best <= 0).all() and int(status) == 0
+
+
 def test_large_scales_and_small_ones():
     """Scales far apart: the groups' sums are scaled one by one."""
     g = torch.Generator().manual_seed(7)
