@@ -831,6 +831,14 @@ def _maps(offsets, counts, E: int) -> None:
         _need_shape(counts, (E,), "counts")
 
 
+def _here(first: torch.Tensor, *others: torch.Tensor | None) -> None:
+    """All on the current device, whose stream the call goes to."""
+    here = _device()
+    for t in (first, *others):
+        if t is not None and t.get_device() != here:
+            raise ValueError(f"tensors must be on the current device, cuda:{here}")
+
+
 def _status(status, device):
     """(status tensor, whether the call waits for its kernels and raises their errors)"""
     if status is not None:
@@ -862,6 +870,7 @@ def quant_e4m3(x: torch.Tensor, block_rows: int = 1, out=None):
         out = (torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device),
                torch.empty(shape, dtype=torch.float32, device=x.device))
     codes, scales = out
+    _here(x, codes, scales)
     _need(codes, torch.float8_e4m3fn, "out[0]")
     _need_shape(codes, x.shape, "out[0]")
     _need(scales, torch.float32, "out[1]")
@@ -951,6 +960,7 @@ def matmul_e4m3(x: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Te
         _need(ys, torch.float32, "out[1]")
         _need_shape(ys, (*lead, N // 128), "out[1]")
     status, wait = _status(status, x.device)
+    _here(x, xs, w, ws, offsets, counts, src, y, ys, status, workspace)
     if workspace is not None:
         _need(workspace, torch.uint8, "workspace")
     elif src is not None:
@@ -1004,6 +1014,7 @@ def matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor | None = None
         _need(products, x.dtype, "out[1]")
         _need_shape(products, (R, wn), "out[1]")
     status, wait = _status(status, x.device)
+    _here(x, w, offsets, counts, y, products, status)
     _check((_lib or load()).moedc_matmul(
         x.data_ptr(), ld, dtype, Kd, w.data_ptr(), E, N, SWIGLU if swiglu else 0, _p(offsets),
         _p(counts), R, y.data_ptr(), _p(products), status.data_ptr(), _stream(None)),
@@ -1026,6 +1037,7 @@ def swiglu_grad(dh: torch.Tensor, products: torch.Tensor,
         out = torch.empty_like(products)
     _need(out, dh.dtype, "out")
     _need_shape(out, (R, 2 * N), "out")
+    _here(dh, products, out)
     _check((_lib or load()).moedc_swiglu_grad(dh.data_ptr(), ld, products.data_ptr(), dtype, R, N,
                                               out.data_ptr(), _stream(None)), "moedc_swiglu_grad")
     return out
@@ -1076,6 +1088,7 @@ def matmul_grad(dout: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | No
         if dw.numel() != E * N * Kd or dw.shape[-2:] != (N, Kd):
             raise ValueError(f"out[1] must have shape {(E, N, Kd)}, not {tuple(dw.shape)}")
     status, wait = _status(status, dout.device)
+    _here(dout, x, w, offsets, counts, dx, dw, status)
     _check((_lib or load()).moedc_matmul_grad(
         dout.data_ptr(), ld, _p(x), ldx, _p(w), dtype, Kd, E, N, _p(offsets), _p(counts), R,
         _p(dx), _p(dw), F32 if dw is not None and dw.dtype == torch.float32 else dtype,

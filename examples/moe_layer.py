@@ -1,10 +1,15 @@
 """A mixture-of-experts layer on one GPU, out of the library's operators.
 
-  decode_step   router -> rows sorted by expert (the maps alone) -> 4-bit gate/up
-                products with SwiGLU, reading the tokens through the maps -> 4-bit
-                down products -> weighted way back.  Nothing is read on the host.
-  MoeLayer      the same layer in training, with bf16 experts: router, sort and
-                unsort as autograd functions over the library's gradients.
+  decode_step   router -> rows sorted by expert (the maps alone) -> gate/up products
+                with SwiGLU, reading the tokens through the maps -> down products
+                -> weighted way back.  4-bit experts, or e4m3 ones with a scale for
+                each 128 x 128 block, which take the tokens and the rows between the
+                products in e4m3 too.  Nothing is read on the host.
+  slots_step    e4m3 experts behind dispatch and before combine: the products read
+                the receive buffer.
+  MoeLayer      the same layer in training, with 16-bit experts: router, sort, gated
+                block, down products and unsort as autograd functions over the
+                library's gradients.  Nothing is read on the host.
 
     python examples/moe_layer.py
 """
@@ -44,17 +49,48 @@ def quantize_int4(w: torch.Tensor, group: int):
     return (q[..., 0] | q[..., 1] << 4).to(torch.uint8).contiguous(), s.contiguous()
 
 
-def decode_step(x: torch.Tensor, logits: torch.Tensor, experts: Int4Experts, K: int,
+@dataclass
+class E4m3Experts:
+    """E experts: gate and up rows [E, 2I, H], down rows [E, H, I], with scales by 128 x 128
+    block (I and H multiples of 128)."""
+    gate_up: torch.Tensor
+    gate_up_scales: torch.Tensor
+    down: torch.Tensor
+    down_scales: torch.Tensor
+
+    @staticmethod
+    def of(gate_up: torch.Tensor, down: torch.Tensor) -> "E4m3Experts":
+        return E4m3Experts(*moedc.quant_e4m3(gate_up, block_rows=128),
+                           *moedc.quant_e4m3(down, block_rows=128))
+
+
+def decode_step(x: torch.Tensor, logits: torch.Tensor, experts: Int4Experts | E4m3Experts, K: int,
                 status: torch.Tensor) -> torch.Tensor:
     """y [T, H] of the tokens x [T, H] with the router's logits [T, E]."""
     E = logits.shape[1]
     idx, w = moedc.gate(logits, K, flags=FLAGS)
     m = moedc.sort(None, idx, E, status=status)          # maps alone: the products gather
+    maps = dict(offsets=m.offsets, counts=m.counts, status=status)
+    if isinstance(experts, E4m3Experts):
+        h = moedc.matmul_e4m3(*moedc.quant_e4m3(x), experts.gate_up, experts.gate_up_scales,
+                              src=m.src, top_k=K, swiglu=True, out_dtype=moedc.FP8_E4M3, **maps)
+        return moedc.unsort(moedc.matmul_e4m3(*h, experts.down, experts.down_scales, **maps), m.row, w)
     h = moedc.matvec_int4(x, experts.gate_up, experts.gate_up_scales, offsets=m.offsets,
                           counts=m.counts, src=m.src, top_k=K, swiglu=True, status=status)
     out = moedc.matvec_int4(h, experts.down, experts.down_scales, offsets=m.offsets,
                             counts=m.counts, status=status)
     return moedc.unsort(out, m.row, w)
+
+
+def slots_step(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tensor, E: int, R: int,
+               cap: int, experts: E4m3Experts) -> torch.Tensor:
+    """y [T, H] through dispatch's receive buffer of cap slots an expert."""
+    lay, recv, scales, _ = moedc.layout_dispatch(x, topk_idx, E, R, cap, moedc.FP8_E4M3)
+    slots = dict(counts=lay.num_tokens_per_expert, status=lay.status)
+    h = moedc.matmul_e4m3(recv, scales, experts.gate_up, experts.gate_up_scales, swiglu=True,
+                          out_dtype=moedc.FP8_E4M3, **slots)
+    out = moedc.matmul_e4m3(*h, experts.down, experts.down_scales, **slots)
+    return moedc.combine(out, topk_idx, lay.slot, topk_weights, status=lay.status)
 
 
 # ----------------------------------------------------------------- training
@@ -106,8 +142,44 @@ class Unsort(torch.autograd.Function):
         return drows, dw, None, None
 
 
+class Block(torch.autograd.Function):
+    """silu(rows Wg^T) * (rows Wu^T) of each expert's rows."""
+
+    @staticmethod
+    def forward(ctx, rows, gate_up, offsets, counts, status):
+        h, products = moedc.matmul(rows, gate_up, offsets=offsets, counts=counts, swiglu=True,
+                                   keep=True, status=status)
+        ctx.save_for_backward(rows, gate_up, products, offsets, counts)
+        ctx.status = status
+        return h
+
+    @staticmethod
+    def backward(ctx, dh):
+        rows, gate_up, products, offsets, counts = ctx.saved_tensors
+        d = moedc.swiglu_grad(dh.contiguous(), products)
+        return *moedc.matmul_grad(d, rows, gate_up, offsets=offsets, counts=counts,
+                                  status=ctx.status), None, None, None
+
+
+class Product(torch.autograd.Function):
+    """rows W^T of each expert's rows."""
+
+    @staticmethod
+    def forward(ctx, rows, w, offsets, counts, status):
+        ctx.save_for_backward(rows, w, offsets, counts)
+        ctx.status = status
+        return moedc.matmul(rows, w, offsets=offsets, counts=counts, status=status)
+
+    @staticmethod
+    def backward(ctx, dout):
+        rows, w, offsets, counts = ctx.saved_tensors
+        return *moedc.matmul_grad(dout.contiguous(), rows, w, offsets=offsets, counts=counts,
+                                  status=ctx.status), None, None, None
+
+
 class MoeLayer(torch.nn.Module):
-    """E SwiGLU experts of width I over H channels, K to a token."""
+    """E SwiGLU experts of width I over H channels, K to a token.  `status` collects what
+    the experts' products report."""
 
     def __init__(self, H: int, I: int, E: int, K: int, align: int = 16,
                  dtype: torch.dtype = torch.bfloat16, device: str = "cuda"):
@@ -121,12 +193,16 @@ class MoeLayer(torch.nn.Module):
         self.router = init(E, H)
         self.gate_up = init(E, 2 * I, H)
         self.down = init(E, H, I)
+        self.register_buffer("status", torch.zeros(1, dtype=torch.int32, device=device), persistent=False)
 
     def forward(self, x: torch.Tensor) -> torch.Tensor:
         idx, w = Gate.apply((x @ self.router.T).float(), self.K)
-        rows, row, src, offsets, _ = Sort.apply(x, idx, self.E, self.align)
-        # the experts' products, group by group: the group sizes are the one thing read on
-        # the host (a grouped GEMM takes `offsets` on the device instead)
+        rows, row, src, offsets, counts = Sort.apply(x, idx, self.E, self.align)
+        if x.dtype != torch.float32 and not (self.down.shape[1] % 8 or self.down.shape[2] % 8):
+            h = Block.apply(rows, self.gate_up, offsets, counts, self.status)
+            return Unsort.apply(Product.apply(h, self.down, offsets, counts, self.status), w, row, src)
+        # binary32 and odd widths: the experts' products group by group, the group sizes read
+        # on the host
         out, edges = [], offsets.tolist()
         for e in range(self.E):
             a, b = (rows[edges[e]:edges[e + 1]] @ self.gate_up[e].T).chunk(2, dim=1)
@@ -157,12 +233,14 @@ def main() -> None:
         print(f"decode step, 16 tokens, {E} experts of {H} x {I}, {name}: "
               f"{(time.perf_counter() - t) / n * 1e6:.1f} us")
 
-    timed("call by call", lambda: decode_step(x, logits, experts, K, status))
-    graph = torch.cuda.CUDAGraph()
-    with torch.cuda.graph(graph):
-        y = decode_step(x, logits, experts, K, status)
-    timed("as a CUDA graph", graph.replay)
-    assert int(status) == 0 and torch.isfinite(y).all()
+    for kind, experts in (("4 bits", experts),
+                          ("e4m3", E4m3Experts.of(up.to(torch.bfloat16), down.to(torch.bfloat16)))):
+        timed(f"{kind}, call by call", lambda: decode_step(x, logits, experts, K, status))
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            y = decode_step(x, logits, experts, K, status)
+        timed(f"{kind}, as a CUDA graph", graph.replay)
+        assert int(status) == 0 and torch.isfinite(y).all()
 
     layer = MoeLayer(512, 256, 8, 2)
     opt = torch.optim.SGD(layer.parameters(), lr=0.05)
