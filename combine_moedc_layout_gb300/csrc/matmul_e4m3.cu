@@ -42,19 +42,34 @@ __global__ void __launch_bounds__(kMmCopyRows* kWarp) matmul_gather_kernel(const
 namespace moedc_host {
 
 #ifndef MOEDC_STREAM_ROWS
-#define MOEDC_STREAM_ROWS 64
+#define MOEDC_STREAM_ROWS 16
 #endif
 
-// Gathering the rows of a block's stage by TMA takes some 80 clocks for four of them, again
-// for every tile of columns: beyond some 25 rows it is longer than the products.  Then they
-// are brought into packed order first.
-bool matmul_gathers_first(int E, int rows)
+// By rows an expert, us of the weights on the tile's rows / of the tokens on them:
+//   rows                              8         16        24        32        64
+//   64 experts of 2 x 2048 x 7168  289 / 300 294 / 302 312 / 304 321 / 305 412 / 309
+//   128 of 2048 x 2048                        92 / 90             106 / 92
+//   8 of 7168 x 2048                                               35 / 28   54 / 29
+// Tiles so few that clusters share them are the exception: one expert of 7168 x 7168, 16 rows
+// 16 / 28, 64 rows 31 / 28.
+static bool weights_on_rows(int E, int N, bool gated, int rows)
 {
     const int64_t active = E < rows ? E : rows;
-    return rows >= 32 * active;
+    return rows <= MOEDC_STREAM_ROWS * active ||
+           (rows <= 2 * MOEDC_STREAM_ROWS && active * ((N + (gated ? 127 : 255)) / (gated ? 128 : 256)) <= 36);
 }
 
-int launch_mm_gather(moedc::MmArgs& a, const void* x, uint8_t* workspace, cudaStream_t stream)
+// Gathering the rows of a block's stage by TMA takes some 80 clocks for four of them, again
+// for every tile of columns: with 128 rows an expert 4220 us against 2000, copy included (256
+// experts of 2 x 2048 x 7168, in a form of pairs of SMs).  So beyond some 25 rows they are
+// brought into packed order first.
+static bool gathers_first(int E, int rows)
+{
+    const int64_t active = E < rows ? E : rows;
+    return rows > MOEDC_STREAM_ROWS * active;
+}
+
+static int launch_mm_gather(moedc::MmArgs& a, const void* x, uint8_t* workspace, cudaStream_t stream)
 {
     const int groups = a.xs_g == 0 ? 1 : a.K / 128;
     float* xs = reinterpret_cast<float*>(workspace + (size_t)a.rows * a.K);
@@ -75,7 +90,7 @@ int launch_mm_gather(moedc::MmArgs& a, const void* x, uint8_t* workspace, cudaSt
 extern "C" size_t moedc_matmul_e4m3_workspace_bytes(int Kd, int E, int rows)
 {
     if (Kd < 128 || Kd % 128 != 0 || E < 1 || E > MOEDC_MAX_E || rows < 1) return 0;
-    return moedc_host::matmul_gathers_first(E, rows) ? (size_t)rows * Kd + (size_t)rows * (Kd / 128) * sizeof(float) : 0;
+    return moedc_host::gathers_first(E, rows) ? (size_t)rows * Kd + (size_t)rows * (Kd / 128) * sizeof(float) : 0;
 }
 
 extern "C" int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float* xs, int scale_layout, const void* w,
@@ -131,7 +146,6 @@ extern "C" int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float*
         if (st != MOEDC_OK) return st;
         x = workspace;
     }
-    const int64_t active = E < rows ? E : rows;
-    if (a.src || rows <= MOEDC_STREAM_ROWS * active) return launch_mm_stream(a, x, w, stream);
+    if (a.src || weights_on_rows(E, N, gated, rows)) return launch_mm_stream(a, x, w, stream);
     return launch_mm_rows(a, x, w, stream);
 }

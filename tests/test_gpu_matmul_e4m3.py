@@ -66,8 +66,10 @@ CASES = [
 @pytest.mark.parametrize("many", [False, True])
 @pytest.mark.parametrize("counts,N,Kd,align", CASES)
 def test_packed_rows(counts, N, Kd, align, swiglu, out, many):
-    """`many`: rows of nobody behind the groups, so that the call expects many rows to an expert
-    and takes its other form."""
+    """`many`: rows of nobody behind the groups, so that the call expects many rows to an expert;
+    else experts without rows behind them, so that it expects few, and takes its other form."""
+    if not many:
+        counts = counts + [0] * (sum(counts) // 12)
     if out == "e4m3":
         N = -(-N // 128) * 128
     g = torch.Generator().manual_seed(len(counts) + N)
@@ -196,7 +198,7 @@ def test_rows_out_of_range_count_as_zeros():
         moedc.matmul_e4m3(x, xs, w, ws, offsets=offsets, counts=cnt, src=src, top_k=2)
     assert err.value.code == moedc.ERR_EXPERT_RANGE
     # where the rows are copied first
-    src = torch.arange(80, dtype=torch.int32).cuda() % 8
+    src = (torch.arange(80, dtype=torch.int32) % 8).cuda()
     src[[7, 50]] = torch.tensor([8, -1], dtype=torch.int32).cuda()
     offsets, cnt, _ = groups([40, 40])
     assert moedc.moedc_matmul_e4m3_workspace_bytes(256, 2, 80) > 0
