@@ -118,6 +118,8 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
             if (some) {
 #pragma unroll
                 for (int c = 0; c < 4; ++c) {
+                    const int n = u.n0 + half * 128 + c * 32;
+                    if (n >= a.N) break;
                     float v[32];
                     if (any) {
                         tc_ld32(d + half * 128 + c * 32, v);
@@ -128,7 +130,6 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0.0f;   // an expert without rows
                     }
-                    const int n = u.n0 + half * 128 + c * 32;
                     if (a.f32) mm_store32(buf, static_cast<float*>(a.out) + at * a.N, a.N, n, a.N, have, v);
                     else mm_store32(buf, o, a.N, n, a.N, have, true, a.f16, v);
                 }

@@ -831,10 +831,10 @@ def _maps(offsets, counts, E: int) -> None:
         _need_shape(counts, (E,), "counts")
 
 
-def _here(first: torch.Tensor, *others: torch.Tensor | None) -> None:
+def _here(*tensors: torch.Tensor | None) -> None:
     """All on the current device, whose stream the call goes to."""
     here = _device()
-    for t in (first, *others):
+    for t in tensors:
         if t is not None and t.get_device() != here:
             raise ValueError(f"tensors must be on the current device, cuda:{here}")
 
