@@ -30,7 +30,15 @@ __global__ void __launch_bounds__(kMmCopyRows* kWarp) matmul_gather_kernel(const
         bad |= t < 0;
         const uint4* from = reinterpret_cast<const uint4*>(x + (int64_t)max(t, 0) * a.K);
         uint4* out = reinterpret_cast<uint4*>(to + (int64_t)r * a.K);
-        for (int i = lane; i < a.K / 16; i += kWarp) out[i] = t < 0 ? make_uint4(0, 0, 0, 0) : __ldg(from + i);
+        for (int i = lane; i < a.K / 16; i += 8 * kWarp) {
+            uint4 v[8];
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                v[k] = t < 0 || i + k * kWarp >= a.K / 16 ? make_uint4(0, 0, 0, 0) : __ldg(from + i + k * kWarp);
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+                if (i + k * kWarp < a.K / 16) out[i + k * kWarp] = v[k];
+        }
         for (int g = lane; g < groups; g += kWarp)
             to_xs[(int64_t)r * groups + g] = t < 0 ? 0.0f : __ldg(a.xs + t * a.xs_r + g * a.xs_g);
     }

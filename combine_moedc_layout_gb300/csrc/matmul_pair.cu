@@ -14,6 +14,10 @@
 //                of its channel in the neighbouring lane
 //   kMmDx        dx = dout W: the rows are W's columns; the contracted axis is its rows
 //
+// Where there are too few tiles for the SMs, two or four pairs share one: each takes a part of
+// the contracted axis and sends its sums to the first pair's shared memory, which adds them in
+// the pairs' order.
+//
 // Warps: 0-7 epilogue (0-3 every other 32 tokens, 4-7 the others), 8 TMA, 9 MMA (of the
 // pair's first block, for both; the copies of both count at its barrier).  Tensor memory: two
 // sums of 256 columns.
@@ -72,8 +76,8 @@ __device__ __forceinline__ uint32_t mp_round2(float lo, float hi, bool f16)
 }
 
 template <int MODE>
-__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMpThreads, 1)
-matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap wmap,
+__global__ void __launch_bounds__(kMpThreads, 1)
+matmul_pair_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_constant__ CUtensorMap wmap,
                    const __grid_constant__ BoxMaps xmaps)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
@@ -83,10 +87,12 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
     __shared__ volatile int s_abort;
 
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
-    const int rank = cluster_rank();
-    const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+    // of the block in its pair; of the pair's first block, and the pair's part of a tile
+    const int rank = cluster_rank() & 1, leader_rank = cluster_rank() & ~1, part = cluster_rank() / 2;
+    const int first_unit = blockIdx.x / (2 * parts), unit_step = gridDim.x / (2 * parts);
     const int tile_n = a.gated ? kMpHalf : kMpTile;
     const int tiles = (a.N + tile_n - 1) / tile_n, ksteps = (a.K + kMpElems - 1) / kMpElems;
+    const int s_first = ksteps * part / parts, s_last = ksteps * (part + 1) / parts - 1;
     int32_t* s_pre = reinterpret_cast<int32_t*>(smem + kMpStages * kMpStage);
     int32_t *s_beg = s_pre + a.E + 1, *s_end = s_beg + a.E;
 
@@ -116,13 +122,23 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
     const int units = s_pre[a.E] * tiles;
     if (over && blockIdx.x == 0) raise_status(a.status, MOEDC_ERR_CAPACITY);
 
+    // every warp of a cluster of several pairs comes by the three barriers of a tile, those that
+    // have nothing to do between them as well
+    auto tile_done = [&]() __attribute__((always_inline)) {
+        if (parts > 1) {
+            __syncwarp();
+            cluster_sync();
+            cluster_sync();
+            cluster_sync();
+        }
+    };
     if (warp < 8) {
         // ---- epilogue
         if (a.wait_extra) mbar_wait(&never, 0, &s_abort);
         const int half = warp >> 2, row = rank * kMpHalf + (warp & 3) * kWarp + lane, odd = lane & 1;
         const uint32_t d0 = tmem + ((uint32_t)((warp & 3) * kWarp) << 16);
         MvRing accs;
-        for (int unit = pair; unit < units; unit += pairs) {
+        for (int unit = first_unit; unit < units; unit += unit_step) {
             const MpUnit u = mp_unit(a, s_pre, s_beg, s_end, tiles, unit);
             mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
             tc_fence_after();
@@ -134,12 +150,41 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
             uint16_t* o = static_cast<uint16_t*>(a.out) + (int64_t)u.r0 * a.N + n;
             uint16_t* keep = static_cast<uint16_t*>(a.extra);
             if (keep) keep += (int64_t)u.r0 * 2 * a.N + odd * a.N + n;
-            for (int c = half * 32; c < u.m; c += 64) {
+            // [part - 1][token / 4][row][token % 4] of the other pairs' sums
+            float* sums = reinterpret_cast<float*>(smem) + (row & (kMpHalf - 1)) * 4;
+            if (parts > 1) {
+                cluster_sync();     // 1: no block's products read its stages any more
+                if (part > 0) {
+                    const uint32_t to = cluster_addr(sums + (part - 1) * u.cols * kMpHalf, rank);
+                    for (int c = half * 32; c < u.m; c += 64) {
+                        float v[32];
+                        tc_ld32(d + c, v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(v[j]));
+#pragma unroll
+                        for (int j = 0; j < 32; j += 4) {
+                            if (c + j >= u.m) break;
+                            st_cluster(to + (c + j) * (kMpHalf * 4), make_float2(v[j], v[j + 1]), make_float2(v[j + 2], v[j + 3]));
+                        }
+                    }
+                }
+                cluster_sync();     // 2: the sums are there
+            }
+            for (int c = half * 32; c < u.m && part == 0; c += 64) {
                 float v[32];
                 tc_ld32(d + c, v);
                 tc_wait_ld();
 #pragma unroll
                 for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(v[j]));
+                for (int p = 1; p < parts; ++p) {
+#pragma unroll
+                    for (int j = 0; j < 32; j += 4) {
+                        if (c + j >= u.m) break;
+                        const float4 s = *reinterpret_cast<const float4*>(sums + ((p - 1) * u.cols + c + j) * kMpHalf);
+                        v[j] += s.x, v[j + 1] += s.y, v[j + 2] += s.z, v[j + 3] += s.w;
+                    }
+                }
 #pragma unroll
                 for (int j = 0; j < 32; j += 2) {
                     const float got = __shfl_xor_sync(0xffffffffu, odd ? v[j] : v[j + 1], 1);
@@ -159,7 +204,12 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, 0);
+            if (parts > 1) {
+                // (the next tile's copies come to where these were)
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                cluster_sync();     // 3: the sums have been read
+            }
+            if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, leader_rank);
             accs.next(2);
         }
     } else if (warp == 8) {
@@ -168,19 +218,17 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
         MvRing ring;
         int issued = 0;
         bool stop = !tc_elect();
-        for (int unit = pair; unit < units && !stop; unit += pairs) {
+        for (int unit = first_unit; unit < units; unit += unit_step) {
             const MpUnit u = mp_unit(a, s_pre, s_beg, s_end, tiles, unit);
             const int mine = u.cols / 2, r0 = u.r0 + rank * mine;
             const int box = (mine + 31) / 32;                             // in 32 rows
             const int bytes = 2 * (kMpOperand + box * 32 * kMpBytes);     // of both blocks
-            for (int s = 0; s < ksteps; ++s) {
-                if (!mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort)) {
-                    stop = true;
-                    break;
-                }
+            for (int s = s_first; s <= s_last && !stop; ++s) {
+                stop = !mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
+                if (stop) break;
                 uint8_t* w = smem + ring.slot * kMpStage;
                 uint8_t* x = w + kMpOperand;
-                const uint32_t at = cluster_addr(full + ring.slot, 0);
+                const uint32_t at = cluster_addr(full + ring.slot, leader_rank);
                 if (rank == 0) mbar_arrive_expect(full + ring.slot, bytes);
                 if constexpr (MODE == kMmDx) {
 #pragma unroll
@@ -197,6 +245,7 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                 ring.next(kMpStages);
                 ++issued;
             }
+            tile_done();
         }
         // no copy may land after the block has gone, whatever else gave up
         for (int n = max(0, issued - kMpStages); n < issued && rank == 0; ++n) {
@@ -214,11 +263,11 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
             MvRing ring, accs;
             int k = 0;
             const uint32_t type = (a.f16 ? 0u : (1u << 7) | (1u << 10)) | (MODE == kMmDx ? 1u << 15 : 0u);
-            for (int unit = pair; unit < units; unit += pairs) {
+            for (int unit = first_unit; unit < units; unit += unit_step) {
                 const MpUnit u = mp_unit(a, s_pre, s_beg, s_end, tiles, unit);
                 const uint32_t idesc = (1u << 4) | type | ((uint32_t)(u.cols / 8) << 17) | ((uint32_t)(kMpTile / 16) << 24);
-                for (int s = 0; s < ksteps; ++s) {
-                    if (s == 0 && k++ >= 2) mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
+                for (int s = s_first; s <= s_last; ++s) {
+                    if (s == s_first && k++ >= 2) mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
                     mbar_wait_warp(full + ring.slot, ring.phase, &s_abort);
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + ring.slot * kMpStage);
@@ -228,18 +277,21 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
 #pragma unroll
                         for (int p = 0; p < 4; ++p)
                             // a descriptor counts in 16 bytes: 32 of a row, or 16 rows of 128
-                            tc_mma_pair(tmem + accs.slot * kMpTile, w + p * (MODE == kMmDx ? 128 : 2), x + p * 2, idesc, p != 0 || s != 0);
-                        tc_commit_pair(empty + ring.slot);
-                        if (s == ksteps - 1) tc_commit_pair(d_full + accs.slot);
+                            tc_mma_pair(tmem + accs.slot * kMpTile, w + p * (MODE == kMmDx ? 128 : 2), x + p * 2, idesc, p != 0 || s != s_first);
+                        tc_commit_pair(empty + ring.slot, leader_rank);
+                        if (s == s_last) tc_commit_pair(d_full + accs.slot, leader_rank);
                     }
                     __syncwarp();
-                    if (s == ksteps - 1) accs.next(2);
+                    if (s == s_last) accs.next(2);
                     ring.next(kMpStages);
                 }
+                tile_done();
             }
             // tensor memory is given back only when the last product is through
-            if (leader) tc_commit_pair(&done);
+            if (leader) tc_commit_pair(&done, leader_rank);
             __syncwarp();
+        } else {
+            for (int unit = first_unit; unit < units; unit += unit_step) tile_done();
         }
         volatile int alone = 0;
         if (!mbar_wait(&done, 0, &alone)) s_abort = 1;
@@ -266,6 +318,12 @@ bool map_rows16(CUtensorMap* map, const void* base, int64_t width, int64_t rows,
 
 namespace {
 
+// most tiles that are split into as many parts
+#ifndef MOEDC_PAIR_PARTS_4
+#define MOEDC_PAIR_PARTS_4 14
+#define MOEDC_PAIR_PARTS_2 36
+#endif
+
 // x: the rows
 template <int MODE>
 int launch_mm_pair(const moedc::MmArgs& a, const CUtensorMap& w, const void* x, int64_t ldx, cudaStream_t stream)
@@ -281,9 +339,17 @@ int launch_mm_pair(const moedc::MmArgs& a, const CUtensorMap& w, const void* x, 
     const int tile = a.gated ? moedc::kMpHalf : moedc::kMpTile;
     const int64_t units = ((int64_t)a.rows / moedc::kMpTile + (a.E < a.rows ? a.E : a.rows)) * ((a.N + (int64_t)tile - 1) / tile);
     const int pairs = sm_count() / 2;
+    // parts of the contracted axis, as in matmul_stream.cu: clusters of four or eight blocks.  One
+    // token x 4096 channels: 14 tiles 21.4 us in one part, 16.1 in two, 12.7 in four; 36 tiles 22.0
+    // and 18.3; 512 channels 9.5 and 10.6.
+    const int64_t most = a.rows < moedc::kMpTile ? a.rows : moedc::kMpTile;
+    const int64_t sums = (most + 31) / 32 * 32 * moedc::kMpHalf * sizeof(float);
+    const int ksteps = (a.K + moedc::kMpElems - 1) / moedc::kMpElems;
+    auto fits = [&](int p, int64_t tiles) { return units <= tiles && ksteps >= 16 * p && (p - 1) * sums <= (int64_t)kFixed; };
+    const int parts = fits(4, MOEDC_PAIR_PARTS_4) ? 4 : fits(2, MOEDC_PAIR_PARTS_2) ? 2 : 1;
     clear_stale_error();
-    launch(k, 2 * (int)(units < pairs ? units : pairs), moedc::kMpThreads, kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a, w,
-           rows);
+    launch_cluster(k, 2 * parts, 2 * parts * (int)(units < pairs ? units : pairs), moedc::kMpThreads,
+                   kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a, parts, w, rows);
     return launch_status();
 }
 

@@ -14,6 +14,7 @@
 // Warps: 0-7 epilogue (0-3 the first half of the columns, or of the channels, 4-7 the
 // others), 8 TMA, 9 MMA.
 #include "matmul_store.cuh"
+#include "quotient.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
 
@@ -205,6 +206,7 @@ matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                 }
                 top = fmaxf(top, 1e-4f);
                 const float sc = __fdiv_rn(top, 448.0f);
+                const Quotient<2> by = Quotient<2>::by(sc);
                 const int n = u.n0 + half * (a.gated ? 64 : 128);
                 if (some && n < a.N) {
                     uint8_t* o = static_cast<uint8_t*>(a.out) + (int64_t)(u.r0 + first) * a.N + n;
@@ -218,8 +220,7 @@ matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
 #pragma unroll
                             for (int i = 0; i < 4; ++i) {
                                 const float* f = v + h + 16 * k + 4 * i;
-                                w[i] = pack_e4m3x2(__fdiv_rn(f[0], sc), __fdiv_rn(f[1], sc)) |
-                                       pack_e4m3x2(__fdiv_rn(f[2], sc), __fdiv_rn(f[3], sc)) << 16;
+                                w[i] = by.codes(f[0], f[1]) | by.codes(f[2], f[3]) << 16;
                             }
                             q[k] = make_uint4(w[0], w[1], w[2], w[3]);
                         }

@@ -100,11 +100,12 @@ __device__ __forceinline__ void tc_free_pair(uint32_t at, uint32_t columns)
 {
     asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(at), "r"(columns) : "memory");
 }
-// arrives at the barrier of that name in both blocks
-__device__ __forceinline__ void tc_commit_pair(uint64_t* bar)
+// arrives at the barrier of that name in both blocks of the pair, whose first is block `first`
+// of the cluster
+__device__ __forceinline__ void tc_commit_pair(uint64_t* bar, int first = 0)
 {
     asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(smem_u32(bar)),
-                 "h"((uint16_t)3) : "memory");
+                 "h"((uint16_t)(3 << first)) : "memory");
 }
 __device__ __forceinline__ void tc_mma_pair(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add)
 {

@@ -153,6 +153,39 @@ def test_block_gradients_against_differences():
         assert abs(by_w - float((dw.double() * ew).sum())) <= 2.0 ** -9 * float(dw.double().norm() * 6)
 
 
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("rows,E,N,Kd", [(1, 1, 4096, 4096), (33, 1, 2048, 1032), (128, 1, 520, 2048), (129, 1, 264, 4096),
+                                         (256, 1, 264, 2048), (300, 1, 264, 1024), (5, 3, 256, 264), (7, 1, 8192, 512), (40, 1, 520, 4168),
+                                         (128, 1, 264, 4168), (9, 4, 1544, 2056)])
+def test_tiles_shared_by_a_cluster(rows, E, N, Kd, swiglu):
+    """Few tiles: the contracted axis is split among pairs, unevenly where its stages do not
+    divide.  The gradient of the rows contracts N."""
+    g = torch.Generator().manual_seed(rows + N)
+    counts = [rows - 2 * (E // 2)] + [2 if i % 2 else 0 for i in range(E - 1)]
+    offsets, cnt, _ = groups(counts)
+    n = 2 * N if swiglu else N
+    x, w = randn(g, torch.bfloat16, rows, Kd), randn(g, torch.bfloat16, E, n, Kd, scale=Kd ** -0.5)
+    d = randn(g, torch.bfloat16, rows, n)
+    maps = dict(offsets=offsets, counts=cnt, status=_status())
+    y = moedc.matmul(x, w, swiglu=swiglu, **maps)
+    dx, _ = moedc.matmul_grad(d, None, w, **maps)
+    assert int(maps["status"]) == 0
+    for e, c in enumerate(counts):
+        a = int(offsets[e])
+        if c:
+            v, err = product(x[a:a + c], w[e], swiglu)
+            assert_within(y[a:a + c], v, err + rounding(v.abs() + err, torch.bfloat16))
+            v, err = product(d[a:a + c], w[e].T.contiguous(), False)
+            assert_within(dx[a:a + c], v, err + rounding(v.abs() + err, torch.bfloat16))
+    mine = owned(offsets, cnt, rows)
+    assert torch.equal(moedc.matmul(x, w, swiglu=swiglu, **maps)[mine], y[mine])
+    # groups that share rows: more tiles than the call can know of
+    offsets.zero_()
+    cnt.fill_(rows)
+    moedc.matmul_grad(d, None, w, **maps)
+    assert int(maps["status"]) == 0
+
+
 def test_slots_strides_and_capacity():
     g = torch.Generator().manual_seed(6)
     E, cap, N, Kd = 5, 40, 72, 104
