@@ -9,6 +9,10 @@
 // memory.  An expert's tokens end anywhere: the rows behind them, which are another
 // expert's, are cleared in shared memory as far as the products reach.
 //
+// A sum in tensor memory loses up to an ulp, always towards zero, with each product of 16
+// tokens: some 4e-8 of it a step, 2e-5 over 8192 tokens, which binary32 gradients would show.
+// They are summed in pieces of 768 tokens (7e-7), which the epilogue adds up, rounding to nearest.
+//
 // Warps: 0-7 epilogue (0-3 the first half of the columns, 4-7 the others), 8 TMA, 9 MMA (of
 // the pair's first block, for both), 10 clears and tells the first block that a stage has
 // arrived.  Tensor memory: two sums of 256 columns.
@@ -23,6 +27,7 @@ constexpr int kMmEpilogue = 8 * kWarp;
 constexpr int kMmTile = 256;                    // of the pair, both ways
 constexpr int kMmHalf = kMmTile / 2;
 constexpr int kMmElems = 64;                    // tokens of a stage
+constexpr int kMmPiece = 12;                    // stages of one sum, of binary32 gradients
 constexpr int kMmBytes = 128;                   // of a row of a box
 constexpr int kMmOperand = kMmHalf * kMmBytes;  // a block's share of one operand
 constexpr int kMmStage = 2 * kMmOperand;
@@ -33,7 +38,7 @@ constexpr int kMmColumns = 512;
 struct DwUnit {
     int e, r0, m;       // expert, its first row and rows
     int m0, n0;         // first row and column of the output
-    int ksteps;
+    int ksteps, piece;  // stages, and those of one sum
 };
 
 __device__ __forceinline__ DwUnit dw_unit(const MmArgs& a, const int32_t* s_beg, const int32_t* s_end, int tiles, int mtiles, int unit)
@@ -47,9 +52,11 @@ __device__ __forceinline__ DwUnit dw_unit(const MmArgs& a, const int32_t* s_beg,
     u.r0 = s_beg[u.e];
     u.m = s_end[u.e] - u.r0;
     u.ksteps = (u.m + kMmElems - 1) / kMmElems;
+    u.piece = a.f32 ? kMmPiece : max(u.ksteps, 1);
     return u;
 }
 
+template <bool kF32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap lmap,
                  const __grid_constant__ CUtensorMap rmap)
@@ -107,6 +114,42 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
             const int first = rank * kMmHalf + (warp & 3) * kWarp;
             const int have = a.M - u.m0 - first;
             const bool some = have > 0;
+            if (kF32 && u.ksteps > u.piece) {
+                float acc[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[c][j] = 0.0f;
+                for (int s = 0; s < u.ksteps; s += u.piece) {
+                    mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
+                    tc_fence_after();
+                    if (some) {
+#pragma unroll
+                        for (int c = 0; c < 8; ++c) {
+                            float v[16];
+                            tc_ld16(d0 + accs.slot * kMmTile + half * 128 + c * 16, v);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) asm volatile("" : "+f"(v[j]));
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) acc[c / 2][c % 2 * 16 + j] += v[j];
+                        }
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, 0);
+                    accs.next(2);
+                }
+                float* o = static_cast<float*>(a.out) + ((int64_t)u.e * a.M + u.m0 + first) * a.N;
+                if (some) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int n = u.n0 + half * 128 + c * 32;
+                        if (n < a.N) mm_store32(buf, o, a.N, n, a.N, have, acc[c]);
+                    }
+                }
+                continue;
+            }
             const bool any = u.ksteps > 0;
             if (any) {
                 mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
@@ -130,7 +173,7 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
 #pragma unroll
                         for (int j = 0; j < 32; ++j) v[j] = 0.0f;   // an expert without rows
                     }
-                    if (a.f32) mm_store32(buf, static_cast<float*>(a.out) + at * a.N, a.N, n, a.N, have, v);
+                    if constexpr (kF32) mm_store32(buf, static_cast<float*>(a.out) + at * a.N, a.N, n, a.N, have, v);
                     else mm_store32(buf, o, a.N, n, a.N, have, true, a.f16, v);
                 }
             }
@@ -184,10 +227,10 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
             const uint32_t idesc = (1u << 4) | type | major | ((uint32_t)(kMmTile / 8) << 17) | ((uint32_t)(kMmTile / 16) << 24);
             for (int unit = pair; unit < units; unit += pairs) {
                 const DwUnit u = dw_unit(a, s_beg, s_end, tiles, mtiles, unit);
+                int in = 0;     // stage of the sum
                 for (int s = 0; s < u.ksteps; ++s) {
-                    if (s == 0 && k++ >= 2) {
-                        mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
-                    }
+                    if (in == 0 && k++ >= 2) mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
+                    const bool last = in == u.piece - 1 || s == u.ksteps - 1;
                     mbar_wait_warp(ready + ring.slot, ring.phase, &s_abort);
                     tc_fence_after();
                     const uint32_t left = smem_u32(smem + ring.slot * kMmStage);
@@ -199,13 +242,14 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
                         for (int p = 0; p < 4; ++p) {
                             if (p >= steps) break;
                             // a descriptor counts in 16 bytes: 16 rows of 128
-                            tc_mma_pair(tmem + accs.slot * kMmTile, l + p * 128, r + p * 128, idesc, p != 0 || s != 0);
+                            tc_mma_pair(tmem + accs.slot * kMmTile, l + p * 128, r + p * 128, idesc, p != 0 || in != 0);
                         }
                         tc_commit_pair(empty + ring.slot);
-                        if (s == u.ksteps - 1) tc_commit_pair(d_full + accs.slot);
+                        if (last) tc_commit_pair(d_full + accs.slot);
                     }
                     __syncwarp();
-                    if (s == u.ksteps - 1) accs.next(2);
+                    if (last) accs.next(2);
+                    in = last ? 0 : in + 1;
                     ring.next(kMmStages);
                 }
             }
@@ -253,12 +297,11 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
 
 namespace moedc_host {
 
-int launch_mm_dw(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* x, int64_t ldx, cudaStream_t stream)
+namespace {
+
+template <bool kF32> int launch_dw(const moedc::MmArgs& a, const CUtensorMap& l, const CUtensorMap& r, cudaStream_t stream)
 {
-    CUtensorMap l, r;
-    if (!map_rows16(&l, dout, a.M, a.rows, ldd, moedc::kMmElems) || !map_rows16(&r, x, a.N, a.rows, ldx, moedc::kMmElems))
-        return MOEDC_ERR_CUDA;
-    auto* k = moedc::matmul_dw_kernel;
+    auto* k = moedc::matmul_dw_kernel<kF32>;
     constexpr size_t kFixed = moedc::kMmStages * moedc::kMmStage + moedc::kMmBuf;
     static PerDevice raised;
     if (!raise_smem_limit(raised, (const void*)k, (int)kFixed + (3 * MOEDC_MAX_E + 1) * 4)) return MOEDC_ERR_CUDA;
@@ -268,6 +311,16 @@ int launch_mm_dw(const moedc::MmArgs& a, const void* dout, int64_t ldd, const vo
     launch(k, 2 * (int)(units < pairs ? units : pairs), moedc::kMmThreads, kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a, l,
            r);
     return launch_status();
+}
+
+}  // namespace
+
+int launch_mm_dw(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* x, int64_t ldx, cudaStream_t stream)
+{
+    CUtensorMap l, r;
+    if (!map_rows16(&l, dout, a.M, a.rows, ldd, moedc::kMmElems) || !map_rows16(&r, x, a.N, a.rows, ldx, moedc::kMmElems))
+        return MOEDC_ERR_CUDA;
+    return a.f32 ? launch_dw<true>(a, l, r, stream) : launch_dw<false>(a, l, r, stream);
 }
 
 }  // namespace moedc_host

@@ -186,6 +186,21 @@ def test_tiles_shared_by_a_cluster(rows, E, N, Kd, swiglu):
     assert int(maps["status"]) == 0
 
 
+@pytest.mark.parametrize("counts", [[8192], [1024, 1025, 2047, 0, 5000]])
+def test_binary32_weight_gradients_of_many_tokens(counts):
+    """The tensor core's sums lose up to an ulp (2^-23) with each product of 16 tokens, 48 of them in a
+    piece of 768, the pieces' sums half an ulp each, 11 of them at most: less than 64 * 2^-23 of the
+    sums, whose norms are at most the result's for values of random signs."""
+    g = torch.Generator().manual_seed(12)
+    offsets, cnt, rows = groups(counts, tail=3)
+    x, d = randn(g, torch.bfloat16, rows, 264), randn(g, torch.bfloat16, rows, 328)
+    _, dw = moedc.matmul_grad(d, x, None, offsets=offsets, counts=cnt, dw_dtype=torch.float32, status=_status())
+    for e, c in enumerate(counts):
+        a = int(offsets[e])
+        ref = d[a:a + c].double().T @ x[a:a + c].double()
+        assert (dw[e].double() - ref).norm() <= 64 * 2.0 ** -23 * ref.norm()
+
+
 def test_slots_strides_and_capacity():
     g = torch.Generator().manual_seed(6)
     E, cap, N, Kd = 5, 40, 72, 104
