@@ -75,16 +75,6 @@ template <typename T> struct Unit<T, 1> {
 
 template <typename T> constexpr int kVec = 16 / (int)sizeof(T);
 
-// s = 1 / (1 + exp(-g)) and 1 - s, both to a few ulps over the whole range: exp(-|g|) does not
-// overflow, so that s goes down to the smallest binary32 numbers, and 1 - s does too.  The
-// quotient, of numbers between 1 and 2, is the fast one of two ulps.
-__device__ __forceinline__ void sigmoid_both(float g, float& s, float& rest)
-{
-    const float e = expf(-fabsf(g)), r = __fdividef(1.0f, 1.0f + e);
-    s = g < 0.0f ? e * r : r;
-    rest = g < 0.0f ? r : e * r;
-}
-
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll

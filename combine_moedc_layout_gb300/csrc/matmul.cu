@@ -5,7 +5,10 @@
 namespace moedc {
 
 // A thread owns eight channels of a row: 6 bytes read and 4 written for each, HBM.
-//   du = dh silu(g);  dg = dh u s (1 + g (1 - s)),  s = 1 / (1 + exp(-g))
+//   du = dh g s;  dg = dh u s (1 + g (1 - s)),  s = 1 / (1 + exp(-g))
+// from left to right, each operation rounded by itself, as the formulas read: the result is
+// rounded to 16 bits, and the products of the backward pass take it from there, so a last bit
+// that another order turns is one of the gradients'.  Where exp(-g) overflows, s is exp(g).
 template <typename T>
 __global__ void swiglu_grad_kernel(const T* __restrict__ dh, int64_t ld, const T* products, int rows, int N,
                                    T* dproducts)   // may be one buffer
@@ -24,10 +27,11 @@ __global__ void swiglu_grad_kernel(const T* __restrict__ dh, int64_t ld, const T
         Unit<T, 8>::widen(*reinterpret_cast<const uint4*>(p + N), u);
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-            float s, rest;
-            sigmoid_both(g[j], s, rest);
-            const float dg = h[j] * u[j] * (s * (1.0f + g[j] * rest));
-            u[j] = h[j] * (g[j] * s);
+            const float e = expf(-g[j]);
+            const float s = isinf(e) ? expf(g[j]) : __fdiv_rn(1.0f, __fadd_rn(1.0f, e));
+            const float slope = __fadd_rn(1.0f, __fmul_rn(g[j], __fadd_rn(1.0f, -s)));
+            const float dg = __fmul_rn(__fmul_rn(__fmul_rn(h[j], u[j]), s), slope);
+            u[j] = __fmul_rn(__fmul_rn(h[j], g[j]), s);
             g[j] = dg;
         }
         *reinterpret_cast<uint4*>(d) = Unit<T, 8>::round(g);
