@@ -13,6 +13,9 @@
 // tokens: some 4e-8 of it a step, 2e-5 over 8192 tokens, which binary32 gradients would show.
 // They are summed in pieces of 768 tokens (7e-7), which the epilogue adds up, rounding to nearest.
 //
+// 32 experts of 512 tokens x 4096 x 4096: 350 us, 1570 TFLOP/s, stores and products together;
+// 60 of 64 x 1024 x 1024: 35 us, the stores (4.4 TB/s); binary32, 64 of 512 x 7168 x 2048: 828 us.
+//
 // Warps: 0-7 epilogue (0-3 the first half of the columns, 4-7 the others), 8 TMA, 9 MMA (of
 // the pair's first block, for both), 10 clears and tells the first block that a stage has
 // arrived.  Tensor memory: two sums of 256 columns.

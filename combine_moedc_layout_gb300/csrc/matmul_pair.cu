@@ -18,6 +18,10 @@
 // the contracted axis and sends its sums to the first pair's shared memory, which adds them in
 // the pairs' order.
 //
+// 8192^3: 573 us, 1917 TFLOP/s, the tensor pipe busy in 97% of the clocks; 32 experts of 512
+// rows x 2 x 2048 x 4096 with both products kept 345 us, 1590 TFLOP/s, of 300 rows 279 us, 1150:
+// with fewer than 256 columns the weights' way from L2 is the bound.
+//
 // Warps: 0-7 epilogue (0-3 every other 32 tokens, 4-7 the others), 8 TMA, 9 MMA (of the
 // pair's first block, for both; the copies of both count at its barrier).  Tensor memory: two
 // sums of 256 columns.

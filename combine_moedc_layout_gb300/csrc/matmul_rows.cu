@@ -10,6 +10,8 @@
 //
 // A buffer goes from the products to the epilogue and back in some 1500 clocks, 512 of them
 // products: that bounds a stage to 750, and reading and adding under it to some 900.
+// 8192^3: 429 us, 2560 TFLOP/s; 256 experts of 128 rows x 2 x 2048 x 7168: 1182 us, 6.4 TB/s
+// of weights.
 //
 // Warps: 0-7 epilogue (0-3 the first half of the columns, or of the channels, 4-7 the
 // others), 8 TMA, 9 MMA.

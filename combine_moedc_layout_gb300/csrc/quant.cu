@@ -4,7 +4,8 @@
 // Bound by HBM: every element is read once and kept in registers between the maximum and
 // the codes.  A thread owns 16 neighbouring channels, so that eight lanes hold a group of
 // 128 and store 128 bytes of codes; for blocks, 512 threads hold the 128 rows, each of them
-// two.  The quotients, not HBM, were the bound while each was a division.
+// two.  65536 x 7168 bf16 rows: 263 us, 5.4 TB/s; 32800 x 7168 in blocks: 144 us, 4.9 TB/s.  The
+// quotients, not HBM, were the bound while each was a division.
 #include "quotient.cuh"
 
 namespace moedc {
