@@ -50,16 +50,16 @@ __global__ void __launch_bounds__(kMmCopyRows* kWarp) matmul_gather_kernel(const
 namespace moedc_host {
 
 #ifndef MOEDC_STREAM_ROWS
-#define MOEDC_STREAM_ROWS 16
+#define MOEDC_STREAM_ROWS 24
 #endif
 
 // By rows an expert, us of the weights on the tile's rows / of the tokens on them:
-//   rows                              8         16        24        32        64
-//   64 experts of 2 x 2048 x 7168  289 / 300 294 / 302 312 / 304 321 / 305 412 / 309
-//   128 of 2048 x 2048                        92 / 90             106 / 92
-//   8 of 7168 x 2048                                               35 / 28   54 / 29
+//   rows                              8         16        24        32
+//   64 experts of 2 x 2048 x 7168  270 / 300 273 / 302 275 / 304 280 / 305
+//   128 of 2048 x 2048                        87 / 90   90 / 91       / 92
+//   8 of 7168 x 2048                                               31 / 28
 // Tiles so few that clusters share them are the exception: one expert of 7168 x 7168, 16 rows
-// 16 / 28, 64 rows 31 / 28.
+// 14.5 / 28, 32 rows 17.5 / 28.
 static bool weights_on_rows(int E, int N, bool gated, int rows)
 {
     const int64_t active = E < rows ? E : rows;
@@ -120,7 +120,7 @@ extern "C" int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float*
         !aligned(offsets, 4) || !aligned(counts, 4) || !aligned(src, 4) || !aligned(out, codes ? 16 : 2) ||
         !aligned(out_scales, 4) || !aligned(workspace, 16) || !aligned(dev_status, 4))
         return MOEDC_ERR_ARG;
-    if (((int64_t)rows / 128 + E) * (N / 128 + 1) > INT32_MAX) return MOEDC_ERR_ARG;   // units are counted in 32 bits
+    if (((int64_t)rows / 64 + E) * (N / 128 + 1) > INT32_MAX) return MOEDC_ERR_ARG;   // units are counted in 32 bits
     if (rows == 0 || x_rows == 0) return MOEDC_OK;
     if (!x || !xs || !out || (codes && !out_scales)) return MOEDC_ERR_ARG;
     moedc::MmArgs a{};

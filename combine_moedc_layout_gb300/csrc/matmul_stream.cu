@@ -2,24 +2,24 @@
 //
 // The weights lie on the rows of the tile and the tokens on its columns, as many (in
 // sixteens) as there are: a block multiplies 256 weight rows, in two tiles of 128 (with
-// `gated` the gate and the up rows of 128 channels), by up to 128 tokens.  A stage, 128
-// channels, is 32 KB of weights and 2 KB for each 16 tokens; three or four stages under way
+// `gated` the gate and the up rows of 128 channels), by up to 64 tokens.  A stage, 128
+// channels, is 32 KB of weights and 2 KB for each 16 tokens; four or five stages under way
 // on each SM keep HBM busy.
 //
-// Each stage has sums of its own, two buffers of tensor memory in turn.  A thread of the
+// Each stage has sums of its own, four buffers of tensor memory in turn.  A thread of the
 // epilogue owns a weight row of both tiles and half of the tokens, and adds
 //   xs[token] ws[block] * sum
-// into 128 registers; the factors come from shared memory, where one warp puts them four
+// into 64 registers; the factors come from shared memory, where one warp puts them four
 // groups ahead.
 //
 // Where there are too few tiles for the SMs, a cluster of blocks shares one: each block takes
 // a part of the channels, in fours of groups, and sends its sums to the first one's shared
 // memory, which adds them in the blocks' order.
 //
-// 64 experts of 8 rows x 2 x 2048 x 7168: 289 us, 6.5 TB/s of weights, HBM's rate; one token x
-// 7168 x 7168: 14 us, latency.
+// 64 experts of 8 rows x 2 x 2048 x 7168: 270 us, 7.0 TB/s of weights, HBM's rate (289 us with
+// room for 128 tokens, two sums and four stages); one token x 7168 x 7168: 13 us, latency.
 //
-// Warps: 0-7 epilogue (0-3 the first 64 tokens, 4-7 the others), 8 TMA, 9 MMA, 10 factors.
+// Warps: 0-7 epilogue (0-3 the first 32 tokens, 4-7 the others), 8 TMA, 9 MMA, 10 factors.
 #include "matmul.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
@@ -28,15 +28,16 @@ namespace moedc {
 
 constexpr int kMsThreads = 11 * kWarp;
 constexpr int kMsRows = 128;                        // of a tile of weights
-constexpr int kMsTokens = 128;
+constexpr int kMsTokens = 64;
 constexpr int kMsHalf = kMsTokens / 2;
 constexpr int kMsGroup = 128;                       // channels, and bytes, of a stage
 constexpr int kMsTile = kMsRows * kMsGroup;
 constexpr int kMsStage = 2 * kMsTile + kMsTokens * kMsGroup;
-constexpr int kMsStages = 4;
+constexpr int kMsStages = 5;
 constexpr int kMsFactors = 4 * 2 * kMsTokens;       // floats of four groups
 constexpr int kMsFactorBufs = 3;
 constexpr int kMsColumns = 512;
+constexpr int kMsAccs = kMsColumns / (2 * kMsTokens);   // sums under way
 
 struct MsUnit {
     int e, r0, m, n0;
@@ -66,7 +67,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int64_t s_scan[kMsThreads / kWarp];
-    __shared__ uint64_t full[kMsStages], empty[kMsStages], d_full[2], d_empty[2], f_full[kMsFactorBufs], f_empty[kMsFactorBufs];
+    __shared__ uint64_t full[kMsStages], empty[kMsStages], d_full[kMsAccs], d_empty[kMsAccs], f_full[kMsFactorBufs], f_empty[kMsFactorBufs];
     __shared__ uint64_t done, never;
     __shared__ float s_top[2][2][4][kMsHalf], s_scale[2][2][kMsHalf];
     __shared__ uint32_t s_tmem;
@@ -87,7 +88,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
             mbar_init(full + s, 1);
             mbar_init(empty + s, 1);
         }
-        for (int b = 0; b < 2; ++b) {
+        for (int b = 0; b < kMsAccs; ++b) {
             mbar_init(d_full + b, 1);
             mbar_init(d_empty + b, 8);
         }
@@ -172,7 +173,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                     mbar_arrive(d_empty + accs.slot);
                     if (g % 4 == 3 || g == g_end - 1) mbar_arrive(f_empty + facs.slot);
                 }
-                accs.next(2);
+                accs.next(kMsAccs);
                 if (g % 4 == 3 || g == g_end - 1) facs.next(kMsFactorBufs);
             }
             if (parts > 1) {
@@ -271,8 +272,8 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                 }
                 asm volatile("bar.sync %0, 128;" ::"r"(1 + half) : "memory");
                 {
-                    const int t = row / kMsHalf, j = row % kMsHalf;   // 128 threads: both tiles' 64 tokens
-                    if (j < mine && !(t == 1 && a.gated)) {
+                    const int t = row / kMsHalf, j = row % kMsHalf;   // both tiles' 32 tokens
+                    if (t < (a.gated ? 1 : 2) && j < mine) {
                         const float(&p)[4][kMsHalf] = s_top[half][t];
                         const float top = fmaxf(fmaxf(p[0][j], p[1][j]), fmaxf(p[2][j], p[3][j]));
                         const float sc = __fdiv_rn(fmaxf(top, 1e-4f), 448.0f);
@@ -312,7 +313,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                 for (int i = 0; i < 4; ++i)
                     if (lane * 4 + i < u.m) t[i] = max(mm_x_row(a, u.r0 + lane * 4 + i), 0);
             }
-            const int box = u.m <= 16 ? 0 : u.m <= 32 ? 1 : u.m <= 64 ? 2 : 3;   // 16 << box rows
+            const int box = u.m <= 16 ? 0 : u.m <= 32 ? 1 : 2;   // 16 << box rows
             const int bytes = 2 * kMsTile + (gather ? (u.m + 3) / 4 * 4 : 16 << box) * kMsGroup;
             for (int g = g_beg; g < g_end && !stop; ++g) {
                 stop = !mbar_wait(empty + ring.slot, ring.phase ^ 1, &s_abort);
@@ -356,7 +357,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
             // columns: as many tokens as there are, by 16
             const uint32_t idesc = (1u << 4) | ((uint32_t)((u.m + 15) / 16 * 2) << 17) | ((uint32_t)(kMsRows / 16) << 24);
             for (int g = g_beg; g < g_end; ++g) {
-                if (k++ >= 2) mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
+                if (k++ >= kMsAccs) mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
                 mbar_wait_warp(full + ring.slot, ring.phase, &s_abort);
                 tc_fence_after();
                 const uint32_t st = smem_u32(smem + ring.slot * kMsStage);
@@ -372,7 +373,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                     tc_commit(d_full + accs.slot);
                 }
                 __syncwarp();
-                accs.next(2);
+                accs.next(kMsAccs);
                 ring.next(kMsStages);
             }
             tile_done();
@@ -390,9 +391,9 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
         const int blocks = (a.N + 127) / 128;
         for (int unit = first_unit; unit < units; unit += unit_step) {
             const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
-            const float* xs[4];
+            const float* xs[kMsTokens / kWarp];
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
+            for (int q = 0; q < kMsTokens / kWarp; ++q) {
                 const int r = u.r0 + min(q * kWarp + lane, u.m - 1);
                 xs[q] = a.xs + (a.offsets || !a.counts || a.src ? max(mm_x_row(a, r), 0) * a.xs_r
                                                                 : u.e * a.xs_e + (r - u.e * a.slots) * a.xs_r);
@@ -400,7 +401,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
             const int b0 = u.n0 / 128;
             const float* w0 = a.ws + ((int64_t)u.e * (a.gated ? 2 : 1) * blocks + b0) * groups;
             const float* w1 = w0 + (int64_t)(a.gated ? blocks : b0 + 1 < blocks) * groups;
-            float s[4][4], v0[4], v1[4];
+            float s[kMsTokens / kWarp][4], v0[4], v1[4];
             auto load = [&](int g0) __attribute__((always_inline)) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
@@ -408,7 +409,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                     v0[i] = __ldg(w0 + g), v1[i] = __ldg(w1 + g);
                 }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kMsTokens / kWarp; ++q) {
                     if (q * kWarp >= u.m) break;
                     if (quads) {
                         const float4 v = __ldg(reinterpret_cast<const float4*>(xs[q] + min(g0, groups - 4)));
@@ -424,7 +425,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
                 mbar_wait_warp(f_empty + facs.slot, facs.phase ^ 1, &s_abort);
                 float* f = s_factors + facs.slot * kMsFactors + lane;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < kMsTokens / kWarp; ++q) {
                     if (q * kWarp >= u.m) break;
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -471,7 +472,7 @@ int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaS
     const cuuint32_t box[4] = {128, moedc::kMsRows, 1, 1};
     if (!tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box)) return MOEDC_ERR_CUDA;
     // gathered rows: one map, a row high; else as many as the rows can need
-    for (int i = 0; i < 4 && (i == 0 || (!a.src && a.rows > 8 << i)); ++i) {
+    for (int i = 0; i < 3 && (i == 0 || (!a.src && a.rows > 8 << i)); ++i) {
         const cuuint32_t xbox[2] = {128, a.src ? 1u : 16u << i};
         if (!tensor_map(xmaps.by + i, kType, kSwizzle, x, 2, xsize, xstride, xbox)) return MOEDC_ERR_CUDA;
     }
