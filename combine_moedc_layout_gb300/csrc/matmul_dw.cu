@@ -219,6 +219,13 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
             if (!mbar_wait(full + n % kMmStages, (n / kMmStages) & 1, &alone)) s_abort = 1;
         }
         __syncwarp();
+        // the last product's arrival at the second block; the wait begins behind the block's last
+        // copy, as its bound is one of a step and not of the call
+        if (rank == 1) {
+            volatile int alone = 0;
+            if (!mbar_wait(&done, 0, &alone)) s_abort = 1;
+        }
+        __syncwarp();
     } else if (warp == 9) {
         // ---- MMA, for both blocks: one elected lane issues; the warp stays together
         if (rank == 0) {
@@ -259,9 +266,9 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
             // tensor memory is given back only when the last product is through
             if (leader) tc_commit_pair(&done);
             __syncwarp();
+            volatile int alone = 0;
+            if (!mbar_wait(&done, 0, &alone)) s_abort = 1;
         }
-        volatile int alone = 0;
-        if (!mbar_wait(&done, 0, &alone)) s_abort = 1;
         __syncwarp();
     } else {
         // ---- stages that have arrived in this block

@@ -256,6 +256,13 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_con
             volatile int alone = 0;
             if (!mbar_wait(full + n % kMpStages, (n / kMpStages) & 1, &alone)) s_abort = 1;
         }
+        __syncwarp();
+        // the last product's arrival at the second block; the wait begins behind the block's last
+        // copy, as its bound is one of a step and not of the call
+        if (rank == 1) {
+            volatile int alone = 0;
+            if (!mbar_wait(&done, 0, &alone)) s_abort = 1;
+        }
         // a second block that gave up sees no barrier of its copies: they have a millisecond
         if (s_abort)
             for (const unsigned long long t0 = globaltimer(); globaltimer() - t0 < 1000000ull;) {}
@@ -294,11 +301,11 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_con
             // tensor memory is given back only when the last product is through
             if (leader) tc_commit_pair(&done, leader_rank);
             __syncwarp();
+            volatile int alone = 0;
+            if (!mbar_wait(&done, 0, &alone)) s_abort = 1;
         } else {
             for (int unit = first_unit; unit < units; unit += unit_step) tile_done();
         }
-        volatile int alone = 0;
-        if (!mbar_wait(&done, 0, &alone)) s_abort = 1;
         __syncwarp();
     }
     tc_fence_before();

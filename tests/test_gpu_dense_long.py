@@ -1,0 +1,51 @@
+"""The dense layers over contracted axes and calls that are long: sums that stay as exact as
+short ones, waits that are bounded by a step of the work and not by the call."""
+import pytest
+import torch
+
+from combine_moedc_layout_gb300 import moedc
+from lm_util import ROUND, U32
+from test_gpu_dense_edges import _need_bytes, _status
+
+pytestmark = pytest.mark.gpu
+
+
+def _uniform(seed, dtype, *shape, lo=0.0, hi=1.0):
+    g = torch.Generator(device="cuda").manual_seed(seed)
+    out = torch.empty(shape, dtype=dtype, device="cuda")
+    for part in out.view(-1).split(1 << 28):
+        part.copy_(torch.rand(part.shape, generator=g, device="cuda") * (hi - lo) + lo)
+    return out
+
+
+def _dw64(d, x, step=1 << 22):
+    return sum(d[a:a + step].double().T @ x[a:a + step].double() for a in range(0, len(x), step))
+
+
+def test_weight_gradients_of_one_tile_over_many_tokens():
+    """One pair of SMs for some 0.4 s.  Values of one sign: relative errors of the sum are at most
+    an ulp (2 * 2^-24) for each of a piece's 48 products, half an ulp for each of the pieces."""
+    _need_bytes(16 << 30)
+    rows = 3 << 25
+    x, d = _uniform(0, torch.bfloat16, rows, 8), _uniform(1, torch.bfloat16, rows, 8)
+    status = _status()
+    _, dw = moedc.matmul_grad(d, x, None, dw_dtype=torch.float32, status=status)
+    assert int(status) == moedc.OK
+    ref = _dw64(d, x)
+    assert ((dw[0].double() - ref).abs() <= (96 + rows / 768) * U32 * ref).all()
+
+
+def test_products_of_a_third_of_a_second():
+    """Every pair of SMs is at work for the whole call."""
+    _need_bytes(64 << 30)
+    rows, N, Kd = 1 << 17, 1 << 16, 1 << 15
+    x, w = _uniform(2, torch.bfloat16, rows, Kd), _uniform(3, torch.bfloat16, N, Kd)
+    status = _status()
+    y = moedc.matmul(x, w, status=status)
+    assert int(status) == moedc.OK
+    for r in (0, 70000, rows - 40):
+        for n in (0, 40000, N - 200):
+            ref = x[r:r + 40].double() @ w[n:n + 200].double().T
+            got = y[r:r + 40, n:n + 200].double()
+            # an ulp for each product of 16, one rounding
+            assert ((got - ref).abs() <= (Kd / 8 * U32 + ROUND[torch.bfloat16]) * ref).all()
