@@ -10,8 +10,10 @@
 // expert's, are cleared in shared memory as far as the products reach.
 //
 // A sum in tensor memory loses up to an ulp, always towards zero, with each product of 16
-// tokens: some 4e-8 of it a step, 2e-5 over 8192 tokens, which binary32 gradients would show.
-// They are summed in pieces of 768 tokens (7e-7), which the epilogue adds up, rounding to nearest.
+// tokens: some 4e-8 of it a step, 2e-5 over 8192 tokens, which binary32 gradients would show,
+// and half a step of f16 over 200000.  So tokens are summed in pieces, of 768 (7e-7) for
+// binary32 and of 8192 for 16 bits, which the epilogue adds up, rounding to nearest.
+// (A piece is also what the epilogue's bounded wait waits for.)
 //
 // 32 experts of 512 tokens x 4096 x 4096: 350 us, 1570 TFLOP/s, stores and products together;
 // 60 of 64 x 1024 x 1024: 35 us, the stores (4.4 TB/s); binary32, 64 of 512 x 7168 x 2048: 828 us.
@@ -31,6 +33,7 @@ constexpr int kMmTile = 256;                    // of the pair, both ways
 constexpr int kMmHalf = kMmTile / 2;
 constexpr int kMmElems = 64;                    // tokens of a stage
 constexpr int kMmPiece = 12;                    // stages of one sum, of binary32 gradients
+constexpr int kMmPiece16 = 128;                 // of 16-bit ones
 constexpr int kMmBytes = 128;                   // of a row of a box
 constexpr int kMmOperand = kMmHalf * kMmBytes;  // a block's share of one operand
 constexpr int kMmStage = 2 * kMmOperand;
@@ -55,8 +58,17 @@ __device__ __forceinline__ DwUnit dw_unit(const MmArgs& a, const int32_t* s_beg,
     u.r0 = s_beg[u.e];
     u.m = s_end[u.e] - u.r0;
     u.ksteps = (u.m + kMmElems - 1) / kMmElems;
-    u.piece = a.f32 ? kMmPiece : max(u.ksteps, 1);
+    u.piece = a.f32 ? kMmPiece : kMmPiece16;
     return u;
+}
+
+// Whether a 16-bit sum has several pieces.  By a whole warp.
+__device__ __forceinline__ bool dw_pieces(const MmArgs& a, const int32_t* s_beg, const int32_t* s_end)
+{
+    int most = 0;
+    if (a.rows > kMmPiece16 * kMmElems)
+        for (int e = threadIdx.x % kWarp; e < a.E; e += kWarp) most = max(most, s_end[e] - s_beg[e]);
+    return __reduce_max_sync(0xffffffffu, most) > kMmPiece16 * kMmElems;
 }
 
 template <bool kF32>
@@ -110,83 +122,91 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
         const int half = warp >> 2;
         const uint32_t d0 = tmem + ((uint32_t)((warp & 3) * kWarp) << 16);
         uint8_t* buf = smem + kMmStages * kMmStage + warp * 2048;
-        MvRing accs;
-        for (int unit = pair; unit < units; unit += pairs) {
-            const DwUnit u = dw_unit(a, s_beg, s_end, tiles, mtiles, unit);
-            // the warp's first row, and how many of its 32 there are
-            const int first = rank * kMmHalf + (warp & 3) * kWarp;
-            const int have = a.M - u.m0 - first;
-            const bool some = have > 0;
-            if (kF32 && u.ksteps > u.piece) {
-                float acc[4][32];
+        // 16 bits: a loop of its own for calls in which an expert has several pieces.  In one with
+        // the other it made that slower (60 x 64 x 1024 x 1024: 33.4 -> 35.1 us).
+        auto tiles_of = [&](auto pieces) __attribute__((always_inline)) {
+            constexpr bool kPieces = decltype(pieces)::value;
+            MvRing accs;
+            for (int unit = pair; unit < units; unit += pairs) {
+                const DwUnit u = dw_unit(a, s_beg, s_end, tiles, mtiles, unit);
+                // the warp's first row, and how many of its 32 there are
+                const int first = rank * kMmHalf + (warp & 3) * kWarp;
+                const int have = a.M - u.m0 - first;
+                const bool some = have > 0;
+                if (kPieces && u.ksteps > u.piece) {
+                    float acc[4][32];
 #pragma unroll
-                for (int c = 0; c < 4; ++c)
+                    for (int c = 0; c < 4; ++c)
 #pragma unroll
-                    for (int j = 0; j < 32; ++j) acc[c][j] = 0.0f;
-                for (int s = 0; s < u.ksteps; s += u.piece) {
-                    mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
-                    tc_fence_after();
+                        for (int j = 0; j < 32; ++j) acc[c][j] = 0.0f;
+                    for (int s = 0; s < u.ksteps; s += u.piece) {
+                        mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
+                        tc_fence_after();
+                        if (some) {
+#pragma unroll
+                            for (int c = 0; c < 8; ++c) {
+                                float v[16];
+                                tc_ld16(d0 + accs.slot * kMmTile + half * 128 + c * 16, v);
+                                tc_wait_ld();
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) asm volatile("" : "+f"(v[j]));
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) acc[c / 2][c % 2 * 16 + j] += v[j];
+                            }
+                        }
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, 0);
+                        accs.next(2);
+                    }
+                    const int64_t at = ((int64_t)u.e * a.M + u.m0 + first) * a.N;
                     if (some) {
 #pragma unroll
-                        for (int c = 0; c < 8; ++c) {
-                            float v[16];
-                            tc_ld16(d0 + accs.slot * kMmTile + half * 128 + c * 16, v);
-                            tc_wait_ld();
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) asm volatile("" : "+f"(v[j]));
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) acc[c / 2][c % 2 * 16 + j] += v[j];
+                        for (int c = 0; c < 4; ++c) {
+                            const int n = u.n0 + half * 128 + c * 32;
+                            if (n >= a.N) break;
+                            if constexpr (kF32) mm_store32(buf, static_cast<float*>(a.out) + at, a.N, n, a.N, have, acc[c]);
+                            else mm_store32(buf, static_cast<uint16_t*>(a.out) + at, a.N, n, a.N, have, true, a.f16, acc[c]);
                         }
                     }
+                    continue;
+                }
+                const bool any = u.ksteps > 0;
+                if (any) {
+                    mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
+                    tc_fence_after();
+                }
+                const uint32_t d = d0 + accs.slot * kMmTile;
+                const int64_t at = ((int64_t)u.e * a.M + u.m0 + first) * a.N;
+                if (some) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        const int n = u.n0 + half * 128 + c * 32;
+                        if (n >= a.N) break;
+                        float v[32];
+                        if (any) {
+                            tc_ld32(d + half * 128 + c * 32, v);
+                            tc_wait_ld();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(v[j]));
+                        } else {
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) v[j] = 0.0f;   // an expert without rows
+                        }
+                        if constexpr (kF32) mm_store32(buf, static_cast<float*>(a.out) + at, a.N, n, a.N, have, v);
+                        else mm_store32(buf, static_cast<uint16_t*>(a.out) + at, a.N, n, a.N, have, true, a.f16, v);
+                    }
+                }
+                if (any) {
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, 0);
                     accs.next(2);
                 }
-                float* o = static_cast<float*>(a.out) + ((int64_t)u.e * a.M + u.m0 + first) * a.N;
-                if (some) {
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        const int n = u.n0 + half * 128 + c * 32;
-                        if (n < a.N) mm_store32(buf, o, a.N, n, a.N, have, acc[c]);
-                    }
-                }
-                continue;
             }
-            const bool any = u.ksteps > 0;
-            if (any) {
-                mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
-                tc_fence_after();
-            }
-            const uint32_t d = d0 + accs.slot * kMmTile;
-            const int64_t at = (int64_t)u.e * a.M + u.m0 + first;
-            uint16_t* o = static_cast<uint16_t*>(a.out) + at * a.N;
-            if (some) {
-#pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    const int n = u.n0 + half * 128 + c * 32;
-                    if (n >= a.N) break;
-                    float v[32];
-                    if (any) {
-                        tc_ld32(d + half * 128 + c * 32, v);
-                        tc_wait_ld();
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) asm volatile("" : "+f"(v[j]));
-                    } else {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = 0.0f;   // an expert without rows
-                    }
-                    if constexpr (kF32) mm_store32(buf, static_cast<float*>(a.out) + at * a.N, a.N, n, a.N, have, v);
-                    else mm_store32(buf, o, a.N, n, a.N, have, true, a.f16, v);
-                }
-            }
-            if (any) {
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, 0);
-                accs.next(2);
-            }
-        }
+        };
+        if (kF32 || dw_pieces(a, s_beg, s_end)) tiles_of(std::true_type());
+        else tiles_of(std::false_type());
     } else if (warp == 8) {
         // ---- TMA: this block's rows of the left operand, its half of the right one
         // (one lane waits and issues)

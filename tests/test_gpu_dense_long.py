@@ -49,3 +49,38 @@ def test_products_of_a_third_of_a_second():
             got = y[r:r + 40, n:n + 200].double()
             # an ulp for each product of 16, one rounding
             assert ((got - ref).abs() <= (Kd / 8 * U32 + ROUND[torch.bfloat16]) * ref).all()
+
+
+# A sum of 16-bit outputs: an ulp (2 * 2^-24) for each of at most 512 products of 16 in a piece, half an
+# ulp for each piece and for the sums of up to four pairs, one rounding of the result.
+def _bound(K, dtype):
+    return (1024 + K / 8192 + 1 + 4) * U32 + ROUND[dtype]
+
+
+@pytest.mark.parametrize("rows", [8200, 65536 + 24, 1 << 20])
+def test_sixteen_bit_weight_gradients_of_many_tokens(rows):
+    """Values of one sign, where what a sum loses adds up."""
+    x, d = (_uniform(s, torch.float16, rows, n, lo=2.0 ** -4, hi=2.0 ** -3) for s, n in ((4, 72), (5, 264)))
+    status = _status()
+    _, dw = moedc.matmul_grad(d, x, None, status=status)
+    ref = _dw64(d, x)
+    assert int(status) == 0 and ((dw[0].double() - ref).abs() <= _bound(rows, torch.float16) * ref).all()
+    # two experts, one of them short
+    o = torch.tensor([0, 100, rows], dtype=torch.int32).cuda()
+    c = torch.tensor([100, rows - 100], dtype=torch.int32).cuda()
+    _, dw = moedc.matmul_grad(d, x, None, offsets=o, counts=c, status=status)
+    for e, part in enumerate((slice(0, 100), slice(100, rows))):
+        ref = _dw64(d[part], x[part])
+        assert ((dw[e].double() - ref).abs() <= _bound(rows, torch.float16) * ref).all()
+
+
+def test_sixteen_bit_gradients_of_one_tile_over_many_tokens():
+    """One pair of SMs for some 0.4 s."""
+    _need_bytes(16 << 30)
+    rows = 3 << 25
+    x, d = _uniform(10, torch.bfloat16, rows, 8), _uniform(11, torch.bfloat16, rows, 8)
+    status = _status()
+    _, dw = moedc.matmul_grad(d, x, None, status=status)
+    assert int(status) == moedc.OK
+    ref = _dw64(d, x)
+    assert ((dw[0].double() - ref).abs() <= _bound(rows, torch.bfloat16) * ref).all()
