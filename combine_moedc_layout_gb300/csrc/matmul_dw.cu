@@ -10,9 +10,10 @@
 // expert's, are cleared in shared memory as far as the products reach.
 //
 // A sum in tensor memory loses up to an ulp, always towards zero, with each product of 16
-// tokens: some 4e-8 of it a step, 2e-5 over 8192 tokens, which binary32 gradients would show,
-// and half a step of f16 over 200000.  So tokens are summed in pieces, of 768 (7e-7) for
-// binary32 and of 8192 for 16 bits, which the epilogue adds up, rounding to nearest.
+// tokens: some 4e-8 of it a step for values of random signs, 1e-7 for those of one sign, 5e-5
+// over 8192 tokens, which binary32 gradients would show, and half a step of f16 over 80000.  So
+// tokens are summed in pieces, of 768 for binary32 and of 8192 for 16 bits, which the epilogue
+// adds up, rounding to nearest.
 // (A piece is also what the epilogue's bounded wait waits for.)
 //
 // 32 experts of 512 tokens x 4096 x 4096: 350 us, 1570 TFLOP/s, stores and products together;

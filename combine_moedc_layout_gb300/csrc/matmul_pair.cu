@@ -14,6 +14,11 @@
 //                of its channel in the neighbouring lane
 //   kMmDx        dx = dout W: the rows are W's columns; the contracted axis is its rows
 //
+// A sum in tensor memory rounds towards zero with each product of 16 elements: 1e-7 of it a step
+// for values of one sign, 5e-5 over 8192 elements (half a step of f16 is 4.9e-4).  Longer axes are
+// summed in pieces of 8192, which the epilogue adds up, rounding to nearest; a piece is also what
+// its bounded wait waits for.  8192 x 4096 x 16384, two pieces: 562 us, 560 without them.
+//
 // Where there are too few tiles for the SMs, two or four pairs share one: each takes a part of
 // the contracted axis and sends its sums to the first pair's shared memory, which adds them in
 // the pairs' order.
@@ -39,6 +44,7 @@ constexpr int kMpBytes = 128;
 constexpr int kMpOperand = kMpHalf * kMpBytes;  // a block's share of one operand
 constexpr int kMpStage = 2 * kMpOperand;
 constexpr int kMpStages = 6;
+constexpr int kMpPiece = 128;                   // stages of one sum
 constexpr int kMpColumns = 512;
 
 struct MpUnit {
@@ -79,7 +85,8 @@ __device__ __forceinline__ uint32_t mp_round2(float lo, float hi, bool f16)
     return (uint32_t)mp_round(lo, f16) | (uint32_t)mp_round(hi, f16) << 16;
 }
 
-template <int MODE>
+// kPieces: the sums of a block's part have several pieces
+template <int MODE, bool kPieces>
 __global__ void __launch_bounds__(kMpThreads, 1)
 matmul_pair_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_constant__ CUtensorMap wmap,
                    const __grid_constant__ BoxMaps xmaps)
@@ -144,8 +151,48 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_con
         MvRing accs;
         for (int unit = first_unit; unit < units; unit += unit_step) {
             const MpUnit u = mp_unit(a, s_pre, s_beg, s_end, tiles, unit);
-            mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
-            tc_fence_after();
+            if constexpr (kPieces) {
+                // the pieces but the last one, then all of them to the last one's place
+                float acc[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) acc[i][j] = 0.0f;
+                for (int s = s_first;; s += kMpPiece) {
+                    mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
+                    tc_fence_after();
+                    const uint32_t at = d0 + accs.slot * kMpTile + half * 32;
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        if (half * 32 + i / 2 * 64 >= u.m) break;
+                        float v[16];
+                        tc_ld16(at + i / 2 * 64 + i % 2 * 16, v);
+                        tc_wait_ld();
+#pragma unroll
+                        for (int j = 0; j < 16; ++j) {
+                            asm volatile("" : "+f"(v[j]));
+                            acc[i / 2][i % 2 * 16 + j] += v[j];
+                        }
+                    }
+                    if (s + kMpPiece > s_last) break;
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive_pair(d_empty + accs.slot, leader_rank);
+                    accs.next(2);
+                }
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if (half * 32 + i / 2 * 64 >= u.m) break;
+                    uint32_t v[16];
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) v[j] = __float_as_uint(acc[i / 2][i % 2 * 16 + j]);
+                    tc_st16(d0 + accs.slot * kMpTile + half * 32 + i / 2 * 64 + i % 2 * 16, v);
+                }
+                tc_wait_st();
+            } else {
+                mbar_wait_warp(d_full + accs.slot, accs.phase, &s_abort);
+                tc_fence_after();
+            }
             const uint32_t d = d0 + accs.slot * kMpTile;
             // The thread's channel; neighbouring lanes trade a token for a token, so that each has
             // two channels of one (with `gated`: gate and up of one), the even lane of the first
@@ -278,7 +325,9 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_con
                 const MpUnit u = mp_unit(a, s_pre, s_beg, s_end, tiles, unit);
                 const uint32_t idesc = (1u << 4) | type | ((uint32_t)(u.cols / 8) << 17) | ((uint32_t)(kMpTile / 16) << 24);
                 for (int s = s_first; s <= s_last; ++s) {
-                    if (s == s_first && k++ >= 2) mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
+                    const bool first = kPieces ? (s - s_first) % kMpPiece == 0 : s == s_first;
+                    const bool last = s == s_last || (kPieces && (s - s_first) % kMpPiece == kMpPiece - 1);
+                    if (first && k++ >= 2) mbar_wait_warp(d_empty + accs.slot, accs.phase ^ 1, &s_abort);
                     mbar_wait_warp(full + ring.slot, ring.phase, &s_abort);
                     tc_fence_after();
                     const uint32_t st = smem_u32(smem + ring.slot * kMpStage);
@@ -288,12 +337,12 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_con
 #pragma unroll
                         for (int p = 0; p < 4; ++p)
                             // a descriptor counts in 16 bytes: 32 of a row, or 16 rows of 128
-                            tc_mma_pair(tmem + accs.slot * kMpTile, w + p * (MODE == kMmDx ? 128 : 2), x + p * 2, idesc, p != 0 || s != s_first);
+                            tc_mma_pair(tmem + accs.slot * kMpTile, w + p * (MODE == kMmDx ? 128 : 2), x + p * 2, idesc, p != 0 || !first);
                         tc_commit_pair(empty + ring.slot, leader_rank);
-                        if (s == s_last) tc_commit_pair(d_full + accs.slot, leader_rank);
+                        if (last) tc_commit_pair(d_full + accs.slot, leader_rank);
                     }
                     __syncwarp();
-                    if (s == s_last) accs.next(2);
+                    if (last) accs.next(2);
                     ring.next(kMpStages);
                 }
                 tile_done();
@@ -343,10 +392,7 @@ int launch_mm_pair(const moedc::MmArgs& a, const CUtensorMap& w, const void* x, 
     // a block's half of a chunk, in 32s
     for (int i = 0; i < 4 && (i == 0 || a.rows > 64 * i); ++i)
         if (!map_rows16(rows.by + i, x, a.K, a.rows, ldx, 32 * (i + 1))) return MOEDC_ERR_CUDA;
-    auto* k = moedc::matmul_pair_kernel<MODE>;
     constexpr size_t kFixed = moedc::kMpStages * moedc::kMpStage;
-    static PerDevice raised;
-    if (!raise_smem_limit(raised, (const void*)k, (int)kFixed + (3 * MOEDC_MAX_E + 1) * 4)) return MOEDC_ERR_CUDA;
     const int tile = a.gated ? moedc::kMpHalf : moedc::kMpTile;
     const int64_t units = ((int64_t)a.rows / moedc::kMpTile + (a.E < a.rows ? a.E : a.rows)) * ((a.N + (int64_t)tile - 1) / tile);
     const int pairs = sm_count() / 2;
@@ -358,6 +404,11 @@ int launch_mm_pair(const moedc::MmArgs& a, const CUtensorMap& w, const void* x, 
     const int ksteps = (a.K + moedc::kMpElems - 1) / moedc::kMpElems;
     auto fits = [&](int p, int64_t tiles) { return units <= tiles && ksteps >= 16 * p && (p - 1) * sums <= (int64_t)kFixed; };
     const int parts = fits(4, MOEDC_PAIR_PARTS_4) ? 4 : fits(2, MOEDC_PAIR_PARTS_2) ? 2 : 1;
+    // the longest part (of parts that differ by a stage)
+    const bool pieces = (ksteps + parts - 1) / parts > moedc::kMpPiece;
+    auto* k = pieces ? moedc::matmul_pair_kernel<MODE, true> : moedc::matmul_pair_kernel<MODE, false>;
+    static PerDevice raised[2];
+    if (!raise_smem_limit(raised[pieces], (const void*)k, (int)kFixed + (3 * MOEDC_MAX_E + 1) * 4)) return MOEDC_ERR_CUDA;
     clear_stale_error();
     launch_cluster(k, 2 * parts, 2 * parts * (int)(units < pairs ? units : pairs), moedc::kMpThreads,
                    kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a, parts, w, rows);

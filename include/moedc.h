@@ -579,7 +579,8 @@ MOEDC_EXPORT int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const floa
  *   dx[r][k]    = round( sum over n of dout[r][n] * w[e][n][k] )
  *   dw[e][n][k] = round( sum over e's rows r of dout[r][n] * x[r][k] ); 0 without rows
  * dx or dw may be NULL and is then not computed (w is read for dx alone, x for dw
- * alone).  dw_dtype is dtype or MOEDC_F32.  Rows that belong to no expert are
+ * alone).  dw_dtype is dtype or MOEDC_F32.  (Sums over more than 8192 elements, or
+ * rows for dw, are sums of pieces of that many; 768 rows for a binary32 dw.)  Rows that belong to no expert are
  * neither read into any result nor written.  The order of every sum is fixed:
  * equal inputs give equal bits.
  * dtype MOEDC_BF16 or MOEDC_F16; Kd and N multiples of 8; leading dimensions

@@ -84,3 +84,51 @@ def test_sixteen_bit_gradients_of_one_tile_over_many_tokens():
     assert int(status) == moedc.OK
     ref = _dw64(d, x)
     assert ((dw[0].double() - ref).abs() <= _bound(rows, torch.bfloat16) * ref).all()
+
+
+# two and four pairs of SMs to a tile, one pair
+@pytest.mark.parametrize("rows,n", [(40, 80), (200, 272), (300, 272), (700, 4112)])
+@pytest.mark.parametrize("K", [8200, 131080, 1 << 20])
+def test_rows_and_their_gradients_over_a_long_axis(rows, n, K):
+    if rows * K + n * K > 1 << 30:
+        K = 131080
+    x = _uniform(6, torch.float16, rows, K, lo=2.0 ** -4, hi=2.0 ** -3)
+    w = _uniform(7, torch.float16, n, K, lo=2.0 ** -4, hi=2.0 ** -3)
+    ref = sum(x[:, k:k + 8192].double() @ w[:, k:k + 8192].double().T for k in range(0, K, 8192))
+    status = _status()
+    y = moedc.matmul(x, w, status=status)
+    assert int(status) == 0 and ((y.double() - ref).abs() <= _bound(K, torch.float16) * ref).all()
+    half = n // 2
+    h, p = moedc.matmul(x[:, :K], w, swiglu=True, keep=True, status=status)
+    assert torch.equal(p, y)
+    # of x W: the weights' rows are contracted
+    dx, _ = moedc.matmul_grad(x, None, w.T.contiguous(), status=status)
+    assert int(status) == 0 and ((dx.double() - ref).abs() <= _bound(K, torch.float16) * ref).all()
+
+
+def test_gated_block_over_a_long_axis():
+    """SwiGLU of sums below 1, where it is not the rounding of one of them."""
+    K = 131080
+    x = _uniform(8, torch.float16, 50, K, lo=2.0 ** -9, hi=2.0 ** -8)
+    w = _uniform(9, torch.float16, 144, K, lo=2.0 ** -9, hi=2.0 ** -8)
+    status = _status()
+    h = moedc.matmul(x, w, swiglu=True, status=status)
+    v = x.double() @ w.double().T
+    a, b = v[:, :72], v[:, 72:]
+    ref = a * torch.sigmoid(a) * b
+    # d log silu(a) / d log a = 1 + a (1 - s) <= 1 + a; 16 roundings of the epilogue
+    off = (_bound(K, torch.float32) * (2 + a) + 16 * U32 + ROUND[torch.float16]) * ref
+    assert int(status) == 0 and ((h.double() - ref).abs() <= off).all()
+
+
+def test_one_tile_over_an_axis_of_many_elements():
+    """Four pairs of SMs for some 0.3 s: each waits for a piece of its sum, not for all of it."""
+    _need_bytes(32 << 30)
+    N = 1 << 28
+    d = _uniform(12, torch.bfloat16, 8, N)
+    w = _uniform(13, torch.bfloat16, N, 8)
+    status = _status()
+    dx, _ = moedc.matmul_grad(d, None, w, status=status)
+    assert int(status) == moedc.OK
+    ref = sum(d[:, a:a + (1 << 22)].double() @ w[a:a + (1 << 22)].double() for a in range(0, N, 1 << 22))
+    assert ((dx.double() - ref).abs() <= _bound(N, torch.bfloat16) * ref).all()
