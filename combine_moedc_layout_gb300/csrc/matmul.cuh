@@ -134,7 +134,8 @@ int launch_mm_dx(const moedc::MmArgs& a, const void* dout, int64_t ldd, const vo
 int launch_mm_dw(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* x, int64_t ldx, cudaStream_t stream);
 // e4m3, by single SMs: the tokens on the tile's rows (matmul_rows.cu), no src
 int launch_mm_rows(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream);
-// the weights on the tile's rows (matmul_stream.cu): few rows to an expert
-int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream);
+// the weights on the tile's rows (matmul_stream.cu): few rows to an expert.  share: blocks may
+// share a tile's channels, which changes the order of the sums
+int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, bool share, cudaStream_t stream);
 
 }  // namespace moedc_host

@@ -154,6 +154,9 @@ extern "C" int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float*
         if (st != MOEDC_OK) return st;
         x = workspace;
     }
-    if (a.src || weights_on_rows(E, N, gated, rows)) return launch_mm_stream(a, x, w, stream);
+    // Rows to gather that a workspace would have brought to the other form keep its order of
+    // sums, every channel's in one block: the workspace changes no bit.
+    const bool few = weights_on_rows(E, N, gated, rows);
+    if (a.src || few) return launch_mm_stream(a, x, w, few, stream);
     return launch_mm_rows(a, x, w, stream);
 }

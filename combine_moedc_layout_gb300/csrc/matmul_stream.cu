@@ -460,7 +460,7 @@ namespace moedc_host {
 #define MOEDC_PARTS_2 72
 #endif
 
-int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaStream_t stream)
+int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, bool share, cudaStream_t stream)
 {
     constexpr auto kType = CU_TENSOR_MAP_DATA_TYPE_UINT8;
     constexpr auto kSwizzle = CU_TENSOR_MAP_SWIZZLE_128B;
@@ -490,7 +490,7 @@ int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, cudaS
     const int64_t most = a.rows < moedc::kMsTokens ? a.rows : moedc::kMsTokens;
     const int64_t sums = (most + 15) / 16 * 16 * 2 * moedc::kMsRows * sizeof(float);
     auto fits = [&](int p, int64_t tiles) {
-        return units <= tiles && a.K / moedc::kMsGroup >= 4 * p && (p - 1) * sums <= moedc::kMsStages * moedc::kMsStage;
+        return share && units <= tiles && a.K / moedc::kMsGroup >= 4 * p && (p - 1) * sums <= moedc::kMsStages * moedc::kMsStage;
     };
     const int parts = fits(8, MOEDC_PARTS_8) ? 8 : fits(4, MOEDC_PARTS_4) ? 4 : fits(2, MOEDC_PARTS_2) ? 2 : 1;
     clear_stale_error();
