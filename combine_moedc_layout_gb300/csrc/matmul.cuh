@@ -20,6 +20,7 @@ struct MmArgs {
     int slots;          // rows of an expert's slots where there are no offsets
     int top_k;
     const int32_t *offsets, *counts, *src;
+    bool packed;        // e4m3: src has been followed, x holds `rows` rows in packed order
     int32_t* status;
     // e4m3: scale of row r (row i of expert e's slots) and channels 128 g ..: xs[r * xs_r +
     // g * xs_g] (xs[e * xs_e + i * xs_r + g * xs_g]); ws [E][1 or 2][blocks][K / 128]
@@ -49,7 +50,7 @@ __device__ __forceinline__ void mm_expert_rows(const MmArgs& a, int e, int& beg,
     end = (int)(b < n ? n : 0);
 }
 
-// Row of x of packed row r; -1 where there is none.
+// Row of x, as the caller has it, of packed row r; -1 where there is none.
 __device__ __forceinline__ int mm_x_row(const MmArgs& a, int r)
 {
     if (!a.src) return r;
@@ -57,6 +58,9 @@ __device__ __forceinline__ int mm_x_row(const MmArgs& a, int r)
     const int t = i < 0 ? -1 : i / a.top_k;
     return t < a.x_rows ? t : -1;
 }
+
+// -0: of packed rows that src led outside of x
+constexpr uint32_t kMmLostScale = 0x80000000u;
 
 // silu(g) u.  exp(-|g|) does not overflow, so that the sigmoid goes down to the smallest
 // binary32 numbers; the quotient, of numbers between 1 and 2, is the fast one of two ulps.

@@ -128,7 +128,7 @@ matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
 #pragma unroll
             for (int j = 0; j < 64; ++j) acc[j] = make_float2(0.0f, 0.0f);
             const int xr = mine ? r : u.r0;
-            const float* xs = a.xs + (a.offsets || !a.counts ? xr * a.xs_r : u.e * a.xs_e + (xr - u.e * a.slots) * a.xs_r);
+            const float* xs = a.xs + (a.offsets || !a.counts || a.packed ? xr * a.xs_r : u.e * a.xs_e + (xr - u.e * a.slots) * a.xs_r);
             const int blocks = (a.N + 127) / 128;
             const int b0 = a.gated ? u.n0 / 128 : min(u.n0 / 128 + half, blocks - 1);
             const float* w0 = a.ws + ((int64_t)u.e * (a.gated ? 2 : 1) * blocks + b0) * groups;
@@ -181,6 +181,12 @@ matmul_rows_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUt
                 }
             }
             float* v = reinterpret_cast<float*>(acc);
+            // a row that src led outside of x: zeros, whatever the weights hold (every sx is the last
+            // group's by now)
+            if (a.packed && __float_as_uint(sx[0]) == kMmLostScale) {
+#pragma unroll
+                for (int j = 0; j < 128; ++j) v[j] = 0.0f;
+            }
             if (a.gated) {
 #pragma unroll
                 for (int j = 0; j < 64; ++j) v[j] = mm_silu_mul(v[j], v[64 + j]);
@@ -318,7 +324,7 @@ int launch_mm_rows(const moedc::MmArgs& a, const void* x, const void* w, cudaStr
     CUtensorMap wmap;
     moedc::BoxMaps xmaps{};
     const cuuint64_t K = a.K, N = a.N, parts = a.gated ? 2 : 1;
-    const cuuint64_t xsize[2] = {K, (cuuint64_t)a.x_rows}, xstride[1] = {K};
+    const cuuint64_t xsize[2] = {K, (cuuint64_t)(a.packed ? a.rows : a.x_rows)}, xstride[1] = {K};
     const cuuint64_t size[4] = {K, N, parts, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * parts};
     const cuuint32_t box[4] = {128, moedc::kMrCols / 2, 1, 1};
     if (!tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box)) return MOEDC_ERR_CUDA;

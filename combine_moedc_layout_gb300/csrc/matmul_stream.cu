@@ -303,7 +303,7 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
         // (one lane waits and issues, but where each lane gathers four of the rows)
         MvRing ring;
         int issued = 0;
-        const bool gather = a.src != nullptr, first = gather ? lane == 0 : tc_elect();
+        const bool gather = a.src && !a.packed, first = gather ? lane == 0 : tc_elect();
         bool stop = !gather && !first;
         for (int unit = first_unit; unit < units; unit += unit_step) {
             const MsUnit u = ms_unit(a, s_pre, s_beg, s_end, tiles, unit);
@@ -395,8 +395,9 @@ matmul_stream_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_c
 #pragma unroll
             for (int q = 0; q < kMsTokens / kWarp; ++q) {
                 const int r = u.r0 + min(q * kWarp + lane, u.m - 1);
-                xs[q] = a.xs + (a.offsets || !a.counts || a.src ? max(mm_x_row(a, r), 0) * a.xs_r
-                                                                : u.e * a.xs_e + (r - u.e * a.slots) * a.xs_r);
+                xs[q] = a.xs + (a.packed                                ? r * a.xs_r
+                                : a.offsets || !a.counts || a.src ? max(mm_x_row(a, r), 0) * a.xs_r
+                                                                  : u.e * a.xs_e + (r - u.e * a.slots) * a.xs_r);
             }
             const int b0 = u.n0 / 128;
             const float* w0 = a.ws + ((int64_t)u.e * (a.gated ? 2 : 1) * blocks + b0) * groups;
@@ -467,13 +468,14 @@ int launch_mm_stream(const moedc::MmArgs& a, const void* x, const void* w, bool 
     CUtensorMap wmap;
     moedc::BoxMaps xmaps{};
     const cuuint64_t K = a.K, N = a.N, both = a.gated ? 2 : 1;
-    const cuuint64_t xsize[2] = {K, (cuuint64_t)a.x_rows}, xstride[1] = {K};
+    const cuuint64_t xsize[2] = {K, (cuuint64_t)(a.packed ? a.rows : a.x_rows)}, xstride[1] = {K};
     const cuuint64_t size[4] = {K, N, both, (cuuint64_t)a.E}, stride[3] = {K, K * N, K * N * both};
     const cuuint32_t box[4] = {128, moedc::kMsRows, 1, 1};
     if (!tensor_map(&wmap, kType, kSwizzle, w, 4, size, stride, box)) return MOEDC_ERR_CUDA;
     // gathered rows: one map, a row high; else as many as the rows can need
-    for (int i = 0; i < 3 && (i == 0 || (!a.src && a.rows > 8 << i)); ++i) {
-        const cuuint32_t xbox[2] = {128, a.src ? 1u : 16u << i};
+    const bool gather = a.src && !a.packed;
+    for (int i = 0; i < 3 && (i == 0 || (!gather && a.rows > 8 << i)); ++i) {
+        const cuuint32_t xbox[2] = {128, gather ? 1u : 16u << i};
         if (!tensor_map(xmaps.by + i, kType, kSwizzle, x, 2, xsize, xstride, xbox)) return MOEDC_ERR_CUDA;
     }
     auto* k = moedc::matmul_stream_kernel;

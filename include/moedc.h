@@ -545,9 +545,10 @@ MOEDC_EXPORT int moedc_quant_e4m3(const void* x, int64_t ldx, int dtype, int E, 
  * same time need their own.
  * Kd % 128 == 0; x, w and e4m3 out 16-byte aligned, out otherwise 2-byte.
  * Data errors (dev_status): MOEDC_ERR_EXPERT_RANGE when src leads outside
- * [0, x_rows) (the row counts as zeros), MOEDC_ERR_CAPACITY when an expert's rows
- * pass `rows` or its slots (those are skipped), MOEDC_ERR_TIMEOUT if a bounded wait
- * gave up (its outputs are then unspecified).
+ * [0, x_rows) (dot is 0 for that row, whatever the weights hold),
+ * MOEDC_ERR_CAPACITY when an expert's rows pass `rows` or its slots (those are
+ * skipped), MOEDC_ERR_TIMEOUT if a bounded wait gave up (its outputs are then
+ * unspecified).
  */
 MOEDC_EXPORT size_t moedc_matmul_e4m3_workspace_bytes(int Kd, int E, int rows);
 MOEDC_EXPORT int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const float* xs, int scale_layout,

@@ -49,3 +49,56 @@ def test_equal_bits_with_and_without_a_workspace(counts, N, Kd, swiglu, out):
         t = token[o:o + c]
         v, err = product(wide_x(x.view(torch.uint8)[t].view(E4M3), xs[t]), wide_w(w[e], ws[e], swiglu), swiglu)
         check((a[0][o:o + c], a[1][o:o + c]) if out == "e4m3" else a[o:o + c], v, err, out)
+
+
+@pytest.mark.parametrize("out", ["bf16", "e4m3"])
+@pytest.mark.parametrize("swiglu", [False, True])
+@pytest.mark.parametrize("form", ["packed", "slots"])
+def test_lost_rows_are_zeros_beside_weights_of_nan(form, swiglu, out):
+    """Rows that src leads outside have outputs of 0 whatever the weights hold, in the copied form and
+    in the other one."""
+    g = torch.Generator().manual_seed(5)
+    E, cap, N, Kd = 2, 60, 256, 512
+    w, ws = weights(g, E, N, Kd, swiglu)
+    w.view(torch.uint8)[:, 3, 7] = 0x7f
+    ws[:, 1, 2] = float("inf")
+    x, xs = rows_of(g, 50, Kd)
+    counts = [60, 47]
+    src = torch.randint(0, 50, (E * cap,), generator=g).to(torch.int32)
+    lost = [0, 17, 59, 60, 101, 106]
+    src[lost] = torch.tensor([50, -1, 2 ** 31 - 1, 51, -(2 ** 31), 1000], dtype=torch.int32)
+    maps = dict(counts=torch.tensor(counts, dtype=torch.int32).cuda(), src=src.cuda())
+    if form == "packed":
+        maps["offsets"] = torch.tensor([0, cap, cap + 47], dtype=torch.int32).cuda()
+    else:
+        maps["src"] = maps["src"].view(E, cap)
+    assert moedc.moedc_matmul_e4m3_workspace_bytes(Kd, E, E * cap) > 0
+    status = _status()
+    a, b = _both(x, xs, w, ws, swiglu=swiglu, out_dtype=OUT[out], status=status, **maps)
+    assert int(status) == moedc.ERR_EXPERT_RANGE
+    mine = torch.zeros(E * cap, dtype=torch.bool)
+    mine[:60], mine[60:107] = True, True
+    for got in (a, b):
+        parts = [t.reshape(E * cap, -1) for t in (got if out == "e4m3" else (got,))]
+        assert (parts[0][lost].float() == 0).all()
+        if out == "e4m3":
+            assert (parts[1][lost] == torch.tensor(1e-4) / torch.tensor(448.0)).all()
+    for p, q in zip(*[[t.reshape(E * cap, -1)[mine] for t in _bits(v)] for v in (a, b)]):
+        assert torch.equal(p, q)
+    first = a[0] if out == "e4m3" else a
+    assert torch.isnan(first.reshape(E * cap, -1)[1, 3].float())      # the others have the weights' NaN
+
+
+def test_scales_of_minus_zero_are_zeros():
+    """No scale of the caller's is taken for a lost row's."""
+    g = torch.Generator().manual_seed(6)
+    w, ws = weights(g, 1, 256, 512, False)
+    x, xs = rows_of(g, 20, 512)
+    src = torch.arange(100, dtype=torch.int32).cuda() % 20
+    for cols in (slice(3, 4), slice(0, 4)):
+        s = xs.clone()
+        s[::3, cols] = 0.0
+        want = moedc.matmul_e4m3(x, s, w, ws, src=src)
+        s[::3, cols] = -0.0
+        assert all(torch.equal(y, want) for y in _both(x, s, w, ws, src=src))
+        assert want[1].any() and want[0].any() == (cols.start == 3)
