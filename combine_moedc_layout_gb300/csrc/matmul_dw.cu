@@ -7,7 +7,11 @@
 // byte is fetched once for a tile, and each SM's share is 32 KB for 512 clocks of products
 // (a stage: 64 tokens).  The contracted axis is the rows of both operands as they lie in
 // memory.  An expert's tokens end anywhere: the rows behind them, which are another
-// expert's, are cleared in shared memory as far as the products reach.
+// expert's, are cleared in shared memory as far as the products reach, by copies of boxes that
+// lie behind the tensor's end and so are zeros.  They count at the barrier of the first block's
+// thread that issues the products.  Stores by threads of the second block would need a release of
+// the cluster's scope: 64 experts of 517 tokens x 2048 x 2048 240 us, 208 so, 200 with stores in
+// no order that the memory model knows.
 //
 // A sum in tensor memory loses up to an ulp, always towards zero, with each product of 16
 // tokens: some 4e-8 of it a step for values of random signs, 1e-7 for those of one sign, 5e-5
@@ -20,8 +24,8 @@
 // 60 of 64 x 1024 x 1024: 35 us, the stores (4.4 TB/s); binary32, 64 of 512 x 7168 x 2048: 828 us.
 //
 // Warps: 0-7 epilogue (0-3 the first half of the columns, 4-7 the others), 8 TMA, 9 MMA (of
-// the pair's first block, for both), 10 clears and tells the first block that a stage has
-// arrived.  Tensor memory: two sums of 256 columns.
+// the pair's first block, for both), 10 tells the first block that a stage has arrived, and
+// clears.  Tensor memory: two sums of 256 columns.
 #include "matmul_store.cuh"
 #include "tcgen05.cuh"
 #include "tensor_map.cuh"
@@ -63,6 +67,9 @@ __device__ __forceinline__ DwUnit dw_unit(const MmArgs& a, const int32_t* s_beg,
     return u;
 }
 
+// Rows behind the expert's last one that the products of stage s reach: up to the end of their 16.
+__device__ __forceinline__ int dw_clears(const DwUnit& u, int s) { return s == u.ksteps - 1 ? (16 - u.m % 16) % 16 : 0; }
+
 // Whether a 16-bit sum has several pieces.  By a whole warp.
 __device__ __forceinline__ bool dw_pieces(const MmArgs& a, const int32_t* s_beg, const int32_t* s_end)
 {
@@ -75,7 +82,7 @@ __device__ __forceinline__ bool dw_pieces(const MmArgs& a, const int32_t* s_beg,
 template <bool kF32>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kMmThreads, 1)
 matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUtensorMap lmap,
-                 const __grid_constant__ CUtensorMap rmap)
+                 const __grid_constant__ CUtensorMap rmap, const __grid_constant__ BoxMaps zeros)
 {
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ int64_t s_scan[kMmThreads / kWarp];
@@ -298,23 +305,27 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
             const DwUnit u = dw_unit(a, s_beg, s_end, tiles, mtiles, unit);
             for (int s = 0; s < u.ksteps; ++s) {
                 mbar_wait_warp(full + ring.slot, ring.phase, &s_abort);
-                // rows behind the expert's last one, up to the end of their 16: a row is 128
-                // bytes of each of the four boxes, in whatever order
-                const int have = u.m - s * kMmElems, to = min((have + 15) / 16 * 16, kMmElems);
-                const bool cleared = have < to;
-                if (cleared) {
-                    for (int i = lane; i < (to - have) * 32; i += kWarp) {
-                        const int box = i & 3, chunk = (i >> 2) & 7, row = have + (i >> 5);
-                        *reinterpret_cast<uint4*>(smem + ring.slot * kMmStage + box * (kMmOperand / 2) + row * kMmBytes +
-                                                  chunk * 16) = make_uint4(0, 0, 0, 0);
+                const int n = dw_clears(u, s);
+                if (n > 0) {
+                    // two boxes of 1, 2, 4 or 8 rows, which may overlap, in each of the four boxes of data
+                    const int log = 31 - __clz(n), rows = 1 << log, have = u.m - s * kMmElems;
+                    if (lane < 8) {
+                        const int row = lane & 1 ? have : have + n - rows;
+                        tma_2d_pair(smem + ring.slot * kMmStage + lane / 2 * (kMmOperand / 2) + row * kMmBytes, zeros.by + log, 0,
+                                    a.rows, cluster_addr(ready + ring.slot, 0));
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                     __syncwarp();
+                    // (those of both blocks)
+                    if (lane == 0 && rank == 0) mbar_arrive_expect(ready + ring.slot, 2 * 8 * rows * kMmBytes);
                 }
-                if (lane == 0) mbar_arrive_pair(ready + ring.slot, 0);
+                if (lane == 0 && (rank == 1 || n == 0)) mbar_arrive_pair(ready + ring.slot, 0);
                 ring.next(kMmStages);
             }
         }
+        // zeros on their way that nobody waits for any more have a millisecond
+        if (s_abort)
+            for (const unsigned long long t0 = globaltimer(); globaltimer() - t0 < 1000000ull;) {}
+        __syncwarp();
     }
     tc_fence_before();
     __syncwarp();
@@ -330,7 +341,8 @@ namespace moedc_host {
 
 namespace {
 
-template <bool kF32> int launch_dw(const moedc::MmArgs& a, const CUtensorMap& l, const CUtensorMap& r, cudaStream_t stream)
+template <bool kF32>
+int launch_dw(const moedc::MmArgs& a, const CUtensorMap& l, const CUtensorMap& r, const moedc::BoxMaps& zeros, cudaStream_t stream)
 {
     auto* k = moedc::matmul_dw_kernel<kF32>;
     constexpr size_t kFixed = moedc::kMmStages * moedc::kMmStage + moedc::kMmBuf;
@@ -340,7 +352,7 @@ template <bool kF32> int launch_dw(const moedc::MmArgs& a, const CUtensorMap& l,
     const int pairs = sm_count() / 2;
     clear_stale_error();
     launch(k, 2 * (int)(units < pairs ? units : pairs), moedc::kMmThreads, kFixed + (3 * (size_t)a.E + 1) * sizeof(int32_t), stream, a, l,
-           r);
+           r, zeros);
     return launch_status();
 }
 
@@ -349,9 +361,16 @@ template <bool kF32> int launch_dw(const moedc::MmArgs& a, const CUtensorMap& l,
 int launch_mm_dw(const moedc::MmArgs& a, const void* dout, int64_t ldd, const void* x, int64_t ldx, cudaStream_t stream)
 {
     CUtensorMap l, r;
+    moedc::BoxMaps zeros{};
     if (!map_rows16(&l, dout, a.M, a.rows, ldd, moedc::kMmElems) || !map_rows16(&r, x, a.N, a.rows, ldx, moedc::kMmElems))
         return MOEDC_ERR_CUDA;
-    return a.f32 ? launch_dw<true>(a, l, r, stream) : launch_dw<false>(a, l, r, stream);
+    for (int i = 0; i < 4; ++i) {
+        const cuuint64_t size[2] = {(cuuint64_t)a.M, (cuuint64_t)a.rows}, stride[1] = {(cuuint64_t)ldd * 2};
+        const cuuint32_t box[2] = {moedc::kMmBytes / 2, 1u << i};
+        if (!tensor_map(zeros.by + i, CU_TENSOR_MAP_DATA_TYPE_UINT16, CU_TENSOR_MAP_SWIZZLE_NONE, dout, 2, size, stride, box))
+            return MOEDC_ERR_CUDA;
+    }
+    return a.f32 ? launch_dw<true>(a, l, r, zeros, stream) : launch_dw<false>(a, l, r, zeros, stream);
 }
 
 }  // namespace moedc_host
