@@ -62,7 +62,7 @@ __device__ __forceinline__ DwUnit dw_unit(const MmArgs& a, const int32_t* s_beg,
     u.m0 = c * kMmTile;
     u.r0 = s_beg[u.e];
     u.m = s_end[u.e] - u.r0;
-    u.ksteps = (u.m + kMmElems - 1) / kMmElems;
+    u.ksteps = u.m / kMmElems + (u.m % kMmElems != 0);   // (sizes go up to INT_MAX)
     u.piece = a.f32 ? kMmPiece : kMmPiece16;
     return u;
 }
@@ -93,7 +93,7 @@ matmul_dw_kernel(const __grid_constant__ MmArgs a, const __grid_constant__ CUten
     const int lane = threadIdx.x % kWarp, warp = threadIdx.x / kWarp;
     const int rank = cluster_rank();
     const int pair = blockIdx.x / 2, pairs = gridDim.x / 2;
-    const int tiles = (a.N + kMmTile - 1) / kMmTile, mtiles = (a.M + kMmTile - 1) / kMmTile;
+    const int tiles = (a.N - 1) / kMmTile + 1, mtiles = (a.M - 1) / kMmTile + 1;
     int32_t* s_pre = reinterpret_cast<int32_t*>(smem + kMmStages * kMmStage + kMmBuf);
     int32_t *s_beg = s_pre + a.E + 1, *s_end = s_beg + a.E;
 

@@ -26,8 +26,9 @@ __global__ void __launch_bounds__(kMmCopyRows* kWarp) matmul_gather_kernel(const
             const int mid = (lo + hi + 1) / 2;
             if (s_pre[mid] <= unit) lo = mid; else hi = mid - 1;
         }
-        const int r = s_beg[lo] + (unit - s_pre[lo]) * kMmCopyRows + threadIdx.x / kWarp;
-        if (r >= s_end[lo]) continue;
+        const int in = (unit - s_pre[lo]) * kMmCopyRows + threadIdx.x / kWarp;
+        if (in >= s_end[lo] - s_beg[lo]) continue;
+        const int r = s_beg[lo] + in;
         const int t = mm_x_row(a, r);
         bad |= t < 0;
         const uint4* from = reinterpret_cast<const uint4*>(x + (int64_t)max(t, 0) * a.K);

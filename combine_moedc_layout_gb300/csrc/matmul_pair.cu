@@ -66,7 +66,7 @@ __device__ __forceinline__ MpUnit mp_unit(const MmArgs& a, const int32_t* s_pre,
     // an expert's chunks are equal ones: chunks - 1 of them are fewer rows than it has, as a
     // chunk is at most 256 and all of its rows more than chunks - 1 times that
     const int rows = s_end[lo] - s_beg[lo];
-    const int size = ((rows + chunks - 1) / chunks + 31) / 32 * 32;
+    const int size = ((rows - 1) / chunks + 32) / 32 * 32;
     MpUnit u;
     u.e = lo;
     u.n0 = t * (a.gated ? kMpHalf : kMpTile);
@@ -102,7 +102,7 @@ matmul_pair_kernel(const __grid_constant__ MmArgs a, int parts, const __grid_con
     const int rank = cluster_rank() & 1, leader_rank = cluster_rank() & ~1, part = cluster_rank() / 2;
     const int first_unit = blockIdx.x / (2 * parts), unit_step = gridDim.x / (2 * parts);
     const int tile_n = a.gated ? kMpHalf : kMpTile;
-    const int tiles = (a.N + tile_n - 1) / tile_n, ksteps = (a.K + kMpElems - 1) / kMpElems;
+    const int tiles = (a.N - 1) / tile_n + 1, ksteps = (a.K - 1) / kMpElems + 1;   // (sizes go up to INT_MAX)
     const int s_first = ksteps * part / parts, s_last = ksteps * (part + 1) / parts - 1;
     int32_t* s_pre = reinterpret_cast<int32_t*>(smem + kMpStages * kMpStage);
     int32_t *s_beg = s_pre + a.E + 1, *s_end = s_beg + a.E;
@@ -401,7 +401,7 @@ int launch_mm_pair(const moedc::MmArgs& a, const CUtensorMap& w, const void* x, 
     // and 18.3; 512 channels 9.5 and 10.6.
     const int64_t most = a.rows < moedc::kMpTile ? a.rows : moedc::kMpTile;
     const int64_t sums = (most + 31) / 32 * 32 * moedc::kMpHalf * sizeof(float);
-    const int ksteps = (a.K + moedc::kMpElems - 1) / moedc::kMpElems;
+    const int ksteps = (a.K - 1) / moedc::kMpElems + 1;
     auto fits = [&](int p, int64_t tiles) { return units <= tiles && ksteps >= 16 * p && (p - 1) * sums <= (int64_t)kFixed; };
     const int parts = fits(4, MOEDC_PAIR_PARTS_4) ? 4 : fits(2, MOEDC_PAIR_PARTS_2) ? 2 : 1;
     // the longest part (of parts that differ by a stage)

@@ -43,7 +43,7 @@ __device__ __forceinline__ void mm_store32(uint8_t* buf, uint16_t* out, int64_t 
             q[c] = make_uint4(mm_pack16(f[0], f[1], f16), mm_pack16(f[2], f[3], f16), mm_pack16(f[4], f[5], f16),
                               mm_pack16(f[6], f[7], f16));
         }
-        mm_store_rows(buf, q, reinterpret_cast<uint8_t*>(out + n), 2 * ld, rows, 2 * (N - n));
+        mm_store_rows(buf, q, reinterpret_cast<uint8_t*>(out + n), 2 * ld, rows, 2 * min(N - n, 32));
     } else if ((int)(threadIdx.x % kWarp) < rows) {
         uint16_t* row = out + threadIdx.x % kWarp * ld + n;
 #pragma unroll
@@ -61,7 +61,7 @@ __device__ __forceinline__ void mm_store32(uint8_t* buf, float* out, int64_t ld,
             const float* f = v + h + 4 * c;
             q[c] = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
         }
-        mm_store_rows(buf, q, reinterpret_cast<uint8_t*>(out + n + h), 4 * ld, rows, 4 * (N - n - h));
+        mm_store_rows(buf, q, reinterpret_cast<uint8_t*>(out + n + h), 4 * ld, rows, 4 * min(N - n - h, 16));
     }
 }
 
