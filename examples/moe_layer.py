@@ -15,6 +15,7 @@
 """
 from __future__ import annotations
 
+import functools
 import os
 import sys
 import time
@@ -96,6 +97,33 @@ def slots_step(x: torch.Tensor, topk_idx: torch.Tensor, topk_weights: torch.Tens
 # ----------------------------------------------------------------- training
 
 
+class _Refused(torch.autograd.Function):
+    """A gradient that has none itself with respect to what it was computed from."""
+
+    @staticmethod
+    def forward(ctx, grad, *of):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError("the layer's operators are differentiable once")
+
+
+def _once(backward):
+    """A backward that refuses second derivatives, of the gradients that it takes and of the tensors
+    that its forward saved (torch's once_differentiable looks at the former alone: under a loss that
+    is linear in the outputs it leaves the others out)."""
+    @functools.wraps(backward)
+    def run(ctx, *grads):
+        with torch.no_grad():
+            out = backward(ctx, *grads)
+        if not torch.is_grad_enabled():
+            return out
+        return tuple(g if g is None else _Refused.apply(g, *grads, *ctx.saved_tensors)
+                     for g in (out if isinstance(out, tuple) else (out,)))
+    return run
+
+
 class Gate(torch.autograd.Function):
     """(topk_idx, topk_weights) of logits."""
 
@@ -107,6 +135,7 @@ class Gate(torch.autograd.Function):
         return idx, w
 
     @staticmethod
+    @_once
     def backward(ctx, _, dw):
         logits, idx = ctx.saved_tensors
         return moedc.gate_grad(logits, idx, dw.contiguous(), flags=FLAGS), None
@@ -123,6 +152,7 @@ class Sort(torch.autograd.Function):
         return m.rows, m.row, m.src, m.offsets, m.counts
 
     @staticmethod
+    @_once
     def backward(ctx, drows, *_):
         return moedc.sort_grad(drows.contiguous(), ctx.saved_tensors[0]), None, None, None
 
@@ -136,6 +166,7 @@ class Unsort(torch.autograd.Function):
         return moedc.unsort(rows, row, w)
 
     @staticmethod
+    @_once
     def backward(ctx, dy):
         rows, w, row, src = ctx.saved_tensors
         drows, dw = moedc.unsort_grad(dy.contiguous(), rows, row, src, w)
@@ -154,6 +185,7 @@ class Block(torch.autograd.Function):
         return h
 
     @staticmethod
+    @_once
     def backward(ctx, dh):
         rows, gate_up, products, offsets, counts = ctx.saved_tensors
         d = moedc.swiglu_grad(dh.contiguous(), products)
@@ -171,6 +203,7 @@ class Product(torch.autograd.Function):
         return moedc.matmul(rows, w, offsets=offsets, counts=counts, status=status)
 
     @staticmethod
+    @_once
     def backward(ctx, dout):
         rows, w, offsets, counts = ctx.saved_tensors
         return *moedc.matmul_grad(dout.contiguous(), rows, w, offsets=offsets, counts=counts,
