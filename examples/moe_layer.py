@@ -169,8 +169,15 @@ class Unsort(torch.autograd.Function):
     @_once
     def backward(ctx, dy):
         rows, w, row, src = ctx.saved_tensors
-        drows, dw = moedc.unsort_grad(dy.contiguous(), rows, row, src, w)
+        drows, dw = moedc.unsort_grad(dy.contiguous(), rows if ctx.needs_input_grad[1] else None, row, src, w)
         return drows, dw, None, None
+
+
+def _grad(ctx, dout, rows, w, offsets, counts):
+    """(drows, dw) of the experts' products, those that are asked for (a frozen expert's are half of the work)."""
+    want_rows, want_w = ctx.needs_input_grad[:2]
+    return moedc.matmul_grad(dout, rows if want_w else None, w if want_rows else None, offsets=offsets,
+                             counts=counts, status=ctx.status)
 
 
 class Block(torch.autograd.Function):
@@ -189,8 +196,7 @@ class Block(torch.autograd.Function):
     def backward(ctx, dh):
         rows, gate_up, products, offsets, counts = ctx.saved_tensors
         d = moedc.swiglu_grad(dh.contiguous(), products)
-        return *moedc.matmul_grad(d, rows, gate_up, offsets=offsets, counts=counts,
-                                  status=ctx.status), None, None, None
+        return *_grad(ctx, d, rows, gate_up, offsets, counts), None, None, None
 
 
 class Product(torch.autograd.Function):
@@ -205,9 +211,7 @@ class Product(torch.autograd.Function):
     @staticmethod
     @_once
     def backward(ctx, dout):
-        rows, w, offsets, counts = ctx.saved_tensors
-        return *moedc.matmul_grad(dout.contiguous(), rows, w, offsets=offsets, counts=counts,
-                                  status=ctx.status), None, None, None
+        return *_grad(ctx, dout.contiguous(), *ctx.saved_tensors), None, None, None
 
 
 class MoeLayer(torch.nn.Module):

@@ -15,6 +15,37 @@ def _layer(ex, dtype=torch.bfloat16, T=70, H=136, I=72, E=5, K=2, align=16):
     return layer, x, torch.randn(T, H, device="cuda", dtype=dtype)
 
 
+@pytest.mark.parametrize("frozen", [("gate_up", "down"), ("gate_up",), ("down", "router"), ("router",)])
+@pytest.mark.parametrize("with_x", [False, True])
+def test_frozen_parameters(frozen, with_x, monkeypatch):
+    """The gradients that are asked for are those of the whole layer; the others are not computed."""
+    ex = _example()
+    layer, x, c = _layer(ex)
+    x.requires_grad_(with_x)
+    (layer(x) * c).sum().backward()
+    whole = {n: p.grad for n, p in layer.named_parameters()} | {"x": x.grad}
+    layer.zero_grad(set_to_none=True)
+    x.grad = None
+    asked = []
+    grad = ex.moedc.matmul_grad
+
+    def counted(dout, rows, w, **kw):
+        asked.append((w is not None, rows is not None))
+        return grad(dout, rows, w, **kw)
+
+    monkeypatch.setattr(ex.moedc, "matmul_grad", counted)
+    for n in frozen:
+        getattr(layer, n).requires_grad_(False)
+    (layer(x) * c).sum().backward()
+    for n, p in layer.named_parameters():
+        assert p.grad is None if n in frozen else torch.equal(p.grad, whole[n])
+    assert x.grad is None if not with_x else torch.equal(x.grad, whole["x"])
+    # the down product's, then the block's: (dx, dw)
+    block = with_x, "gate_up" not in frozen
+    down = any(block), "down" not in frozen
+    assert asked == [pair for pair in (down, block) if any(pair)]
+
+
 @pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
 def test_second_derivatives_are_refused(dtype):
     ex = _example()
