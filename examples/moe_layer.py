@@ -173,11 +173,18 @@ class Unsort(torch.autograd.Function):
         return drows, dw, None, None
 
 
+def _rows(like, n):
+    """Rows for an output of the experts' products, which leave the padding rows as they are: zeros
+    there, as hooks, norms and anomaly detection see them."""
+    return torch.zeros((like.shape[0], n), dtype=like.dtype, device=like.device)
+
+
 def _grad(ctx, dout, rows, w, offsets, counts):
     """(drows, dw) of the experts' products, those that are asked for (a frozen expert's are half of the work)."""
     want_rows, want_w = ctx.needs_input_grad[:2]
+    out = _rows(dout, w.shape[2]) if want_rows else None, torch.empty_like(w) if want_w else None
     return moedc.matmul_grad(dout, rows if want_w else None, w if want_rows else None, offsets=offsets,
-                             counts=counts, status=ctx.status)
+                             counts=counts, status=ctx.status, out=out)
 
 
 class Block(torch.autograd.Function):
@@ -185,8 +192,9 @@ class Block(torch.autograd.Function):
 
     @staticmethod
     def forward(ctx, rows, gate_up, offsets, counts, status):
+        out = _rows(rows, gate_up.shape[1] // 2), rows.new_empty((rows.shape[0], gate_up.shape[1]))
         h, products = moedc.matmul(rows, gate_up, offsets=offsets, counts=counts, swiglu=True,
-                                   keep=True, status=status)
+                                   keep=True, status=status, out=out)
         ctx.save_for_backward(rows, gate_up, products, offsets, counts)
         ctx.status = status
         return h
@@ -206,7 +214,8 @@ class Product(torch.autograd.Function):
     def forward(ctx, rows, w, offsets, counts, status):
         ctx.save_for_backward(rows, w, offsets, counts)
         ctx.status = status
-        return moedc.matmul(rows, w, offsets=offsets, counts=counts, status=status)
+        return moedc.matmul(rows, w, offsets=offsets, counts=counts, status=status,
+                            out=_rows(rows, w.shape[1]))
 
     @staticmethod
     @_once

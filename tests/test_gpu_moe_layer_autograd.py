@@ -15,6 +15,44 @@ def _layer(ex, dtype=torch.bfloat16, T=70, H=136, I=72, E=5, K=2, align=16):
     return layer, x, torch.randn(T, H, device="cuda", dtype=dtype)
 
 
+def _spoil(shapes, dtype):
+    """NaN in the memory that the next tensors of these shapes get."""
+    held = [torch.full(s, float("nan"), dtype=dtype, device="cuda") for s in shapes for _ in range(4)]
+    del held
+
+
+def test_padding_rows_hold_no_old_memory():
+    ex = _example()
+    layer, x, c = _layer(ex)
+    idx, _ = ex.Gate.apply((x @ layer.router.T).float(), layer.K)
+    rows, _, src, offsets, counts = ex.Sort.apply(x.requires_grad_(True), idx, layer.E, layer.align)
+    R, (H, I) = rows.shape[0], layer.down.shape[1:]
+    pad = src < 0
+    assert pad.any() and (rows[pad] == 0).all()
+    _spoil([(R, I), (R, 2 * I), (R, H)], x.dtype)
+    h = ex.Block.apply(rows, layer.gate_up, offsets, counts, layer.status)
+    out = ex.Product.apply(h, layer.down, offsets, counts, layer.status)
+    assert (h[pad] == 0).all() and (out[pad] == 0).all()
+    seen = []
+    h.register_hook(lambda g: seen.append(g.clone()))
+    rows.register_hook(lambda g: seen.append(g.clone()))
+    dout = torch.randn_like(out)
+    _spoil([(R, I), (R, 2 * I), (R, H)], x.dtype)
+    out.backward(dout)
+    assert len(seen) == 2 and all((g[pad] == 0).all() and torch.isfinite(g).all() for g in seen)
+
+
+def test_anomaly_detection_finds_nothing():
+    ex = _example()
+    layer, x, c = _layer(ex)
+    R, (H, I) = 70 * 2 + 5 * 15, layer.down.shape[1:]
+    with torch.autograd.detect_anomaly():
+        for _ in range(3):
+            _spoil([(R, I), (R, 2 * I), (R, H)], x.dtype)
+            (layer(x) * c).sum().backward()
+    assert all(torch.isfinite(p.grad).all() for p in layer.parameters())
+
+
 @pytest.mark.parametrize("frozen", [("gate_up", "down"), ("gate_up",), ("down", "router"), ("router",)])
 @pytest.mark.parametrize("with_x", [False, True])
 def test_frozen_parameters(frozen, with_x, monkeypatch):
