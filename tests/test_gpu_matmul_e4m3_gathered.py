@@ -102,3 +102,32 @@ def test_scales_of_minus_zero_are_zeros():
         s[::3, cols] = -0.0
         assert all(torch.equal(y, want) for y in _both(x, s, w, ws, src=src))
         assert want[1].any() and want[0].any() == (cols.start == 3)
+
+
+# copied for the form for many rows, and for clusters of the other one
+@pytest.mark.parametrize("cap,Kd", [(60, 512), (40, 4096), (24, 1024)])
+@pytest.mark.parametrize("layout", [0, moedc.SCALES_PER_TOKEN])
+def test_lost_rows_in_every_form_and_scale_layout(cap, Kd, layout):
+    g = torch.Generator().manual_seed(cap)
+    E, N = 2, 256
+    w, ws = weights(g, E, N, Kd, False)
+    w.view(torch.uint8)[:, 3, 7] = 0x7f
+    x, xs = rows_of(g, 31, Kd)
+    if layout:
+        xs = xs[:, 0].contiguous()
+    src = torch.randint(0, 31, (E, cap), generator=g).to(torch.int32)
+    src[0, 1], src[1, cap - 1] = 31, -7
+    status = _status()
+    maps = dict(counts=torch.full((E,), cap, dtype=torch.int32).cuda(), src=src.cuda(), scale_layout=layout, status=status)
+    a, b = _both(x, xs, w, ws, **maps)
+    assert int(status) == moedc.ERR_EXPERT_RANGE
+    assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    lost = torch.zeros(E, cap, dtype=torch.bool)
+    lost[0, 1] = lost[1, cap - 1] = True
+    assert (a[lost] == 0).all() and torch.isnan(a[~lost][:, 3]).all() and not torch.isnan(a[~lost][:, 4:]).any()
+    t = src.long().clamp(0, 30).cuda()
+    for e in range(E):
+        s = xs[t[e]][:, None].expand(cap, Kd // 128) if layout else xs[t[e]]
+        keep = ~lost[e]
+        v, err = product(wide_x(x.view(torch.uint8)[t[e]].view(E4M3), s)[keep], wide_w(w[e], ws[e], False)[4:], False)
+        check(a[e][keep][:, 4:], v, err, "bf16")
