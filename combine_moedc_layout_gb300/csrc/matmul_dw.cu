@@ -20,8 +20,9 @@
 // adds up, rounding to nearest.
 // (A piece is also what the epilogue's bounded wait waits for.)
 //
-// 32 experts of 512 tokens x 4096 x 4096: 350 us, 1570 TFLOP/s, stores and products together;
-// 60 of 64 x 1024 x 1024: 35 us, the stores (4.4 TB/s); binary32, 64 of 512 x 7168 x 2048: 828 us.
+// 32 experts of 512 tokens x 4096 x 4096: 357 us, 1540 TFLOP/s, stores and products together;
+// 60 of 64 x 1024 x 1024: 34 us, the stores (4.4 TB/s); binary32, 64 of 512 x 7168 x 2048: 850 us
+// (815 to 890).
 //
 // Warps: 0-7 epilogue (0-3 the first half of the columns, 4-7 the others), 8 TMA, 9 MMA (of
 // the pair's first block, for both), 10 tells the first block that a stage has arrived, and

@@ -62,9 +62,12 @@ namespace moedc_host {
 //   rows                              8         16        24        32
 //   64 experts of 2 x 2048 x 7168  270 / 300 273 / 302 275 / 304 280 / 305
 //   128 of 2048 x 2048                        87 / 90   90 / 91       / 92
-//   8 of 7168 x 2048                                               31 / 28
-// Tiles so few that clusters share them are the exception: one expert of 7168 x 7168, 16 rows
-// 14.5 / 28, 32 rows 17.5 / 28.
+//   8 of 7168 x 2048                          26 / 28             31 / 29
+// Tiles so few that clusters share them are the exception, up to twice as many rows: one expert of
+// 7168 x 7168, 16 rows 15.5 / 28, 32 rows 17.6 / 28, 48 rows 19 / 28.  (49 to 64 rows are still
+// one chunk of tokens and would take 20 to 23; four experts of 2 x 2048 x 7168, 64 tiles, are
+// beyond: 32 / 33 at 16 rows, 36 / 33 at 32.)
+// `rows` is what the buffer holds, padding and unused slots included: the counts are on the device.
 static bool weights_on_rows(int E, int N, bool gated, int rows)
 {
     const int64_t active = E < rows ? E : rows;
@@ -73,9 +76,11 @@ static bool weights_on_rows(int E, int N, bool gated, int rows)
 }
 
 // Gathering the rows of a block's stage by TMA takes some 80 clocks for four of them, again
-// for every tile of columns: with 128 rows an expert 4220 us against 2000, copy included (256
-// experts of 2 x 2048 x 7168, in a form of pairs of SMs).  So where the tokens would lie on the
-// tile's rows they are brought into packed order first.
+// for every tile of columns.  By rows an expert, us of rows gathered so / of rows brought into
+// packed order first, with the tokens on the tile's rows:
+//   rows                              8         16        24        32        48        128
+//   64 experts of 2 x 2048 x 7168  284 / 307 297 / 310 321 / 312 352 / 314 407 / 317 908 / 333
+//   128 of 2 x 1024 x 4096         170 / 189 179 / 191 193 / 193 213 / 196 242 / 199
 static bool gathers_first(int E, int rows)
 {
     const int64_t active = E < rows ? E : rows;

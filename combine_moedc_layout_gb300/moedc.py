@@ -536,17 +536,22 @@ def _lm_dtype(t: torch.Tensor, name: str) -> int:
     return d
 
 
-def _need_ints(*sizes: int) -> None:
+_INT_MAX = 2 ** 31 - 1
+
+
+def _need_ints(t: torch.Tensor, *sizes: int) -> None:
     """ctypes would pass a larger size on without its upper bits."""
-    if max(sizes) > 2 ** 31 - 1:
-        raise ValueError(f"sizes must be below 2^31, not {max(sizes)}")
+    if t.numel() > _INT_MAX or sizes and max(sizes) > _INT_MAX:
+        most = max(*t.shape, *sizes)
+        if most > _INT_MAX:
+            raise ValueError(f"sizes must be below 2^31, not {most}")
 
 
 def _need_rows(t: torch.Tensor, name: str) -> int:
     """A 2-D CUDA tensor whose rows are contiguous; returns its row stride."""
     if t.dim() != 2 or not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA matrix with contiguous rows")
-    _need_ints(*t.shape)
+    _need_ints(t)
     if t.is_contiguous():
         return t.shape[1]
     if t.shape[1] > 1 and t.stride(1) != 1:
@@ -864,7 +869,7 @@ def quant_e4m3(x: torch.Tensor, block_rows: int = 1, out=None):
     earlier call's result to write into."""
     if x.dim() == 3:
         _need(x, x.dtype, "x")
-        _need_ints(*x.shape)
+        _need_ints(x)
         ld = x.shape[2]
         E, R, Kd = x.shape
     else:
@@ -942,7 +947,7 @@ def matmul_e4m3(x: torch.Tensor, xs: torch.Tensor, w: torch.Tensor, ws: torch.Te
         raise ValueError(f"src must be {len(lead)}-dimensional")
     rows = math.prod(lead)
     x_rows = math.prod(x.shape[:-1])
-    _need_ints(rows, x_rows, *w.shape)
+    _need_ints(w, rows, x_rows)
     if scale_layout == SCALES_COL_MAJOR:
         if not slots or src is not None:
             raise ValueError("SCALES_COL_MAJOR is the receive buffer's: counts alone, no src")
@@ -1006,7 +1011,7 @@ def matmul(x: torch.Tensor, w: torch.Tensor, offsets: torch.Tensor | None = None
     R = x.shape[0]
     if x.shape[1] != Kd:
         raise ValueError(f"x must have {Kd} channels, not {x.shape[1]}")
-    _need_ints(*w.shape)
+    _need_ints(w)
     if swiglu and wn % 2:
         raise ValueError("swiglu needs an even number of weight rows")
     if keep and not swiglu:
