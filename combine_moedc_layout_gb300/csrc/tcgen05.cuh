@@ -82,10 +82,9 @@ __device__ __forceinline__ void cluster_sync()
     asm volatile("barrier.cluster.arrive.release.aligned;\n barrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
 // One arrival at the barrier of that name in block `rank` of the cluster.  What it announces
-// is copies, tensor-memory accesses, and stores to the arriving block's own shared memory
-// behind a proxy fence, all of which have their own completion or fence before it; with the
-// release of a cluster's scope spelled out an arrival waits on a memory barrier of some
-// 1.2 us.
+// is copies and tensor-memory accesses, which have their own completion or fence before it (and
+// no stores: the other block would not have to see them); with the release of a cluster's scope
+// spelled out an arrival waits on a memory barrier of some 1.2 us.
 __device__ __forceinline__ void mbar_arrive_pair(uint64_t* b, int rank)
 {
     asm volatile("{\n .reg .b32 at;\n mapa.shared::cluster.u32 at, %0, %1;\n"

@@ -529,7 +529,8 @@ MOEDC_EXPORT int moedc_quant_e4m3(const void* x, int64_t ldx, int dtype, int E, 
  *   neither, E = 1                   all rows
  * r' = r, with x_rows = rows; or src[r] / top_k with src, whose rows may be
  * gathered from any x (of moedc_sort, with its top_k; src_idx of
- * moedc_dispatch, with top_k 1).  x_rows = 0: nothing is written.
+ * moedc_dispatch, with top_k 1).  x_rows = 0: nothing is written and no data
+ * error raised, whatever src holds.
  *   x     e4m3 [x_rows, Kd], contiguous
  *   xs    scale_layout 0 [x_rows, Kd / 128]; MOEDC_SCALES_PER_TOKEN [x_rows];
  *         MOEDC_SCALES_COL_MAJOR [E, Kd / 128, rows / E] (counts alone, no src)
@@ -541,8 +542,8 @@ MOEDC_EXPORT int moedc_quant_e4m3(const void* x, int64_t ldx, int dtype, int E, 
  * workspace (16-byte aligned, no initialisation): with src and many rows to an
  * expert, where moedc_matmul_e4m3_workspace_bytes is not 0, the rows are first
  * copied into packed order there; without one (NULL, or smaller) they are gathered
- * as the products need them.  The results are the same.  Calls that can run at the
- * same time need their own.
+ * as the products need them, which takes longer.  The results are the same, bit for
+ * bit.  Calls that can run at the same time need their own.
  * Kd % 128 == 0; x, w and e4m3 out 16-byte aligned, out otherwise 2-byte.
  * Data errors (dev_status): MOEDC_ERR_EXPERT_RANGE when src leads outside
  * [0, x_rows) (dot is 0 for that row, whatever the weights hold),
@@ -580,10 +581,11 @@ MOEDC_EXPORT int moedc_matmul_e4m3(const void* x, int x_rows, int Kd, const floa
  *   dx[r][k]    = round( sum over n of dout[r][n] * w[e][n][k] )
  *   dw[e][n][k] = round( sum over e's rows r of dout[r][n] * x[r][k] ); 0 without rows
  * dx or dw may be NULL and is then not computed (w is read for dx alone, x for dw
- * alone).  dw_dtype is dtype or MOEDC_F32.  (Sums over more than 8192 elements, or
- * rows for dw, are sums of pieces of that many; 768 rows for a binary32 dw.)  Rows that belong to no expert are
+ * alone).  dw_dtype is dtype or MOEDC_F32.  Rows that belong to no expert are
  * neither read into any result nor written.  The order of every sum is fixed:
- * equal inputs give equal bits.
+ * equal inputs give equal bits.  Long sums are sums of pieces of 8192 elements (rows
+ * for dw; 768 for a binary32 dw), each rounded towards zero in its steps of 16
+ * (5e-5 of it over 8192 of one sign), to nearest where they are added up.
  * dtype MOEDC_BF16 or MOEDC_F16; Kd and N multiples of 8; leading dimensions
  * multiples of 8; matrices 16-byte aligned, all but x, dh and dout contiguous.
  * Data errors (dev_status): MOEDC_ERR_CAPACITY and MOEDC_ERR_TIMEOUT as for
