@@ -1075,6 +1075,7 @@ def matmul_grad(dout: torch.Tensor, x: torch.Tensor | None, w: torch.Tensor | No
     if w is not None:
         w = _experts(w)
         _need(w, dout.dtype, "w")
+        _need_ints(w)
         E, Kd = w.shape[0], w.shape[2]
         _need_shape(w, (E, N, Kd), "w")
     else:

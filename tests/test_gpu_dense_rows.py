@@ -99,4 +99,6 @@ def test_more_rows_than_numbers_are_refused():
     with pytest.raises(ValueError):
         moedc.matmul(wide[:1], wide)
     with pytest.raises(ValueError):
+        moedc.matmul_grad(w[:1], None, wide)
+    with pytest.raises(ValueError):
         moedc.quant_e4m3(wide[None], block_rows=128)
